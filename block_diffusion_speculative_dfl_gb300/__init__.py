@@ -15,7 +15,11 @@ from ._lib import (DflError, load, version, status_string, workspace_size, ptr, 
                    dfl_tv_acceptance, dfl_spec_accept, DFL_OP_TV_ACCEPTANCE, DFL_OP_SPEC_ACCEPT,
                    dfl_block_ffn, DFL_OP_BLOCK_FFN, dfl_draft_step_cached, DFL_OP_DRAFT_STEP_CACHED,
                    dfl_draft_step_host, DFL_OP_DRAFT_STEP_HOST, CtxCache, dfl_fc_fuse, DFL_OP_FC_FUSE,
-                   dfl_sampled_greedy_accept, DFL_OP_SAMPLED_GREEDY, dfl_philox4x32_10)
-from .step import DraftShape, DraftModel, CachedDraftModel
+                   dfl_sampled_greedy_accept, DFL_OP_SAMPLED_GREEDY, dfl_philox4x32_10,
+                   Kv4Pool, Pages, PagedCtx, dfl_kv4_page_bytes, dfl_kv4_append, dfl_kv4_read, dfl_kv4_attn,
+                   DFL_OP_KV4_ATTN, dfl_pages_reserve, DFL_OP_PAGES_RESERVE, dfl_pages_remap, DFL_OP_PAGES_REMAP,
+                   dfl_pages_compact, DFL_OP_PAGES_COMPACT, dfl_draft_step_paged, DFL_OP_DRAFT_STEP_PAGED)
+from .paged import PagedCache
+from .step import DraftShape, DraftModel, CachedDraftModel, PagedDraftModel
 
 __all__ = [n for n in dir() if not n.startswith("_")]

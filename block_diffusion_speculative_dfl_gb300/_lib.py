@@ -17,6 +17,8 @@ DFL_F32, DFL_BF16 = 0, 1
 DFL_OP_DUAL_KV_PROJ, DFL_OP_BLOCK_ATTN, DFL_OP_LM_HEAD, DFL_OP_SELF_SELECT, DFL_OP_DRAFT_STEP = 1, 2, 3, 4, 5
 DFL_OP_TV_ACCEPTANCE, DFL_OP_SPEC_ACCEPT, DFL_OP_BLOCK_FFN, DFL_OP_DRAFT_STEP_CACHED = 6, 7, 8, 9
 DFL_OP_DRAFT_STEP_HOST, DFL_OP_FC_FUSE, DFL_OP_SAMPLED_GREEDY = 10, 11, 12
+DFL_OP_KV4_ATTN, DFL_OP_PAGES_RESERVE, DFL_OP_PAGES_REMAP, DFL_OP_PAGES_COMPACT = 13, 14, 15, 16
+DFL_OP_DRAFT_STEP_PAGED = 17
 
 # Every function the header declares; tests check each is exported.
 EXPORTED = ("dfl_version", "dfl_status_string", "dfl_workspace_size", "dfl_rope_table",
@@ -25,7 +27,8 @@ EXPORTED = ("dfl_version", "dfl_status_string", "dfl_workspace_size", "dfl_rope_
             "dfl_set_wait_limit_ns", "dfl_selftest_bounded_wait", "dfl_profile_enable", "dfl_profile_report",
             "dfl_self_select_noalloc", "dfl_tv_acceptance", "dfl_spec_accept", "dfl_block_ffn",
             "dfl_draft_step_cached", "dfl_draft_step_host", "dfl_fc_fuse", "dfl_sampled_greedy_accept",
-            "dfl_philox4x32_10")
+            "dfl_philox4x32_10", "dfl_kv4_page_bytes", "dfl_kv4_append", "dfl_kv4_read", "dfl_kv4_attn",
+            "dfl_pages_reserve", "dfl_pages_remap", "dfl_pages_compact", "dfl_draft_step_paged")
 
 
 class DflError(RuntimeError):
@@ -40,7 +43,7 @@ class SampleParams(C.Structure):
 
 class Shape(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("N", "C", "B", "d", "Hq", "Hkv", "hd", "D", "L", "V", "K", "G", "row0",
-                                         "dtype", "F", "R", "fc")]
+                                         "dtype", "F", "R", "fc", "pages")]
 
 
 class LayerWeights(C.Structure):
@@ -63,6 +66,21 @@ class StepArgs(C.Structure):
 class CtxCache(C.Structure):
     _fields_ = [("K", C.c_void_p), ("V", C.c_void_p), ("layer_stride", C.c_int64), ("R", C.c_int32),
                 ("ctx_len", C.c_void_p), ("n_new", C.c_void_p), ("advance", C.c_int32)]
+
+
+class Kv4Pool(C.Structure):
+    _fields_ = ([("data", C.c_void_p), ("layer_stride", C.c_int64)] +
+                [(n, C.c_int32) for n in ("layers", "num_pages", "page", "Hkv", "hd", "k_exp", "v_exp")])
+
+
+class Pages(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("len", C.c_void_p), ("ref", C.c_void_p), ("N", C.c_int32),
+                ("max_pages", C.c_int32)]
+
+
+class PagedCtx(C.Structure):
+    _fields_ = [("pool", C.POINTER(Kv4Pool)), ("pages", Pages), ("R", C.c_int32), ("n_new", C.c_void_p),
+                ("start", C.c_void_p)]
 
 
 _P, _I32, _I64, _F, _D, _SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_size_t
@@ -96,6 +114,14 @@ _SIGS = {
     "dfl_sampled_greedy_accept": ([_P, _I32, _P, _P, _I32, _I32, _I32, _I32, C.c_uint64, _P, _P, _P, _SZ, _P],
                                   _I32),
     "dfl_philox4x32_10": ([_P, _I32, _P, _P], _I32),
+    "dfl_kv4_page_bytes": ([_I32, _I32, _I32], _SZ),
+    "dfl_kv4_append": ([C.POINTER(Kv4Pool), _I32, C.POINTER(Pages), _P, _P, _I32, _P, _P, _P], _I32),
+    "dfl_kv4_read": ([C.POINTER(Kv4Pool), _I32, C.POINTER(Pages), _P, _P, _I32, _P, _P, _P], _I32),
+    "dfl_kv4_attn": ([C.POINTER(Kv4Pool), _I32, C.POINTER(Pages), _P, _P, _P, _I32, _I32, _P, _P, _SZ, _P], _I32),
+    "dfl_pages_reserve": ([C.POINTER(Kv4Pool), C.POINTER(Pages), _P, _P, _P, _SZ, _P], _I32),
+    "dfl_pages_remap": ([C.POINTER(Kv4Pool), C.POINTER(Pages), _P, _P, _P, _SZ, _P], _I32),
+    "dfl_pages_compact": ([C.POINTER(Kv4Pool), C.POINTER(Pages), _P, _P, _P, _SZ, _P], _I32),
+    "dfl_draft_step_paged": ([C.POINTER(StepArgs), C.POINTER(PagedCtx), _P, _SZ, _P], _I32),
 }
 
 _lib = None
@@ -288,3 +314,48 @@ def dfl_sampled_greedy_accept(vlog, dt, drafts, sel, N, K, G, V, seed, accept_le
 
 def dfl_philox4x32_10(inp, n, out, stream=None):
     _check("dfl_philox4x32_10", load().dfl_philox4x32_10(ptr(inp), n, ptr(out), _stream(stream)))
+
+
+def dfl_kv4_page_bytes(page, Hkv, hd) -> int:
+    return int(load().dfl_kv4_page_bytes(page, Hkv, hd))
+
+
+def dfl_kv4_append(pool: Kv4Pool, layer, pages: Pages, start, n_new, R, K, V, stream=None):
+    _check("dfl_kv4_append",
+           load().dfl_kv4_append(C.byref(pool), layer, C.byref(pages), ptr(start), ptr(n_new), R, ptr(K), ptr(V),
+                                 _stream(stream)))
+
+
+def dfl_kv4_read(pool: Kv4Pool, layer, pages: Pages, start, count, R, K, V, stream=None):
+    _check("dfl_kv4_read",
+           load().dfl_kv4_read(C.byref(pool), layer, C.byref(pages), ptr(start), ptr(count), R, ptr(K), ptr(V),
+                               _stream(stream)))
+
+
+def dfl_kv4_attn(pool: Kv4Pool, layer, pages: Pages, Q, Kb, Vb, B, Hq, O, ws, ws_bytes, stream=None):
+    _check("dfl_kv4_attn",
+           load().dfl_kv4_attn(C.byref(pool), layer, C.byref(pages), ptr(Q), ptr(Kb), ptr(Vb), B, Hq, ptr(O), ptr(ws),
+                               ws_bytes, _stream(stream)))
+
+
+def dfl_pages_reserve(pool: Kv4Pool, pages: Pages, n_new, start, ws, ws_bytes, stream=None):
+    _check("dfl_pages_reserve",
+           load().dfl_pages_reserve(C.byref(pool), C.byref(pages), ptr(n_new), ptr(start), ptr(ws), ws_bytes,
+                                    _stream(stream)))
+
+
+def dfl_pages_remap(pool: Kv4Pool, pages: Pages, parent, keep_len, ws, ws_bytes, stream=None):
+    _check("dfl_pages_remap",
+           load().dfl_pages_remap(C.byref(pool), C.byref(pages), ptr(parent), ptr(keep_len), ptr(ws), ws_bytes,
+                                  _stream(stream)))
+
+
+def dfl_pages_compact(pool: Kv4Pool, pages: Pages, map_, live, ws, ws_bytes, stream=None):
+    _check("dfl_pages_compact",
+           load().dfl_pages_compact(C.byref(pool), C.byref(pages), ptr(map_), ptr(live), ptr(ws), ws_bytes,
+                                    _stream(stream)))
+
+
+def dfl_draft_step_paged(args: StepArgs, ctx: PagedCtx, ws, ws_bytes, stream=None):
+    _check("dfl_draft_step_paged",
+           load().dfl_draft_step_paged(C.byref(args), C.byref(ctx), ptr(ws), ws_bytes, _stream(stream)))

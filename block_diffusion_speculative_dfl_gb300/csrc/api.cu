@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "paged.h"
 #include "small_kernels.h"
 
 // Per-device error word: the first kernel that records an error wins.
@@ -88,6 +89,7 @@ DeviceCtx* current_ctx() {
     }
     for (auto& f : c.gemm_attr_set) f = false;
     for (auto& f : c.attn_attr_set) f = false;
+    for (auto& f : c.kv4_attr_set) f = false;
     c.mix_attr_set = false;
     c.err_word = word;
     c.device = dev;
@@ -149,18 +151,30 @@ size_t ws_lm_head(int N, int B, int row0, int d, int V, int dt, bool logits_miss
 // drafts, then scratch shared by the calls in turn.  The cached step mixes
 // and projects R rows per sequence, keeps K/V in the caller's cache (C is its
 // capacity) and, when sampling, lends the feature area to the logits.
-size_t step_ws_bytes(const dfl_shape& s, bool cached);
+// The paged step keeps the R new rows' K/V in scratch until they are written
+// into pages, and holds its page plan.
+enum StepMode { STEP_PLAIN = 0, STEP_CACHED = 1, STEP_PAGED = 2 };
+size_t step_ws_bytes(const dfl_shape& s, StepMode mode);
+
+// Attention output, the paged attention's partials, room for the K-split of
+// the output projection.
+size_t ws_block_attn_paged(int N, int B, int Hq, int Hkv, int hd, int d) {
+    return al256((size_t)N * B * Hq * hd * 2) + al256(kv4_attn_ws_bytes(N, B, Hq, Hkv, hd)) +
+           ws_oproj_split((int64_t)N * B, d);
+}
 
 // Host-input step: the plain step's workspace, then the context K/V of layers
 // 1..D-1 (layer 0's are the plain step's Kc / Vc).
 size_t kv_layer_bytes(const dfl_shape& s) { return al256((size_t)s.N * s.C * s.Hkv * s.hd * 2); }
 size_t step_host_ws_bytes(const dfl_shape& s) {
     if (s.dtype != DFL_BF16 || s.D < 1) return 0;
-    return step_ws_bytes(s, false) + (size_t)(s.D - 1) * 2 * kv_layer_bytes(s);
+    return step_ws_bytes(s, STEP_PLAIN) + (size_t)(s.D - 1) * 2 * kv_layer_bytes(s);
 }
 
-size_t step_ws_bytes(const dfl_shape& s, bool cached) {
+size_t step_ws_bytes(const dfl_shape& s, StepMode mode) {
+    const bool cached = mode != STEP_PLAIN;
     if (cached && (s.dtype != DFL_BF16 || s.R < 1)) return 0;
+    if (mode == STEP_PAGED && (s.N < 1 || s.pages < 1)) return 0;
     const size_t e = esz(s.dtype);
     const int64_t rows = (int64_t)s.N * (cached ? s.R : s.C);   // context rows mixed this step
     // per-layer mixtures of all D layers, or one fused representation and its
@@ -169,11 +183,13 @@ size_t step_ws_bytes(const dfl_shape& s, bool cached) {
     if (cached && s.V > 0 && s.K > 0) xc = std::max(xc, (size_t)s.N * (s.B - 1) * s.V * 4);
     size_t b = al256(xc);
     b += al256((size_t)s.N * s.B * s.Hq * s.hd * e);                         // Q
-    if (!cached) b += 2 * al256((size_t)s.N * s.C * s.Hkv * s.hd * e);       // Kc, Vc
+    if (mode != STEP_CACHED) b += 2 * al256((size_t)rows * s.Hkv * s.hd * e);  // Kc, Vc
     b += 2 * al256((size_t)s.N * s.B * s.Hkv * s.hd * e);                    // Kb, Vb
     if (cached) b += 2 * al256((size_t)rows * 4) + al256((size_t)s.N * s.B * 4) + al256((size_t)s.N * 4);
+    if (mode == STEP_PAGED) b += al256(pages_reserve_ws(s.N, s.pages));
     size_t sub = ws_dual_kv_proj(s.N, s.B, s.d, s.dtype);
-    sub = std::max(sub, ws_block_attn(s.N, s.C, s.B, s.Hq, s.Hkv, s.hd, s.dtype, cached, s.d));
+    sub = std::max(sub, mode == STEP_PAGED ? ws_block_attn_paged(s.N, s.B, s.Hq, s.Hkv, s.hd, s.d)
+                                           : ws_block_attn(s.N, s.C, s.B, s.Hq, s.Hkv, s.hd, s.dtype, cached, s.d));
     if (s.F > 0) sub = std::max(sub, ws_block_ffn(s.N, s.B, s.d, s.F, s.dtype, true));
     if (s.V > 0) {
         sub = std::max(sub, ws_lm_head(s.N, s.B, 1, s.d, s.V, s.dtype, true));
@@ -216,7 +232,7 @@ extern "C" size_t dfl_workspace_size(dfl_op op, const dfl_shape* s) {
     if (!s || (s->dtype != DFL_F32 && s->dtype != DFL_BF16)) return 0;
     // every size is a count: a negative one makes the shape invalid
     for (int32_t v : {s->N, s->C, s->B, s->d, s->Hq, s->Hkv, s->hd, s->D, s->L, s->V, s->K, s->G, s->row0, s->F, s->R,
-                      s->fc})
+                      s->fc, s->pages})
         if (v < 0) return 0;
     switch (op) {
         case DFL_OP_DUAL_KV_PROJ: return ws_dual_kv_proj(s->N, s->B, s->d, s->dtype);
@@ -228,11 +244,16 @@ extern "C" size_t dfl_workspace_size(dfl_op op, const dfl_shape* s) {
         case DFL_OP_TV_ACCEPTANCE: return tv_ws_bytes(s->N, s->K, s->G);
         case DFL_OP_SPEC_ACCEPT: return spec_ws_bytes(s->N, s->G, s->V);
         case DFL_OP_BLOCK_FFN: return s->F > 0 ? ws_block_ffn(s->N, s->B, s->d, s->F, s->dtype, true) : 0;
-        case DFL_OP_DRAFT_STEP: return step_ws_bytes(*s, false);
-        case DFL_OP_DRAFT_STEP_CACHED: return step_ws_bytes(*s, true);
+        case DFL_OP_DRAFT_STEP: return step_ws_bytes(*s, STEP_PLAIN);
+        case DFL_OP_DRAFT_STEP_CACHED: return step_ws_bytes(*s, STEP_CACHED);
         case DFL_OP_DRAFT_STEP_HOST: return step_host_ws_bytes(*s);
         case DFL_OP_FC_FUSE: return ws_fc_fuse((int64_t)s->N * s->C, s->d);
         case DFL_OP_SAMPLED_GREEDY: return sg_ws_bytes(s->N, s->G, s->V);
+        case DFL_OP_KV4_ATTN: return kv4_attn_ws_bytes(s->N, s->B, s->Hq, s->Hkv, s->hd);
+        case DFL_OP_PAGES_RESERVE: return s->N > 0 && s->pages > 0 ? pages_reserve_ws(s->N, s->pages) : 0;
+        case DFL_OP_PAGES_REMAP: return s->N > 0 && s->pages > 0 ? pages_remap_ws(s->N, s->pages) : 0;
+        case DFL_OP_PAGES_COMPACT: return s->pages > 0 ? pages_compact_ws(s->pages) : 0;
+        case DFL_OP_DRAFT_STEP_PAGED: return step_ws_bytes(*s, STEP_PAGED);
     }
     return 0;
 }
@@ -429,6 +450,24 @@ dfl_status dual_kv_proj_bf16(DeviceCtx* ctx, const void* Xc, int64_t ctx_M, int 
     return gemm_tc2(ctx, gb, gc, plan ? "gemm_kv_qkv_append" : "gemm_kv_qkv", st);
 }
 
+// Xb += O Wo^T.  The projection's few output tiles stream Wo through a few
+// CTAs: with `split` (room for the partials) it is split along K and summed in
+// a fixed order.
+dfl_status o_proj_bf16(DeviceCtx* ctx, const void* O, int M, int qd, const void* Wo, int d, float* Xb, float* split,
+                       size_t split_bytes, cudaStream_t st) {
+    GemmArgs g{};
+    g.A = O; g.M = M; g.K = qd;
+    g.B[0] = Wo; g.b_rows[0] = d; g.b_begin[0] = 0; g.nb = 1; g.N = d;
+    g.bn = 0;   // chosen per shape
+    g.m_inner = 1;
+    g.epi = EPI_RESID;
+    g.ep.resid = Xb; g.ep.ld_resid = d;
+    g.tag = "gemm_o_proj";
+    g.split_part = split;
+    g.split_part_bytes = split_bytes;
+    return gemm_tc(ctx, g, st);
+}
+
 // bf16 block attention and output projection, Xb += Attn(Q, [Kc;Kb], [Vc;Vb]) Wo^T.
 // ctx_len (nullable, device [N]): context keys of each sequence, C the maximum
 // and C_stride the context rows per sequence of Kc / Vc.
@@ -442,24 +481,12 @@ dfl_status block_attn_bf16(DeviceCtx* ctx, const void* Q, const void* Kc, const 
     void* O = carve(p, (size_t)N * B * qd * 2);
     if ((rc = attn_bf16(Q, Kc, Vc, Kb, Vb, N, C, B, Hq, Hkv, hd, O, p, st, ctx_len, C_stride, policy_N)) != DFL_OK)
         return rc;
-    GemmArgs g{};   // Xb += O Wo^T
-    g.A = O; g.M = N * B; g.K = qd;
-    g.B[0] = Wo; g.b_rows[0] = d; g.b_begin[0] = 0; g.nb = 1; g.N = d;
-    g.bn = 0;   // chosen per shape
-    g.m_inner = 1;
-    g.epi = EPI_RESID;
-    g.ep.resid = Xb; g.ep.ld_resid = d;
-    g.tag = "gemm_o_proj";
-    // The projection's few output tiles stream Wo through a few CTAs: when
-    // the workspace has room, it is split along K (partials after the
-    // attention's scratch) and summed in a fixed order.
+    // partials after the attention's scratch, when the workspace has room
     const size_t base = ws_block_attn(N, C, B, Hq, Hkv, hd, DFL_BF16, ctx_len != nullptr);
     const size_t room = ws_oproj_split((int64_t)N * B, d);
-    if (room > 0 && ws_bytes >= base + room) {
-        g.split_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + base);
-        g.split_part_bytes = room;
-    }
-    return gemm_tc(ctx, g, st);
+    const bool split = room > 0 && ws_bytes >= base + room;
+    return o_proj_bf16(ctx, O, N * B, qd, Wo, d, Xb,
+                       split ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + base) : nullptr, split ? room : 0, st);
 }
 
 }  // namespace
@@ -738,7 +765,9 @@ dfl_status rc_fc_shape(const dfl_step_args* a) {
 }
 
 // Host-side checks of a step's arguments (no launch).
-dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const void* ws) {
+// `paged`: the paged form (never together with `cache`).
+dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const void* ws,
+                      const dfl_paged_ctx* paged = nullptr) {
     if (!a || !ws) return DFL_ERR_INVALID_ARG;
     const int dt = a->dtype;
     if (dt != DFL_F32 && dt != DFL_BF16) return DFL_ERR_INVALID_ARG;
@@ -763,7 +792,7 @@ dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const 
     // Shape rules of the calls the step makes that hold for every dtype (each
     // with the status that call returns), checked before the first launch.
     if (a->L > 16 || a->Hq <= 0 || a->Hkv <= 0 || a->hd <= 0 || a->Hq % a->Hkv != 0) return DFL_ERR_INVALID_ARG;
-    const int64_t h_rows = (int64_t)a->N * (cache ? cache->R : a->C);
+    const int64_t h_rows = (int64_t)a->N * (cache ? cache->R : paged ? paged->R : a->C);
     if (!rows_fit(h_rows) || !rows_fit((int64_t)a->N * a->C) || !rows_fit((int64_t)a->N * a->B))
         return DFL_ERR_UNSUPPORTED_SHAPE;
     if (a->L > 1 && a->h_layer_stride < h_rows * a->d) return DFL_ERR_INVALID_ARG;
@@ -790,14 +819,27 @@ dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const 
             return DFL_ERR_MISALIGNED;
         return step_bf16_shape(a);
     }
+    if (paged) {
+        if (dt != DFL_BF16) return DFL_ERR_UNSUPPORTED_SHAPE;
+        if (!paged->n_new || !paged->start || paged->R < 1 || !paged->pages.ref) return DFL_ERR_INVALID_ARG;
+        dfl_status rc = kv4_check(paged->pool, 0, &paged->pages);
+        if (rc != DFL_OK) return rc;
+        const dfl_kv4_pool& p = *paged->pool;
+        if (p.layers < a->D || p.Hkv != a->Hkv || p.hd != a->hd || paged->pages.N != a->N) return DFL_ERR_INVALID_ARG;
+        if ((int64_t)paged->pages.max_pages * p.page > a->C) return DFL_ERR_INVALID_ARG;
+        if (!aligned4(paged->n_new) || !aligned4(paged->start)) return DFL_ERR_MISALIGNED;
+        if (a->B > 64) return DFL_ERR_UNSUPPORTED_SHAPE;
+        return step_bf16_shape(a);
+    }
     return DFL_OK;
 }
 
-dfl_shape step_shape(const dfl_step_args* a, const dfl_ctx_cache* cache) {
+dfl_shape step_shape(const dfl_step_args* a, const dfl_ctx_cache* cache, const dfl_paged_ctx* paged = nullptr) {
     dfl_shape s{};
     s.N = a->N; s.C = a->C; s.B = a->B; s.d = a->d; s.Hq = a->Hq; s.Hkv = a->Hkv; s.hd = a->hd; s.D = a->D;
     s.L = a->L; s.V = a->V; s.K = a->sample ? a->sample->K : 0; s.G = a->B - 1; s.row0 = 1; s.dtype = a->dtype;
-    s.F = a->F; s.R = cache ? cache->R : 0;
+    s.F = a->F; s.R = cache ? cache->R : paged ? paged->R : 0;
+    s.pages = paged ? paged->pool->num_pages : 0;
     s.fc = a->W_fc ? 1 : 0;
     return s;
 }
@@ -807,14 +849,15 @@ dfl_status step_tail(const dfl_step_args* a, const dfl_shape& s, uint8_t* Xc, si
 
 // The whole draft step; with `cache`, the incremental form over the caller's
 // context K/V cache (args->C its capacity, args->H the R new rows per sequence).
-dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, void* ws, size_t ws_bytes,
-                           dfl_stream stream) {
-    dfl_status rc = step_check(a, cache, ws);
+// With `paged`, the same over the 4-bit paged cache.
+dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, const dfl_paged_ctx* paged, void* ws,
+                           size_t ws_bytes, dfl_stream stream) {
+    dfl_status rc = step_check(a, cache, ws, paged);
     if (rc != DFL_OK) return rc;
     if (!aligned16(a->H)) return DFL_ERR_MISALIGNED;   // read by the mix's bulk copies
     const int dt = a->dtype;
-    const dfl_shape s = step_shape(a, cache);
-    if (ws_bytes < step_ws_bytes(s, cache != nullptr)) return DFL_ERR_WORKSPACE;
+    const dfl_shape s = step_shape(a, cache, paged);
+    if (ws_bytes < step_ws_bytes(s, cache ? STEP_CACHED : paged ? STEP_PAGED : STEP_PLAIN)) return DFL_ERR_WORKSPACE;
     if (!aligned16(ws)) return DFL_ERR_MISALIGNED;
     DeviceCtx* dctx = current_ctx();
     if (!dctx) return DFL_ERR_NO_DEVICE;
@@ -822,12 +865,12 @@ dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, v
     const dfl_dtype ddt = static_cast<dfl_dtype>(dt);
     const size_t e = esz(dt);
     const int N = a->N, C = a->C, B = a->B, d = a->d;
-    const int R = cache ? cache->R : C;
+    const int R = cache ? cache->R : paged ? paged->R : C;
     const int64_t ctx_rows = (int64_t)N * R;   // context rows mixed and projected this step
     uint8_t* p = static_cast<uint8_t*>(ws);
     const bool fc = a->W_fc != nullptr;
     size_t xc_bytes = fc ? al256((size_t)ctx_rows * d * e) + ws_fc_fuse(ctx_rows, d) : (size_t)a->D * ctx_rows * d * e;
-    if (cache && a->V > 0 && s.K > 0) xc_bytes = std::max(xc_bytes, (size_t)N * (B - 1) * a->V * 4);
+    if ((cache || paged) && a->V > 0 && s.K > 0) xc_bytes = std::max(xc_bytes, (size_t)N * (B - 1) * a->V * 4);
     uint8_t* Xc = carve(p, xc_bytes);
     float* F_fc = fc ? reinterpret_cast<float*>(Xc + al256((size_t)ctx_rows * d * e)) : nullptr;
     void* Q = carve(p, (size_t)N * B * a->Hq * a->hd * e);
@@ -837,12 +880,14 @@ dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, v
     void* Vb = carve(p, (size_t)N * B * a->Hkv * a->hd * e);
     KvRowPlan plan{};
     int32_t* len_new = nullptr;
-    if (cache) {
+    void* reserve_ws = nullptr;
+    if (cache || paged) {
         plan.ctx_pos = reinterpret_cast<int32_t*>(carve(p, (size_t)ctx_rows * 4));
         plan.ctx_dst = reinterpret_cast<int32_t*>(carve(p, (size_t)ctx_rows * 4));
         plan.blk_pos = reinterpret_cast<int32_t*>(carve(p, (size_t)N * B * 4));
-        plan.dst_rows = (int64_t)N * C;
+        plan.dst_rows = cache ? (int64_t)N * C : ctx_rows;
         len_new = reinterpret_cast<int32_t*>(carve(p, (size_t)N * 4));
+        if (paged) reserve_ws = carve(p, pages_reserve_ws(N, s.pages));
     }
     int32_t* samples = a->samples;
     if (a->V > 0 && s.K > 0) {
@@ -868,6 +913,14 @@ dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, v
                          const_cast<int32_t*>(plan.ctx_dst), const_cast<int32_t*>(plan.blk_pos), len_new,
                          dev_err(dctx), st)) != DFL_OK)
         return rc;
+    if (paged) {
+        if ((rc = pages_reserve_run(dctx, *paged->pool, paged->pages, paged->n_new, R, paged->start, reserve_ws, st)) !=
+            DFL_OK)
+            return rc;
+        if ((rc = paged_plan(N, R, B, paged->pages.max_pages * paged->pool->page, paged->pages.len, paged->start, paged->n_new, const_cast<int32_t*>(plan.ctx_pos),
+                             const_cast<int32_t*>(plan.ctx_dst), const_cast<int32_t*>(plan.blk_pos), st)) != DFL_OK)
+            return rc;
+    }
     if (fc) {
         if ((rc = fc_fuse_check(a->H, a->h_layer_stride, a->L, ctx_rows, d, dt, a->W_fc, a->fc_gain, Xc)) != DFL_OK)
             return rc;
@@ -890,6 +943,22 @@ dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, v
                 return rc;
             if ((rc = block_attn_bf16(dctx, Q, Kl, Vl, Kb, Vb, N, C, B, a->Hq, a->Hkv, a->hd, w.Wo, d, a->Xb, sub,
                                       sub_bytes, len_new, C, st)) != DFL_OK)
+                return rc;
+        } else if (paged) {
+            if ((rc = dual_kv_proj_bf16(dctx, xc_l, ctx_rows, R, a->Xb, N, B, d, a->blk_gain + (size_t)l * d, a->eps,
+                                        w.Wq, w.Wkc, w.Wvc, w.Wkb, w.Wvb, a->Hq, a->Hkv, a->hd, a->rope, Q, Kc, Vc,
+                                        Kb, Vb, sub, &plan, st, l == 0 ? a->Xb0 : nullptr)) != DFL_OK)
+                return rc;
+            if ((rc = kv4_append_run(dctx, *paged->pool, l, paged->pages, paged->start, paged->n_new, R, Kc, Vc, st)) !=
+                DFL_OK)
+                return rc;
+            uint8_t* q = sub;
+            void* O = carve(q, (size_t)N * B * a->Hq * a->hd * 2);
+            void* aws = carve(q, kv4_attn_ws_bytes(N, B, a->Hq, a->Hkv, a->hd));
+            if ((rc = kv4_attn_run(dctx, *paged->pool, l, paged->pages, Q, Kb, Vb, B, a->Hq, O, aws, st)) != DFL_OK)
+                return rc;
+            if ((rc = o_proj_bf16(dctx, O, N * B, a->Hq * a->hd, w.Wo, d, a->Xb, reinterpret_cast<float*>(q),
+                                  ws_oproj_split((int64_t)N * B, d), st)) != DFL_OK)
                 return rc;
         } else {
             if (bf) {
@@ -973,7 +1042,7 @@ dfl_status draft_step_host_impl(const dfl_step_args* a, void* H_dev, int chunks,
     if (!aligned16(H_dev) || (a->h_layer_stride * 2) % 16 != 0 || a->d % 8 != 0) return DFL_ERR_MISALIGNED;
     if (a->h_layer_stride < (int64_t)a->N * a->C * a->d) return DFL_ERR_INVALID_ARG;
     const dfl_shape s = step_shape(a, nullptr);
-    const size_t plain_bytes = step_ws_bytes(s, false);
+    const size_t plain_bytes = step_ws_bytes(s, STEP_PLAIN);
     if (ws_bytes < step_host_ws_bytes(s)) return DFL_ERR_WORKSPACE;
     DeviceCtx* dctx = current_ctx();
     if (!dctx) return DFL_ERR_NO_DEVICE;
@@ -1117,7 +1186,7 @@ dfl_status draft_step_host_impl(const dfl_step_args* a, void* H_dev, int chunks,
 
 extern "C" dfl_status dfl_draft_step(const dfl_step_args* a, void* ws, size_t ws_bytes, dfl_stream stream) {
     const dfl::ApiRange nvtx_range("dfl_draft_step");
-    return draft_step_impl(a, nullptr, ws, ws_bytes, stream);
+    return draft_step_impl(a, nullptr, nullptr, ws, ws_bytes, stream);
 }
 
 extern "C" dfl_status dfl_draft_step_host(const dfl_step_args* a, void* H_dev, int32_t chunks, void* ws,
@@ -1130,7 +1199,14 @@ extern "C" dfl_status dfl_draft_step_cached(const dfl_step_args* a, const dfl_ct
                                             size_t ws_bytes, dfl_stream stream) {
     const dfl::ApiRange nvtx_range("dfl_draft_step_cached");
     if (!cache) return DFL_ERR_INVALID_ARG;
-    return draft_step_impl(a, cache, ws, ws_bytes, stream);
+    return draft_step_impl(a, cache, nullptr, ws, ws_bytes, stream);
+}
+
+extern "C" dfl_status dfl_draft_step_paged(const dfl_step_args* a, const dfl_paged_ctx* ctx, void* ws, size_t ws_bytes,
+                                           dfl_stream stream) {
+    const dfl::ApiRange nvtx_range("dfl_draft_step_paged");
+    if (!ctx) return DFL_ERR_INVALID_ARG;
+    return draft_step_impl(a, nullptr, ctx, ws, ws_bytes, stream);
 }
 
 // ---------------------------------------------------------------- tracing

@@ -1,0 +1,681 @@
+// Block attention over the 4-bit paged context cache.
+//
+//   O = softmax(Q [Kc; Kb]^T / sqrt(hd)) [Vc; Vb]
+// for the R = B * (Hq / Hkv) query rows that share K/V head h of sequence n:
+// Kc, Vc the len[n] cached tokens of the sequence's pages (4-bit cells, see
+// kv4.cuh), Kb, Vb the block's own B keys in bf16.  No mask.
+//
+// Work.  The keys of a sequence are cut into units of 64: ceil(len / 64)
+// context units and one unit of the block's own keys.  All units of all
+// (sequence, K/V head, row tile) triples in order form one line, cut into
+// equal ranges, one per CTA, whatever the lengths: no CTA waits for a longer
+// sequence, and the scratch depends on the grid alone.  A triple that lies
+// within one CTA's range is written directly; one that crosses borders leaves
+// one partial (sum, maximum, unnormalised O) per CTA, and a second kernel adds
+// a triple's partials in the order of the keys, so results repeat bit for bit.
+//
+// A CTA is four warps; warp w takes tokens 16w .. 16w + 15 (one cell) of every
+// unit of its range with its own running maximum, sum and O, so the warps meet
+// only at the end of a triple.  Each warp keeps a ring of cells in flight
+// (one bulk copy of 18 hd bytes each, K, V and scales together) and expands
+// codes in registers straight into operand fragments:
+//   S^T (16 tokens x 8 rows)  = K Q^T,  A = K codes * scale in fp16
+//   O^T (hd x 8 rows)        += V^T P^T, A = V codes * scale in fp16
+// with m16n8k16 warp products.  At these row counts the kernel is bound by
+// bytes and by the expansion, not by products: expanding into shared memory
+// for tcgen05 operands would write and read 4 hd bytes per key more than the
+// 9/8 hd that arrive, and that traffic alone takes longer than the reads from
+// HBM (18 B per token and dimension pair through 128 B per clock and SM).
+//
+// Numbers.  Expanded codes are exact in fp16.  Q is brought to fp16 after a
+// power of two per row takes its largest element to [1, 2): bf16's 8 bits
+// survive, elements below 2^-14 of the largest lose bits that are under 2^-24
+// of it.  P = 2^(s - m + 7) is rounded to fp16 (11 bits; the 7 keeps weights
+// down to 2^-31 of the largest, m trails the true maximum by at most 8); sums
+// of P are fp32 of the unrounded values.  The block's own keys and values use
+// bf16 products, which take their range.  Maxima are per row; O is rescaled
+// only when a maximum grows by more than 2^8.
+#include "internal.h"
+#include "kv4.cuh"
+#include "paged.h"
+
+namespace dfl {
+
+namespace {
+
+constexpr int KA_UNIT = 64;        // keys per unit
+constexpr int KA_WARPS = 4;        // one cell of 16 keys per warp and unit
+constexpr int KA_THREADS = KA_WARPS * 32;
+constexpr int KA_SLOTS = 4;        // cells in flight per warp
+constexpr float KA_LAZY = 8.f;     // rescale when a maximum grows by more (log2)
+constexpr float KA_LIFT = 7.f;     // P is 2^7 above its nominal value
+
+struct KaArgs {
+    Kv4Slab slab;
+    const int32_t* table;
+    const int32_t* len;
+    int max_pages;
+    int N, B, Hq, G, R;
+    int subs;                 // row tiles per K/V head
+    int HS;                   // Hkv * subs
+    const __nv_bfloat16* Q;   // [N*B][Hq][hd]
+    const __nv_bfloat16* Kb;  // [N*B][Hkv][hd]
+    const __nv_bfloat16* Vb;
+    __nv_bfloat16* O;         // [N*B][Hq][hd]
+    float* Opart;             // [2 * grid][rows][hd]
+    float2* ml;               // [2 * grid][rows] (maximum in log2 units, sum)
+    float scale_log2;         // log2(e) / sqrt(hd)
+    float k_pow2, v_pow2, v_inv;   // 2^k_exp, 2^v_exp, 2^-v_exp
+};
+
+__device__ __forceinline__ int ka_len(const KaArgs& a, int n, const DevErr& err) {
+    const int l = a.len[n], cap = a.max_pages * a.slab.page;
+    if (l >= 0 && l <= cap) return l;
+    record_error(err, DFL_ERR_INVALID_ARG);
+    return min(max(l, 0), cap);
+}
+
+__device__ __forceinline__ int ka_units(int len) { return (len + KA_UNIT - 1) / KA_UNIT + 1; }
+
+// The line of units and where position x falls on it.
+struct KaLine {
+    int total, per;     // units in all, per CTA
+    int n, before;      // sequence that holds x, units of the line before it
+};
+
+struct KaLineSmem {
+    int red[KA_THREADS / 32];
+    int n, before;
+};
+
+// per: units per CTA for a grid of gridDim.x; x = at(per, total), located when
+// 0 <= x < total.
+template <typename At>
+__device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int grid, KaLineSmem& sm, const DevErr& err, At at) {
+    const int chunk = (a.N + KA_THREADS - 1) / KA_THREADS;
+    const int n0 = min(a.N, (int)threadIdx.x * chunk), n1 = min(a.N, n0 + chunk);
+    int sum = 0;
+    for (int n = n0; n < n1; ++n) sum += ka_units(ka_len(a, n, err));
+    sum *= a.HS;
+    KaLine l;
+    const int pre = block_exscan<KA_THREADS>(sum, sm.red, &l.total);
+    l.per = max(1, (l.total + grid - 1) / grid);
+    const int x = at(l.per, l.total);
+    if (x >= pre && x < pre + sum) {
+        int p = pre;
+        for (int n = n0; n < n1; ++n) {
+            const int w = ka_units(ka_len(a, n, err)) * a.HS;
+            if (x < p + w) { sm.n = n; sm.before = p; break; }
+            p += w;
+        }
+    }
+    __syncthreads();
+    l.n = sm.n;
+    l.before = sm.before;
+    return l;
+}
+
+// A position on the line as (sequence, head and row tile, unit).
+struct KaPos {
+    int n, hs, u, nu, len;
+    __device__ __forceinline__ void next_triple(const KaArgs& a, const DevErr& err) {
+        u = 0;
+        if (++hs == a.HS) {
+            hs = 0;
+            if (++n < a.N) { len = ka_len(a, n, err); nu = ka_units(len); }
+        }
+    }
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int HD, int NT>
+struct KaCfg {
+    static constexpr int ROWS = 8 * NT;               // query rows of a tile
+    static constexpr int KSTEPS = HD / 16;            // products over the head dim
+    static constexpr int MT = HD / 16;                // 16-dim tiles of O^T
+    static constexpr int CELL = Kv4Cell<HD>::BYTES;
+    static constexpr int PITCH = HD + 4;              // floats per row of the warps' O in shared memory
+    static constexpr int RING = KA_WARPS * KA_SLOTS * CELL;
+    static constexpr int MERGE = KA_WARPS * ROWS * PITCH * 4;
+    static constexpr int ML = KA_WARPS * ROWS * 8;
+    static constexpr int SMEM = RING + MERGE + ML + KA_WARPS * KA_SLOTS * 8;
+    static constexpr int CTAS = NT == 1 ? 4 : 3;      // per SM (registers)
+    static_assert(CTAS * (SMEM + 1024) <= 227 * 1024, "shared memory");
+};
+
+// State of one warp over one triple: per lane, for query rows 2t and 2t + 1 of
+// each 8-row tile (t = lane % 4).
+template <int HD, int NT>
+struct KaAcc {
+    float o[NT][HD / 16][4];   // O^T: dims of this lane's eighth (lane / 4) x the two rows
+    float m[NT][2], l[NT][2];
+};
+
+// Softmax of one cell: s[nt] = (slot g, rows 2t, 2t+1), (slot g + 8, same), in
+// log2 units, masked slots -inf.  Updates m, l, rescales O; s becomes P.
+template <int HD, int NT>
+__device__ __forceinline__ void ka_softmax(KaAcc<HD, NT>& acc, float (&s)[NT][4]) {
+    bool need = false;
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        need |= fmaxf(s[nt][0], s[nt][2]) > acc.m[nt][0] + KA_LAZY || fmaxf(s[nt][1], s[nt][3]) > acc.m[nt][1] + KA_LAZY;
+    if (__any_sync(0xFFFFFFFFu, need)) {
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float mx = fmaxf(s[nt][r], s[nt][r + 2]);
+                #pragma unroll
+                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                const float mo = acc.m[nt][r], mn = fmaxf(mo, mx);
+                const float al = mn == mo ? 1.f : ex2_ftz(mo - mn);   // 0 for the first cell
+                acc.m[nt][r] = mn;
+                acc.l[nt][r] *= al;
+                #pragma unroll
+                for (int i = 0; i < HD / 16; ++i) { acc.o[nt][i][r] *= al; acc.o[nt][i][r + 2] *= al; }
+            }
+        }
+    }
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        #pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float off = KA_LIFT - acc.m[nt][r];
+            s[nt][r] = ex2_ftz(s[nt][r] + off);
+            s[nt][r + 2] = ex2_ftz(s[nt][r + 2] + off);
+            acc.l[nt][r] += s[nt][r] + s[nt][r + 2];
+        }
+    }
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(KA_THREADS, KaCfg<HD, NT>::CTAS)
+kv4_attn_kernel(const KaArgs a, const DevErr err) {
+    using Cfg = KaCfg<HD, NT>;
+    using Cell = Kv4Cell<HD>;
+    constexpr int KW = HD / 32;          // words of a lane's quarter of a K row (codes)
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ KaLineSmem line_sm;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint8_t* ring = sm + warp * KA_SLOTS * Cfg::CELL;
+    float* merge = reinterpret_cast<float*>(sm + Cfg::RING);
+    float2* mlsm = reinterpret_cast<float2*>(sm + Cfg::RING + Cfg::MERGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + Cfg::RING + Cfg::MERGE + Cfg::ML) + warp * KA_SLOTS;
+    if (lane == 0) {
+        for (int i = 0; i < KA_SLOTS; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    grid_dep_begin();
+
+    const KaLine line = ka_locate(a, gridDim.x, line_sm, err, [&](int per, int total) {
+        const int64_t x = (int64_t)blockIdx.x * per;
+        return x < total ? (int)x : -1;
+    });
+    const int64_t x0l = (int64_t)blockIdx.x * line.per;
+    if (x0l >= line.total) return;
+    const int x0 = (int)x0l, x1 = min(line.total - x0, line.per) + x0;
+
+    KaPos pos;   // the triple being computed
+    pos.n = line.n;
+    pos.len = ka_len(a, pos.n, err);
+    pos.nu = ka_units(pos.len);
+    pos.hs = (x0 - line.before) / pos.nu;
+    pos.u = (x0 - line.before) - pos.hs * pos.nu;
+
+    // Producer: walks the same units ahead of the computation.  Lane i holds
+    // the pool cell of this warp's tokens in unit pbase + i.
+    KaPos pp = pos;
+    int pleft = x1 - x0;       // units the producer has not passed
+    int pbase = -1, pcell = 0;
+    unsigned issued = 0, taken = 0;
+    bool dead = false;         // a wait ran out: no more copies, no more computation
+    auto produce = [&]() {     // issue this warp's next cell, if any is left
+        while (pleft > 0) {
+            const int key = pp.u * KA_UNIT + warp * KV4_CELL_TOKENS;
+            if (key >= pp.len) {   // past the context (the block's own unit, or a short last unit): next unit
+                --pleft;
+                if (++pp.u == pp.nu) pp.next_triple(a, err);
+                pbase = -1;
+                continue;
+            }
+            if (pbase < 0 || pp.u >= pbase + 32) {
+                pbase = pp.u;
+                const int k = (pbase + lane) * KA_UNIT + warp * KV4_CELL_TOKENS;
+                if (k < pp.len) {
+                    const int j = k / a.slab.page, in = k - j * a.slab.page;
+                    int p = a.table[(int64_t)pp.n * a.max_pages + j];
+                    if (p < 0 || p >= a.slab.num_pages) { record_error(err, DFL_ERR_INVALID_ARG); p = 0; }
+                    pcell = (p * a.slab.Hkv + pp.hs / a.subs) * a.slab.cells + in / KV4_CELL_TOKENS;
+                }
+            }
+            const int cell = __shfl_sync(0xFFFFFFFFu, pcell, pp.u - pbase);
+            if (lane == 0) {
+                const int s = issued % KA_SLOTS;
+                mbar_arrive_expect_tx(&full[s], Cfg::CELL);
+                bulk_g2s(ring + s * Cfg::CELL, a.slab.data + (int64_t)cell * Cfg::CELL, Cfg::CELL, &full[s]);
+            }
+            ++issued;
+            --pleft;
+            if (++pp.u == pp.nu) pp.next_triple(a, err);   // cannot happen: the last unit is the block's own
+            return;
+        }
+    };
+    #pragma unroll 1
+    for (int i = 0; i < KA_SLOTS; ++i) produce();
+
+    int x = x0;
+    #pragma unroll 1
+    while (x < x1) {
+        const int head = pos.hs / a.subs, row0 = (pos.hs - head * a.subs) * Cfg::ROWS;
+        const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
+        // ---- Q of this triple: lane (g, t) holds row g's quarter t of each 8-row tile
+        uint32_t q[NT][2 * Cfg::KSTEPS];
+        float mult[NT][2];   // rows 2t, 2t + 1: score of fp16 operands -> log2 units
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = row0 + nt * 8 + g;
+            uint32_t mx = 0;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.Q + ((int64_t)(pos.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + t * (HD / 4));
+            #pragma unroll
+            for (int i = 0; i < HD / 32; ++i) {
+                const uint4 w = r < a.R ? src[i] : make_uint4(0, 0, 0, 0);
+                q[nt][4 * i] = w.x; q[nt][4 * i + 1] = w.y; q[nt][4 * i + 2] = w.z; q[nt][4 * i + 3] = w.w;
+            }
+            #pragma unroll
+            for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) mx = max(mx, max(q[nt][i] & 0x7FFFu, (q[nt][i] >> 16) & 0x7FFFu));
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+            mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+            int e = (int)(mx >> 7);                       // biased exponent of the row's largest element
+            e = (e == 0 || e >= 254) ? 127 : e;           // zero, subnormal, huge or not finite: as it is
+            const float down = __int_as_float((254 - e) << 23);
+            #pragma unroll
+            for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) q[nt][i] = pack_half(bf16lo(q[nt][i]) * down, bf16hi(q[nt][i]) * down);
+            const float up = __int_as_float(e << 23) * a.scale_log2 * a.k_pow2;
+            mult[nt][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * t);       // lane of row 2t
+            mult[nt][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * t + 4);   // lane of row 2t + 1
+        }
+        KaAcc<HD, NT> acc;
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            #pragma unroll
+            for (int i = 0; i < Cfg::MT; ++i)
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) acc.o[nt][i][c] = 0.f;
+            acc.m[nt][0] = acc.m[nt][1] = -INFINITY;
+            acc.l[nt][0] = acc.l[nt][1] = 0.f;
+        }
+        // ---- context cells
+        const int ctx_end = min(u1, pos.nu - 1);
+        #pragma unroll 1
+        for (int u = u0; u < ctx_end; ++u) {
+            const int left = pos.len - u * KA_UNIT - warp * KV4_CELL_TOKENS;   // tokens from this cell on
+            if (left <= 0 || dead) continue;
+            const int sl = taken % KA_SLOTS;
+            const bool ok = mbar_wait(&full[sl], (taken / KA_SLOTS) & 1, err);
+            if (!__all_sync(0xFFFFFFFFu, ok)) { dead = true; continue; }
+            const uint8_t* cell = ring + sl * Cfg::CELL;
+            ++taken;
+            float s[NT][4];
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+            {   // S^T: slots g and g + 8
+                uint32_t kc[2][KW];   // codes of this lane's quarter
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t* p = cell + Cell::K_CODES + (g + 8 * h) * Cell::ROW + t * (Cell::ROW / 4);
+                    if constexpr (HD == 128) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(p);
+                        kc[h][0] = w.x; kc[h][1] = w.y; kc[h][2] = w.z; kc[h][3] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(p);
+                        kc[h][0] = w.x; kc[h][1] = w.y;
+                    }
+                }
+                uint32_t sc[2][HD / 64];   // fp16 pairs (s, s) of the lane's groups
+                if constexpr (HD == 128) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(cell + Cell::K_SCALES + lane * 4);
+                    const uint32_t h0 = e4m3x2_to_half(w & 0xFFFFu), h1 = e4m3x2_to_half(w >> 16);
+                    sc[0][0] = __byte_perm(h0, h0, 0x1010); sc[0][1] = __byte_perm(h0, h0, 0x3232);
+                    sc[1][0] = __byte_perm(h1, h1, 0x1010); sc[1][1] = __byte_perm(h1, h1, 0x3232);
+                } else {
+                    const uint32_t w = *reinterpret_cast<const uint16_t*>(cell + Cell::K_SCALES + lane * 2);
+                    const uint32_t h0 = e4m3x2_to_half(w);
+                    sc[0][0] = __byte_perm(h0, h0, 0x1010);
+                    sc[1][0] = __byte_perm(h0, h0, 0x3232);
+                }
+                #pragma unroll
+                for (int w = 0; w < KW; ++w) {   // 8 dims: two products over the head dim
+                    uint32_t h0[4], h1[4];
+                    e2m1x8_to_half(kc[0][w], h0);
+                    e2m1x8_to_half(kc[1][w], h1);
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h0[i] = hmul2u(h0[i], sc[0][w / 2]);
+                        h1[i] = hmul2u(h1[i], sc[1][w / 2]);
+                    }
+                    #pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t af[4] = {h0[2 * j], h1[2 * j], h0[2 * j + 1], h1[2 * j + 1]};
+                        #pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], af, q[nt][4 * w + 2 * j], q[nt][4 * w + 2 * j + 1]);
+                    }
+                }
+            }
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                s[nt][0] *= mult[nt][0]; s[nt][1] *= mult[nt][1];
+                s[nt][2] *= mult[nt][0]; s[nt][3] *= mult[nt][1];
+            }
+            if (left < KV4_CELL_TOKENS) {   // the cell's last tokens do not exist
+                const bool v0 = Cell::token(g) < left, v1 = Cell::token(g + 8) < left;
+                #pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (!v0) s[nt][0] = s[nt][1] = -INFINITY;
+                    if (!v1) s[nt][2] = s[nt][3] = -INFINITY;
+                }
+            }
+            ka_softmax<HD, NT>(acc, s);
+            uint32_t pb[NT][2];
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                pb[nt][0] = transpose8x8(pack_half(s[nt][0], s[nt][1]));
+                pb[nt][1] = transpose8x8(pack_half(s[nt][2], s[nt][3]));
+            }
+            {   // O^T: tokens t, 4 + t (slots 2t, 2t + 1) and 8 + t, 12 + t
+                const int vg = HD == 128 ? g : g >> 1;
+                uint32_t sw = *reinterpret_cast<const uint32_t*>(cell + Cell::V_SCALES + vg * 16 + t * 4);
+                uint32_t sp[2] = {e4m3x2_to_half(sw & 0xFFFFu), e4m3x2_to_half(sw >> 16)};
+                if (left < KV4_CELL_TOKENS) {   // weight 0 times a stored NaN would be NaN
+                    #pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (8 * i + t >= left) sp[i] &= 0xFFFF0000u;
+                        if (8 * i + 4 + t >= left) sp[i] &= 0x0000FFFFu;
+                    }
+                }
+                uint32_t ev[2][HD / 64], od[2][HD / 64];   // (token pair) x even / odd dims of the lane's eighth
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t A[HD / 64], Bw[HD / 64];
+                    const uint8_t* pa = cell + Cell::V_CODES + (8 * i + t) * Cell::ROW;
+                    const uint8_t* pbp = pa + 4 * Cell::ROW;
+                    if constexpr (HD == 128) {
+                        const int off = (g * 8) ^ Cell::v_swap(t);   // tokens t and t + 4 k swap alike
+                        const uint2 wa = *reinterpret_cast<const uint2*>(pa + off);
+                        const uint2 wb = *reinterpret_cast<const uint2*>(pbp + off);
+                        A[0] = wa.x; A[1] = wa.y; Bw[0] = wb.x; Bw[1] = wb.y;
+                    } else {
+                        A[0] = *reinterpret_cast<const uint32_t*>(pa + g * 4);
+                        Bw[0] = *reinterpret_cast<const uint32_t*>(pbp + g * 4);
+                    }
+                    #pragma unroll
+                    for (int w = 0; w < HD / 64; ++w) {
+                        ev[i][w] = (A[w] & 0x0F0F0F0Fu) | ((Bw[w] << 4) & 0xF0F0F0F0u);
+                        od[i][w] = ((A[w] >> 4) & 0x0F0F0F0Fu) | (Bw[w] & 0xF0F0F0F0u);
+                    }
+                }
+                #pragma unroll
+                for (int w = 0; w < HD / 64; ++w) {
+                    uint32_t e0[4], e1[4], o0[4], o1[4];
+                    e2m1x8_to_half(ev[0][w], e0);
+                    e2m1x8_to_half(ev[1][w], e1);
+                    e2m1x8_to_half(od[0][w], o0);
+                    e2m1x8_to_half(od[1][w], o1);
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t af[4] = {hmul2u(e0[i], sp[0]), hmul2u(o0[i], sp[0]), hmul2u(e1[i], sp[1]),
+                                                hmul2u(o1[i], sp[1])};
+                        #pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16(acc.o[nt][4 * w + i], af, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+            __syncwarp();   // the slot has been read by every lane
+            produce();
+        }
+        // ---- the block's own keys (bf16), 16 per warp
+        if (u1 == pos.nu && warp * KV4_CELL_TOKENS < a.B && !dead) {
+            const int Hkv = a.slab.Hkv;
+            float s[NT][4];
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+            const int b0 = warp * KV4_CELL_TOKENS + Cell::token(g), b1 = warp * KV4_CELL_TOKENS + Cell::token(g + 8);
+            const uint4* k0 = reinterpret_cast<const uint4*>(a.Kb + ((int64_t)(pos.n * a.B + b0) * Hkv + head) * HD + t * (HD / 4));
+            const uint4* k1 = reinterpret_cast<const uint4*>(a.Kb + ((int64_t)(pos.n * a.B + b1) * Hkv + head) * HD + t * (HD / 4));
+            #pragma unroll
+            for (int i = 0; i < HD / 32; ++i) {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                const uint4 w0 = b0 < a.B ? k0[i] : z, w1 = b1 < a.B ? k1[i] : z;
+                const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
+                #pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int r = row0 + nt * 8 + g;
+                    const uint4 qw = r < a.R ? reinterpret_cast<const uint4*>(
+                        a.Q + ((int64_t)(pos.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + t * (HD / 4))[i] : z;
+                    mma_b16(s[nt], f0, qw.x, qw.y);
+                    mma_b16(s[nt], f1, qw.z, qw.w);
+                }
+            }
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) s[nt][c] = (c < 2 ? b0 : b1) < a.B ? s[nt][c] * a.scale_log2 : -INFINITY;
+            ka_softmax<HD, NT>(acc, s);
+            uint32_t pb[NT][2];
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {   // O is kept in units of 2^v_exp
+                pb[nt][0] = transpose8x8(pack_bf16(s[nt][0] * a.v_inv, s[nt][1] * a.v_inv));
+                pb[nt][1] = transpose8x8(pack_bf16(s[nt][2] * a.v_inv, s[nt][3] * a.v_inv));
+            }
+            #pragma unroll
+            for (int w = 0; w < HD / 64; ++w) {   // 8 dims of the lane's eighth at a time
+                uint4 v[4];
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int b = warp * KV4_CELL_TOKENS + 4 * i + t;
+                    v[i] = b < a.B ? *reinterpret_cast<const uint4*>(
+                        a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0);
+                }
+                const uint32_t* v0 = &v[0].x; const uint32_t* v1 = &v[1].x;
+                const uint32_t* v2 = &v[2].x; const uint32_t* v3 = &v[3].x;
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t af[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
+                                            __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632)};
+                    #pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_b16(acc.o[nt][4 * w + i], af, pb[nt][0], pb[nt][1]);
+                }
+            }
+        }
+        // ---- the warps' parts of this triple
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            #pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float l = acc.l[nt][r];
+                #pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                const int row = nt * 8 + 2 * t + r;
+                if (g == 0) mlsm[warp * Cfg::ROWS + row] = make_float2(acc.m[nt][r], l);
+                float* dst = merge + (warp * Cfg::ROWS + row) * Cfg::PITCH + g * (HD / 8);
+                #pragma unroll
+                for (int i = 0; i < Cfg::MT; i += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc.o[nt][i][r], acc.o[nt][i][r + 2],
+                                                                          acc.o[nt][i + 1][r], acc.o[nt][i + 1][r + 2]);
+            }
+        __syncthreads();
+        {
+            const bool whole = u0 == 0 && u1 == pos.nu;
+            const int part = 2 * (int)blockIdx.x + (u0 == 0 ? 1 : 0);
+            constexpr int TPR = HD / 4;   // threads per row
+            #pragma unroll 1
+            for (int row = threadIdx.x / TPR; row < Cfg::ROWS; row += KA_THREADS / TPR) {
+                const int r = row0 + row, c = (threadIdx.x % TPR) * 4;
+                if (r >= a.R) break;
+                float2 ml[KA_WARPS];
+                float M = -INFINITY, L = 0.f;
+                #pragma unroll
+                for (int w = 0; w < KA_WARPS; ++w) { ml[w] = mlsm[w * Cfg::ROWS + row]; M = fmaxf(M, ml[w].x); }
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                #pragma unroll
+                for (int w = 0; w < KA_WARPS; ++w) {
+                    const float f = ml[w].x == -INFINITY ? 0.f : ex2_ftz(ml[w].x - M);
+                    const float4 v = *reinterpret_cast<const float4*>(merge + (w * Cfg::ROWS + row) * Cfg::PITCH + c);
+                    L += f * ml[w].y;
+                    o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+                }
+                if (whole) {
+                    const float inv = a.v_pow2 / L;
+                    const int64_t at = ((int64_t)(pos.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + c;
+                    if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
+                        *reinterpret_cast<uint2*>(a.O + at) =
+                            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+                } else {
+                    const int64_t at = ((int64_t)part * Cfg::ROWS + row) * HD + c;
+                    if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)2 * gridDim.x * Cfg::ROWS * HD)) {
+                        *reinterpret_cast<float4*>(a.Opart + at) = o;
+                        if (c == 0) a.ml[part * Cfg::ROWS + row] = make_float2(M, L);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        x += u1 - u0;
+        pos.u = u1;
+        if (u1 == pos.nu) pos.next_triple(a, err);
+    }
+    // After a wait that ran out: let the copies in flight land before the CTA's shared memory goes.
+    for (; taken < issued; ++taken) mbar_wait(&full[taken % KA_SLOTS], (taken / KA_SLOTS) & 1, err);
+}
+
+// Adds up the triple that starts in CTA blockIdx.x's range and ends past it:
+// partials of that CTA (its last) and of the following CTAs (their first), in
+// the order of the keys.
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(KA_THREADS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
+    __shared__ KaLineSmem line_sm;
+    grid_dep_begin();
+    const KaLine line = ka_locate(a, gridDim.x, line_sm, err, [&](int per, int total) {
+        const int64_t end = ((int64_t)blockIdx.x + 1) * per;   // a triple crosses the border before `end`
+        return end < total ? (int)end : -1;
+    });
+    const int64_t endl = ((int64_t)blockIdx.x + 1) * line.per;
+    if (endl >= line.total) return;
+    const int end = (int)endl;
+    const int nu = ka_units(ka_len(a, line.n, err));
+    const int hs = (end - line.before) / nu;
+    const int p0 = line.before + hs * nu, p1 = p0 + nu;   // the triple holding unit `end`
+    if (p0 == end || p0 < end - line.per) return;          // none crosses, or it started before this CTA
+    const int first = blockIdx.x, last = (p1 - 1) / line.per;
+    const int head = hs / a.subs, row0 = (hs - head * a.subs) * ROWS;
+    constexpr int TPR = HD / 4;
+    for (int row = threadIdx.x / TPR; row < ROWS; row += KA_THREADS / TPR) {
+        const int r = row0 + row, c = (threadIdx.x % TPR) * 4;
+        if (r >= a.R) break;
+        float M = -INFINITY, L = 0.f;
+        for (int j = first; j <= last; ++j) M = fmaxf(M, a.ml[(2 * j + (j == first)) * ROWS + row].x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        #pragma unroll 4
+        for (int j = first; j <= last; ++j) {
+            const int64_t at = (int64_t)(2 * j + (j == first)) * ROWS + row;
+            const float2 ml = a.ml[at];
+            const float4 v = *reinterpret_cast<const float4*>(a.Opart + at * HD + c);
+            const float f = ml.x == -INFINITY ? 0.f : ex2_ftz(ml.x - M);
+            L += f * ml.y;
+            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+        }
+        const float inv = a.v_pow2 / L;
+        const int64_t at = ((int64_t)(line.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + c;
+        if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
+            *reinterpret_cast<uint2*>(a.O + at) =
+                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    }
+}
+
+constexpr int KA_SMS = 152;   // SMs of a GB300
+
+// Row tiles of 8 query rows when a group has at most 8, else of 16: a wider
+// tile expands each key for more rows at once.
+int ka_nt(int R) { return R <= 8 ? 1 : 2; }
+
+// CTAs of the launch: every SM full, or one per unit when there are fewer.
+int ka_grid(int64_t units, int nt) { return (int)std::min<int64_t>(units, KA_SMS * (nt == 1 ? 4 : 3)); }
+
+inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
+    if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    const int nt = ka_nt(B * (Hq / Hkv));
+    const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * 8 * nt;
+    return al256(parts * hd * 4) + al256(parts * 8);
+}
+
+dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
+                        const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st) {
+    const int G = Hq / pool.Hkv, R = B * G, nt = ka_nt(R);
+    KaArgs a{};
+    a.slab = kv4_slab(pool, layer);
+    a.table = pg.table; a.len = pg.len; a.max_pages = pg.max_pages;
+    a.N = pg.N; a.B = B; a.Hq = Hq; a.G = G; a.R = R;
+    a.subs = (R + 8 * nt - 1) / (8 * nt);
+    a.HS = pool.Hkv * a.subs;
+    a.Q = static_cast<const __nv_bfloat16*>(Q);
+    a.Kb = static_cast<const __nv_bfloat16*>(Kb);
+    a.Vb = static_cast<const __nv_bfloat16*>(Vb);
+    a.O = static_cast<__nv_bfloat16*>(O);
+    const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * 8 * nt;
+    a.Opart = static_cast<float*>(ws);
+    a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
+    a.scale_log2 = 1.4426950408889634f / sqrtf((float)pool.hd);
+    a.k_pow2 = kv4_exp2i(pool.k_exp); a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
+    const int64_t cap_units = (int64_t)pg.max_pages * pool.page / KA_UNIT + 2;
+    if (cap_units * pg.N * a.HS >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    const int grid = ka_grid(cap_units * pg.N * a.HS, nt);
+    const DevErr err = dev_err(ctx);
+    auto run = [&](auto kern, auto join, int smem, int slot) -> dfl_status {
+        if (!ctx->kv4_attr_set[slot]) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return DFL_ERR_CUDA;
+            ctx->kv4_attr_set[slot] = true;
+        }
+        {
+            ProfScope ps("kv4_attn", st);
+            const dfl_status rc = launch_pdl(kern, grid, KA_THREADS, smem, st, a, err);
+            if (rc != DFL_OK) return rc;
+        }
+        ProfScope ps("kv4_attn_join", st);
+        return launch_pdl(join, grid, KA_THREADS, 0, st, a, err);
+    };
+    if (pool.hd == 128)
+        return nt == 1 ? run(kv4_attn_kernel<128, 1>, kv4_attn_join_kernel<128, 8>, KaCfg<128, 1>::SMEM, 0)
+                       : run(kv4_attn_kernel<128, 2>, kv4_attn_join_kernel<128, 16>, KaCfg<128, 2>::SMEM, 1);
+    return nt == 1 ? run(kv4_attn_kernel<64, 1>, kv4_attn_join_kernel<64, 8>, KaCfg<64, 1>::SMEM, 2)
+                   : run(kv4_attn_kernel<64, 2>, kv4_attn_join_kernel<64, 16>, KaCfg<64, 2>::SMEM, 3);
+}
+
+}  // namespace dfl

@@ -178,6 +178,29 @@ dfl_status cache_plan(int N, int R, int B, int C, int32_t* ctx_len, const int32_
                       pos_blk, len_new, err);
 }
 
+// The same for the paged cache, after the step's pages are reserved: new rows
+// of a served sequence (start[n] >= 0) keep their slot n*R + i until they are
+// written into pages; the block follows the len[n] tokens held.
+// len is read as 0..cap (a length outside is recorded by the reservation):
+// the block's positions index the rotary table.
+__global__ void paged_plan_kernel(int R, int B, int cap, const int32_t* len, const int32_t* start, const int32_t* n_new,
+                                  int32_t* pos_ctx, int32_t* dst_ctx, int32_t* pos_blk) {
+    grid_dep_begin();
+    const int n = blockIdx.x;
+    const int s = start[n], m = s >= 0 ? n_new[n] : 0, l = min(max(len[n], 0), cap);
+    for (int i = threadIdx.x; i < R; i += blockDim.x) {
+        pos_ctx[(int64_t)n * R + i] = i < m ? s + i : 0;
+        dst_ctx[(int64_t)n * R + i] = i < m ? n * R + i : -1;
+    }
+    for (int b = threadIdx.x; b < B; b += blockDim.x) pos_blk[(int64_t)n * B + b] = l + b;
+}
+
+dfl_status paged_plan(int N, int R, int B, int cap, const int32_t* len, const int32_t* start, const int32_t* n_new,
+                      int32_t* pos_ctx, int32_t* dst_ctx, int32_t* pos_blk, cudaStream_t st) {
+    ProfScope ps("paged_plan", st);
+    return launch_pdl(paged_plan_kernel, N, 128, 0, st, R, B, cap, len, start, n_new, pos_ctx, dst_ctx, pos_blk);
+}
+
 // --------------------------------------------------------- argmax combine
 
 // argmax over per-tile partials; equal maxima resolve to the lower column

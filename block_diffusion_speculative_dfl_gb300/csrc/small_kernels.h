@@ -20,6 +20,9 @@ dfl_status rmsnorm_rows(const float* in, int d, int64_t M, int per, int stride, 
 dfl_status cache_plan(int N, int R, int B, int C, int32_t* ctx_len, const int32_t* n_new, int advance,
                       int32_t* pos_ctx, int32_t* dst_ctx, int32_t* pos_blk, int32_t* len_new, DevErr err,
                       cudaStream_t st);
+// cap: the tokens a sequence can hold.
+dfl_status paged_plan(int N, int R, int B, int cap, const int32_t* len, const int32_t* start, const int32_t* n_new,
+                      int32_t* pos_ctx, int32_t* dst_ctx, int32_t* pos_blk, cudaStream_t st);
 dfl_status greedy_accept(const int32_t* draft, const int32_t* target, int N, int n, int32_t* accept_len,
                          int32_t* bonus, cudaStream_t st);
 dfl_status argmax_combine(const float* pmax, const int* pidx, int64_t M, int tiles, int32_t* out,

@@ -17,6 +17,7 @@ import torch
 
 from . import _lib
 from ._lib import DFL_BF16, DFL_F32, LayerWeights, SampleParams, StepArgs
+from .paged import PagedCache
 
 
 @dataclass(frozen=True)
@@ -265,6 +266,71 @@ class CachedDraftModel(DraftModel):
                       advance=advance, stream=st)
             out = {"accept_len": self.accept_len.to("cpu", non_blocking=True),
                    "bonus": self.bonus.to("cpu", non_blocking=True)}
+            if self.draft is not None:
+                out["draft"] = self.draft.to("cpu", non_blocking=True)
+        st.synchronize()
+        return out, dev_in
+
+
+class PagedDraftModel(DraftModel):
+    """Drafter over a paged 4-bit context cache (``dfl_draft_step_paged``).
+
+    ``shape.C`` is the most tokens a sequence may hold (a multiple of
+    ``page``).  ``cache`` holds the pages of all draft layers; between steps
+    its ``remap`` (fork, roll back, end) and ``compact`` apply.  A step
+    reserves pages for its new rows; ``cache.start`` then has each sequence's
+    old length, or -1 where the pool had no room and the rows were dropped.
+    """
+
+    def __init__(self, shape: DraftShape, R_max: int, num_pages: int, *args, page=64, k_exp=0, v_exp=0, device="cuda",
+                 **kw):
+        if shape.dtype != "bf16":
+            raise ValueError("the paged draft step runs in bf16")
+        if shape.C % page != 0:
+            raise ValueError("shape.C must be a multiple of the page")
+        self.R_max = self.R = int(R_max)
+        self.cache = PagedCache(shape.D, num_pages, page, shape.Hkv, shape.hd, shape.N, shape.C // page, k_exp, v_exp,
+                                device)
+        super().__init__(shape, *args, device=device, **kw)
+
+    def _workspace_bytes(self) -> int:
+        s = self.shape
+        return _lib.workspace_size(_lib.DFL_OP_DRAFT_STEP_PAGED, N=s.N, C=s.C, B=s.B, d=s.d, Hq=s.Hq, Hkv=s.Hkv,
+                                   hd=s.hd, D=s.D, L=s.L, V=s.V, K=s.K, G=s.B - 1, row0=1, dtype=s.dt, F=s.F,
+                                   R=self.R_max, fc=s.fc, pages=self.cache.num_pages)
+
+    def _h_rows(self) -> int:
+        return self.R
+
+    def step(self, H_new, Xb0, n_new, target=None, vlog=None, R=None, stream=None):
+        """One paged draft step; H_new [L][N*R][d] as in ``CachedDraftModel.step``."""
+        self.R = self.R_max if R is None else int(R)
+        if not 1 <= self.R <= self.R_max:
+            raise ValueError(f"R={self.R} outside 1..{self.R_max}")
+        ctx = _lib.PagedCtx(C.pointer(self.cache.pool), self.cache.pages, self.R, _lib.ptr(n_new),
+                            _lib.ptr(self.cache.start))
+        self._last_args, self._last_ctx = self._args(H_new, Xb0, target, vlog), ctx
+        _lib.dfl_draft_step_paged(self._last_args, ctx, self.ws, self.ws_bytes, stream)
+
+    def step_from_host(self, H_host, Xb0_host, n_new_host, target_host=None, vlog_host=None, dev_in=None, R=None,
+                       stream=None):
+        """End-to-end paged step: pinned host inputs (the new rows, block init, n_new) in, results out."""
+        st = stream or torch.cuda.current_stream()
+        if dev_in is None:
+            dev_in = {}
+        ins = {"H": H_host, "Xb0": Xb0_host, "n_new": n_new_host, "target": target_host, "vlog": vlog_host}
+        with torch.cuda.stream(st):
+            for k, h in ins.items():
+                if h is None:
+                    continue
+                if k not in dev_in:
+                    dev_in[k] = torch.empty(h.shape, dtype=h.dtype, device=self.Xb.device)
+                dev_in[k].copy_(h, non_blocking=True)
+            self.step(dev_in["H"], dev_in["Xb0"], dev_in["n_new"], dev_in.get("target"), dev_in.get("vlog"), R=R,
+                      stream=st)
+            out = {"accept_len": self.accept_len.to("cpu", non_blocking=True),
+                   "bonus": self.bonus.to("cpu", non_blocking=True),
+                   "start": self.cache.start.to("cpu", non_blocking=True)}
             if self.draft is not None:
                 out["draft"] = self.draft.to("cpu", non_blocking=True)
         st.synchronize()

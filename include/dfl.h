@@ -90,6 +90,9 @@ typedef struct dfl_shape {
                          where C is the cache capacity) */
     int32_t fc;       /* 1: the step's context features come from the DFlash
                          fusion (dfl_fc_fuse) instead of per-layer mixtures */
+    int32_t pages;        /* pages of the pool (DFL_OP_PAGES_RESERVE, DFL_OP_PAGES_COMPACT,
+                             DFL_OP_DRAFT_STEP_PAGED) or entries of a sequence's page table
+                             (DFL_OP_PAGES_REMAP) */
 } dfl_shape;
 
 typedef enum dfl_op {
@@ -104,7 +107,12 @@ typedef enum dfl_op {
     DFL_OP_DRAFT_STEP_CACHED = 9,
     DFL_OP_DRAFT_STEP_HOST = 10,
     DFL_OP_FC_FUSE = 11,           /* rows = N*C, d */
-    DFL_OP_SAMPLED_GREEDY = 12     /* N, G, V */
+    DFL_OP_SAMPLED_GREEDY = 12,    /* N, G, V */
+    DFL_OP_KV4_ATTN = 13,          /* N, B, Hq, Hkv, hd */
+    DFL_OP_PAGES_RESERVE = 14,     /* N, pages */
+    DFL_OP_PAGES_REMAP = 15,       /* N, pages */
+    DFL_OP_PAGES_COMPACT = 16,     /* pages */
+    DFL_OP_DRAFT_STEP_PAGED = 17   /* as DFL_OP_DRAFT_STEP_CACHED, and pages */
 } dfl_op;
 
 /* Library version string (static storage). */
@@ -559,6 +567,167 @@ typedef struct dfl_ctx_cache {
  */
 dfl_status dfl_draft_step_cached(const dfl_step_args* args, const dfl_ctx_cache* cache,
                                  void* ws, size_t ws_bytes, dfl_stream stream);
+
+/*
+ * Paged 4-bit context cache.
+ *
+ * A context key or value element is kept as c * s * 2^e: c one of the e2m1
+ * numbers 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign (4 bits), s an e4m3 number
+ * shared by 16 consecutive dimensions of one token and K/V head (a group), e
+ * an integer of the pool (k_exp for keys, v_exp for values; it moves the range
+ * 2^-9 .. 448 of the scales over the data).  Of a group x:
+ *   s = max(2^-9, e4m3(min(448, max|x| 2^-e / 6))),  c = e2m1(x / (s 2^e)),
+ * both to nearest even, c at most 6 in magnitude.  A group that holds an
+ * infinity or a NaN reads back as NaN throughout.  (9/16 byte per element; the
+ * values read back are exact in bf16.)
+ *
+ * The pool holds `layers` slabs of `num_pages` pages; a page holds `page`
+ * tokens (a multiple of 16, at most 1024) of every K/V head of one layer.  The
+ * order of bytes inside a page belongs to the library: dfl_kv4_append writes
+ * pages, dfl_kv4_read and dfl_kv4_attn read them, and pages may be copied as a
+ * whole.  All layers share one page table per sequence.  hd 64 or 128; rows,
+ * queries and outputs bf16.
+ */
+typedef struct dfl_kv4_pool {   /* host struct */
+    void* data;             /* device [layers] slabs of num_pages * dfl_kv4_page_bytes() bytes */
+    int64_t layer_stride;   /* bytes between slabs, a multiple of 16 */
+    int32_t layers, num_pages, page, Hkv, hd;
+    int32_t k_exp, v_exp;   /* -60..60 */
+} dfl_kv4_pool;
+
+/* Which pages the N sequences hold.  Host struct, device int32 arrays. */
+typedef struct dfl_pages {
+    int32_t* table;   /* [N][max_pages]: page of tokens j*page .. (j+1)*page - 1; entries past
+                         ceil(len / page) are -1 after the calls that write them */
+    int32_t* len;     /* [N] tokens held */
+    int32_t* ref;     /* [num_pages] holders of each page: its table entries, plus whatever
+                         the caller adds for holders of its own; 0: free.  (nullable for
+                         dfl_kv4_append, dfl_kv4_read and dfl_kv4_attn) */
+    int32_t N, max_pages;
+} dfl_pages;
+
+/* Bytes of one page of one layer; 0 for a page, Hkv or hd without support. */
+size_t dfl_kv4_page_bytes(int32_t page, int32_t Hkv, int32_t hd);
+
+/*
+ * dfl_kv4_append -- write context rows into pages: row n*R + i of K and V goes
+ *   to position start[n] + i of sequence n, for i < n_new[n].
+ *   pages   table (len and ref are not read)
+ *   start   in, device int32 [N]; negative: the sequence is skipped
+ *   n_new   in, device int32 [N], 0..R; rows past it are ignored
+ *   K, V    in, bf16 [N*R][Hkv][hd]
+ *   A sequence with n_new outside 0..R or positions past max_pages * page
+ *   writes nothing and records DFL_ERR_INVALID_ARG in the device error word;
+ *   so does a row whose table entry is outside 0..num_pages-1, alone.  Rows
+ *   that several sequences write into one shared page race
+ *   (dfl_pages_reserve gives each its own).
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (hd, page, sizes), MISALIGNED.
+ */
+dfl_status dfl_kv4_append(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
+                          const int32_t* start, const int32_t* n_new, int32_t R, const void* K,
+                          const void* V, dfl_stream stream);
+
+/*
+ * dfl_kv4_read -- the reverse: positions start[n] .. start[n] + count[n] - 1
+ *   of sequence n to rows n*R + i of K and V (out, bf16 [N*R][Hkv][hd]).
+ *   Other rows are left as they were, among them those that dfl_kv4_append
+ *   would skip.  Errors: as dfl_kv4_append.
+ */
+dfl_status dfl_kv4_read(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
+                        const int32_t* start, const int32_t* count, int32_t R, void* K, void* V,
+                        dfl_stream stream);
+
+/*
+ * dfl_kv4_attn -- block attention over the cache, before the output projection.
+ *   DFlare post, "Generating candidates in parallel, the target decides
+ *   acceptance" (as dfl_block_attn): for each sequence n
+ *     O = softmax(Q [Kc;Kb]^T / sqrt(hd)) [Vc;Vb]
+ *   with Kc, Vc the pages->len[n] tokens it holds (none is fine) and Kb, Vb
+ *   the block's own rows; no mask; query head h reads K/V head h / (Hq/Hkv).
+ *   Single tokens are blocks of B = 1.
+ *   Q       in, bf16 [N*B][Hq][hd]
+ *   Kb, Vb  in, bf16 [N*B][Hkv][hd]
+ *   O       out, bf16 [N*B][Hq][hd]
+ *   ws      dfl_workspace_size(DFL_OP_KV4_ATTN) bytes
+ *   fp32 sums, softmax weights rounded to 11 bits (8 for the block's own
+ *   keys); the same inputs give the same bits.  A length outside
+ *   0..max_pages*page is read as the nearest of these, a table entry outside
+ *   0..num_pages-1 as page 0, and either records DFL_ERR_INVALID_ARG in the
+ *   device error word.
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (B above 64, hd, page, sizes),
+ *   MISALIGNED, WORKSPACE.
+ */
+dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
+                        const void* Q, const void* Kb, const void* Vb, int32_t B, int32_t Hq, void* O,
+                        void* ws, size_t ws_bytes, dfl_stream stream);
+
+/*
+ * dfl_pages_reserve -- room for n_new[n] more tokens of each sequence.
+ *   Sequences are served in order; the k-th page asked for is the k-th lowest
+ *   free one (ref 0).  A last page that is partly filled and held by others too
+ *   (ref above 1 before the call) is replaced by a copy of it, in every layer,
+ *   and loses one holder.  start[n] receives the old length and len[n] grows by
+ *   n_new[n].  A sequence whose pages, with those asked for before it, exceed
+ *   the free ones is not served: start[n] = -1 and nothing of it changes.
+ *   n_new   in, device int32 [N]; start out, device int32 [N]
+ *   ws      dfl_workspace_size(DFL_OP_PAGES_RESERVE) bytes
+ *   n_new[n] below 0 or past max_pages * page in all, or a length out of range:
+ *   not served, DFL_ERR_INVALID_ARG in the device error word.
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE.
+ */
+dfl_status dfl_pages_reserve(const dfl_kv4_pool* pool, const dfl_pages* pages, const int32_t* n_new,
+                             int32_t* start, void* ws, size_t ws_bytes, dfl_stream stream);
+
+/*
+ * dfl_pages_remap -- sequence n becomes what sequence parent[n] was, cut to
+ *   keep_len[n] tokens: forks (two rows of one parent), reorderings, roll-backs
+ *   (parent[n] = n) and ends (parent[n] < 0: empty) of all sequences at once.
+ *   Tables, lengths and reference counts only: forked rows share their pages,
+ *   a page no row holds any more is free.
+ *   parent    in, device int32 [N]; >= N: the row stays as it was and
+ *             DFL_ERR_INVALID_ARG is recorded in the device error word
+ *   keep_len  in, nullable device int32 [N]; negative or above the parent's
+ *             length: all of it
+ *   ws        dfl_workspace_size(DFL_OP_PAGES_REMAP) bytes, pages = max_pages
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE.
+ */
+dfl_status dfl_pages_remap(const dfl_kv4_pool* pool, const dfl_pages* pages, const int32_t* parent,
+                           const int32_t* keep_len, void* ws, size_t ws_bytes, dfl_stream stream);
+
+/*
+ * dfl_pages_compact -- the used pages (ref above 0) to the pool's low end: of
+ *   `live` used pages, those at live and above move, in order, into the free
+ *   pages below, in every layer; table entries and reference counts follow.
+ *   map   out, device int32 [num_pages]: new index of each page that was used,
+ *         -1 for the others (for page numbers held outside the table)
+ *   live  out, device int32 [1]
+ *   ws    dfl_workspace_size(DFL_OP_PAGES_COMPACT) bytes
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE.
+ */
+dfl_status dfl_pages_compact(const dfl_kv4_pool* pool, const dfl_pages* pages, int32_t* map,
+                             int32_t* live, void* ws, size_t ws_bytes, dfl_stream stream);
+
+/* A step's paged cache.  Host struct; the tensors are device memory. */
+typedef struct dfl_paged_ctx {
+    const dfl_kv4_pool* pool;   /* layers >= args->D, Hkv and hd as the step's */
+    dfl_pages pages;            /* in/out, N as the step's, max_pages * page <= args->C */
+    int32_t R;                  /* rows per sequence of args->H this step, >= 1 */
+    const int32_t* n_new;       /* in device [N]: valid new rows of each sequence, <= R */
+    int32_t* start;             /* out device [N]: as from dfl_pages_reserve */
+} dfl_paged_ctx;
+
+/*
+ * dfl_draft_step_paged -- dfl_draft_step_cached over the paged 4-bit cache:
+ *   dfl_pages_reserve, then per layer the projections, dfl_kv4_append and
+ *   dfl_kv4_attn, the rest as dfl_draft_step.  Lengths always advance.  A
+ *   sequence that could not be served (start[n] = -1) drafts over the tokens
+ *   it holds; its new rows are dropped.  bf16 only, args->C at least
+ *   max_pages * page with args->rope holding C+B positions, B at most 64.
+ *   ws: dfl_workspace_size(DFL_OP_DRAFT_STEP_PAGED) bytes.
+ *   Errors: as dfl_draft_step_cached and the calls it makes.
+ */
+dfl_status dfl_draft_step_paged(const dfl_step_args* args, const dfl_paged_ctx* ctx, void* ws,
+                                size_t ws_bytes, dfl_stream stream);
 
 /* Synchronise `stream`, then read and clear this device's error word (DFL_OK
  * if no kernel recorded an error). */
