@@ -17,7 +17,7 @@ LIB = os.path.join(OUT_DIR, "libdfl.so")
 CHECK_DIR = os.path.join(OUT_DIR, "check")
 LIB_CHECK = os.path.join(CHECK_DIR, "libdfl_check.so")
 SOURCES = ["api.cu", "mix_rmsnorm.cu", "gemm_tc.cu", "block_attn.cu", "block_attn_tc.cu", "small_kernels.cu", "self_select.cu",
-           "accept_ext.cu", "kv4_cache.cu", "kv4_attn.cu", "pages.cu", "api_paged.cu"]
+           "accept_ext.cu", "kv4_cache.cu", "kv4_attn.cu", "kv4_attn_tc.cu", "pages.cu", "api_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

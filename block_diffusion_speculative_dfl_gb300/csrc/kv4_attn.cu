@@ -36,96 +36,16 @@
 // bf16 products, which take their range.  Maxima are per row; O is rescaled
 // only when a maximum grows by more than 2^8.
 #include "internal.h"
-#include "kv4.cuh"
+#include "kv4_attn.cuh"
 #include "paged.h"
 
 namespace dfl {
 
 namespace {
 
-constexpr int KA_UNIT = 64;        // keys per unit
 constexpr int KA_WARPS = 4;        // one cell of 16 keys per warp and unit
 constexpr int KA_THREADS = KA_WARPS * 32;
 constexpr int KA_SLOTS = 4;        // cells in flight per warp
-constexpr float KA_LAZY = 8.f;     // rescale when a maximum grows by more (log2)
-constexpr float KA_LIFT = 7.f;     // P is 2^7 above its nominal value
-
-struct KaArgs {
-    Kv4Slab slab;
-    const int32_t* table;
-    const int32_t* len;
-    int max_pages;
-    int N, B, Hq, G, R;
-    int subs;                 // row tiles per K/V head
-    int HS;                   // Hkv * subs
-    const __nv_bfloat16* Q;   // [N*B][Hq][hd]
-    const __nv_bfloat16* Kb;  // [N*B][Hkv][hd]
-    const __nv_bfloat16* Vb;
-    __nv_bfloat16* O;         // [N*B][Hq][hd]
-    float* Opart;             // [2 * grid][rows][hd]
-    float2* ml;               // [2 * grid][rows] (maximum in log2 units, sum)
-    float scale_log2;         // log2(e) / sqrt(hd)
-    float k_pow2, v_pow2, v_inv;   // 2^k_exp, 2^v_exp, 2^-v_exp
-};
-
-__device__ __forceinline__ int ka_len(const KaArgs& a, int n, const DevErr& err) {
-    const int l = a.len[n], cap = a.max_pages * a.slab.page;
-    if (l >= 0 && l <= cap) return l;
-    record_error(err, DFL_ERR_INVALID_ARG);
-    return min(max(l, 0), cap);
-}
-
-__device__ __forceinline__ int ka_units(int len) { return (len + KA_UNIT - 1) / KA_UNIT + 1; }
-
-// The line of units and where position x falls on it.
-struct KaLine {
-    int total, per;     // units in all, per CTA
-    int n, before;      // sequence that holds x, units of the line before it
-};
-
-struct KaLineSmem {
-    int red[KA_THREADS / 32];
-    int n, before;
-};
-
-// per: units per CTA for a grid of gridDim.x; x = at(per, total), located when
-// 0 <= x < total.
-template <typename At>
-__device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int grid, KaLineSmem& sm, const DevErr& err, At at) {
-    const int chunk = (a.N + KA_THREADS - 1) / KA_THREADS;
-    const int n0 = min(a.N, (int)threadIdx.x * chunk), n1 = min(a.N, n0 + chunk);
-    int sum = 0;
-    for (int n = n0; n < n1; ++n) sum += ka_units(ka_len(a, n, err));
-    sum *= a.HS;
-    KaLine l;
-    const int pre = block_exscan<KA_THREADS>(sum, sm.red, &l.total);
-    l.per = max(1, (l.total + grid - 1) / grid);
-    const int x = at(l.per, l.total);
-    if (x >= pre && x < pre + sum) {
-        int p = pre;
-        for (int n = n0; n < n1; ++n) {
-            const int w = ka_units(ka_len(a, n, err)) * a.HS;
-            if (x < p + w) { sm.n = n; sm.before = p; break; }
-            p += w;
-        }
-    }
-    __syncthreads();
-    l.n = sm.n;
-    l.before = sm.before;
-    return l;
-}
-
-// A position on the line as (sequence, head and row tile, unit).
-struct KaPos {
-    int n, hs, u, nu, len;
-    __device__ __forceinline__ void next_triple(const KaArgs& a, const DevErr& err) {
-        u = 0;
-        if (++hs == a.HS) {
-            hs = 0;
-            if (++n < a.N) { len = ka_len(a, n, err); nu = ka_units(len); }
-        }
-    }
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -217,7 +137,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     using Cell = Kv4Cell<HD>;
     constexpr int KW = HD / 32;          // words of a lane's quarter of a K row (codes)
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ KaLineSmem line_sm;
+    __shared__ KaLineSmem<KA_THREADS> line_sm;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * KA_SLOTS * Cfg::CELL;
     float* merge = reinterpret_cast<float*>(sm + Cfg::RING);
@@ -230,7 +150,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     __syncwarp();
     grid_dep_begin();
 
-    const KaLine line = ka_locate(a, gridDim.x, line_sm, err, [&](int per, int total) {
+    const KaLine line = ka_locate<KA_THREADS>(a, gridDim.x, line_sm, err, [&](int per, int total) {
         const int64_t x = (int64_t)blockIdx.x * per;
         return x < total ? (int)x : -1;
     });
@@ -571,54 +491,12 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     for (; taken < issued; ++taken) mbar_wait(&full[taken % KA_SLOTS], (taken / KA_SLOTS) & 1, err);
 }
 
-// Adds up the triple that starts in CTA blockIdx.x's range and ends past it:
-// partials of that CTA (its last) and of the following CTAs (their first), in
-// the order of the keys.
-template <int HD, int ROWS>
-__global__ void __launch_bounds__(KA_THREADS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
-    __shared__ KaLineSmem line_sm;
-    grid_dep_begin();
-    const KaLine line = ka_locate(a, gridDim.x, line_sm, err, [&](int per, int total) {
-        const int64_t end = ((int64_t)blockIdx.x + 1) * per;   // a triple crosses the border before `end`
-        return end < total ? (int)end : -1;
-    });
-    const int64_t endl = ((int64_t)blockIdx.x + 1) * line.per;
-    if (endl >= line.total) return;
-    const int end = (int)endl;
-    const int nu = ka_units(ka_len(a, line.n, err));
-    const int hs = (end - line.before) / nu;
-    const int p0 = line.before + hs * nu, p1 = p0 + nu;   // the triple holding unit `end`
-    if (p0 == end || p0 < end - line.per) return;          // none crosses, or it started before this CTA
-    const int first = blockIdx.x, last = (p1 - 1) / line.per;
-    const int head = hs / a.subs, row0 = (hs - head * a.subs) * ROWS;
-    constexpr int TPR = HD / 4;
-    for (int row = threadIdx.x / TPR; row < ROWS; row += KA_THREADS / TPR) {
-        const int r = row0 + row, c = (threadIdx.x % TPR) * 4;
-        if (r >= a.R) break;
-        float M = -INFINITY, L = 0.f;
-        for (int j = first; j <= last; ++j) M = fmaxf(M, a.ml[(2 * j + (j == first)) * ROWS + row].x);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        #pragma unroll 4
-        for (int j = first; j <= last; ++j) {
-            const int64_t at = (int64_t)(2 * j + (j == first)) * ROWS + row;
-            const float2 ml = a.ml[at];
-            const float4 v = *reinterpret_cast<const float4*>(a.Opart + at * HD + c);
-            const float f = ml.x == -INFINITY ? 0.f : ex2_ftz(ml.x - M);
-            L += f * ml.y;
-            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
-        }
-        const float inv = a.v_pow2 / L;
-        const int64_t at = ((int64_t)(line.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + c;
-        if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
-            *reinterpret_cast<uint2*>(a.O + at) =
-                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    }
-}
-
 constexpr int KA_SMS = 152;   // SMs of a GB300
 
-// Row tiles of 8 query rows when a group has at most 8, else of 16: a wider
-// tile expands each key for more rows at once.
+// Row tiles of 8 query rows when a group has at most 8, of 16 up to 16: a wider
+// tile expands each key for more rows at once.  More rows go to the
+// tensor-memory kernel.
+constexpr int KA_MAX_ROWS = 16;
 int ka_nt(int R) { return R <= 8 ? 1 : 2; }
 
 // CTAs of the launch: every SM full, or one per unit when there are fewer.
@@ -630,7 +508,8 @@ inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
     if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
-    const int nt = ka_nt(B * (Hq / Hkv));
+    const int R = B * (Hq / Hkv), nt = ka_nt(R);
+    if (R > KA_MAX_ROWS) return kv4_attn_tc_ws_bytes(R, hd);
     const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * 8 * nt;
     return al256(parts * hd * 4) + al256(parts * 8);
 }
@@ -638,24 +517,27 @@ size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
                         const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st) {
     const int G = Hq / pool.Hkv, R = B * G, nt = ka_nt(R);
+    const bool tc = R > KA_MAX_ROWS;
+    const int rows = tc ? kv4_attn_tc_rows(R) : 8 * nt;
     KaArgs a{};
     a.slab = kv4_slab(pool, layer);
     a.table = pg.table; a.len = pg.len; a.max_pages = pg.max_pages;
     a.N = pg.N; a.B = B; a.Hq = Hq; a.G = G; a.R = R;
-    a.subs = (R + 8 * nt - 1) / (8 * nt);
+    a.subs = (R + rows - 1) / rows;
     a.HS = pool.Hkv * a.subs;
     a.Q = static_cast<const __nv_bfloat16*>(Q);
     a.Kb = static_cast<const __nv_bfloat16*>(Kb);
     a.Vb = static_cast<const __nv_bfloat16*>(Vb);
     a.O = static_cast<__nv_bfloat16*>(O);
-    const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * 8 * nt;
-    a.Opart = static_cast<float*>(ws);
-    a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)pool.hd);
     a.k_pow2 = kv4_exp2i(pool.k_exp); a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
-    const int64_t cap_units = (int64_t)pg.max_pages * pool.page / KA_UNIT + 2;
-    if (cap_units * pg.N * a.HS >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;
-    const int grid = ka_grid(cap_units * pg.N * a.HS, nt);
+    const int64_t units = ((int64_t)pg.max_pages * pool.page / KA_UNIT + 2) * pg.N * a.HS;
+    if (units >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, st);
+    const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * rows;
+    a.Opart = static_cast<float*>(ws);
+    a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
+    const int grid = ka_grid(units, nt);
     const DevErr err = dev_err(ctx);
     auto run = [&](auto kern, auto join, int smem, int slot) -> dfl_status {
         if (!ctx->kv4_attr_set[slot]) {
@@ -669,7 +551,7 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
             if (rc != DFL_OK) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
-        return launch_pdl(join, grid, KA_THREADS, 0, st, a, err);
+        return launch_pdl(join, dim3(grid, rows / KJ_ROWS), pool.hd / 4 * KJ_ROWS, 0, st, a, err);
     };
     if (pool.hd == 128)
         return nt == 1 ? run(kv4_attn_kernel<128, 1>, kv4_attn_join_kernel<128, 8>, KaCfg<128, 1>::SMEM, 0)
