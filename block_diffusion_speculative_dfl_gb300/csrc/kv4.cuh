@@ -118,15 +118,16 @@ __device__ __forceinline__ T block_exscan(T v, T* red, T* sum) {
     }
     if (lane == 31) red[warp] = inc;
     __syncthreads();
-    T before = 0, all = 0;
+    T all = lane < W ? red[lane] : 0;   // every warp sums the warps' totals
+    const T own = all;
     #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const T x = red[w];
-        if (w < warp) before += x;
-        all += x;
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(0xFFFFFFFFu, all, o);
+        if (lane >= o) all += u;
     }
+    const T before = __shfl_sync(0xFFFFFFFFu, all - own, warp);
+    *sum = __shfl_sync(0xFFFFFFFFu, all, W - 1);
     __syncthreads();
-    *sum = all;
     return before + inc - v;
 }
 

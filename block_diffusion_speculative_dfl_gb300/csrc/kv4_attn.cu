@@ -43,6 +43,7 @@ namespace dfl {
 
 namespace {
 
+constexpr int KA_UNIT = 64;        // keys per unit
 constexpr int KA_WARPS = 4;        // one cell of 16 keys per warp and unit
 constexpr int KA_THREADS = KA_WARPS * 32;
 constexpr int KA_SLOTS = 4;        // cells in flight per warp
@@ -137,7 +138,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     using Cell = Kv4Cell<HD>;
     constexpr int KW = HD / 32;          // words of a lane's quarter of a K row (codes)
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ KaLineSmem<KA_THREADS> line_sm;
+    __shared__ KaLineSmem<KA_THREADS, 1> line_sm;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * KA_SLOTS * Cfg::CELL;
     float* merge = reinterpret_cast<float*>(sm + Cfg::RING);
@@ -150,7 +151,8 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     __syncwarp();
     grid_dep_begin();
 
-    const KaLine line = ka_locate<KA_THREADS>(a, gridDim.x, line_sm, err, [&](int per, int total) {
+    ka_check_lengths<KA_THREADS>(a, err);
+    const KaLine line = ka_locate<KA_THREADS, 1>(a, gridDim.x, line_sm, [&](int, int per, int total) {
         const int64_t x = (int64_t)blockIdx.x * per;
         return x < total ? (int)x : -1;
     });
@@ -159,11 +161,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     const int x0 = (int)x0l, x1 = min(line.total - x0, line.per) + x0;
 
     KaPos pos;   // the triple being computed
-    pos.n = line.n;
-    pos.len = ka_len(a, pos.n, err);
-    pos.nu = ka_units(pos.len);
-    pos.hs = (x0 - line.before) / pos.nu;
-    pos.u = (x0 - line.before) - pos.hs * pos.nu;
+    pos.set(a, line_sm.at[0], x0);
 
     // Producer: walks the same units ahead of the computation.  Lane i holds
     // the pool cell of this warp's tokens in unit pbase + i.
@@ -177,29 +175,24 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
             const int key = pp.u * KA_UNIT + warp * KV4_CELL_TOKENS;
             if (key >= pp.len) {   // past the context (the block's own unit, or a short last unit): next unit
                 --pleft;
-                if (++pp.u == pp.nu) pp.next_triple(a, err);
+                if (++pp.u == pp.nu) pp.next_triple(a);
                 pbase = -1;
                 continue;
             }
             if (pbase < 0 || pp.u >= pbase + 32) {
                 pbase = pp.u;
                 const int k = (pbase + lane) * KA_UNIT + warp * KV4_CELL_TOKENS;
-                if (k < pp.len) {
-                    const int j = k / a.slab.page, in = k - j * a.slab.page;
-                    int p = a.table[(int64_t)pp.n * a.max_pages + j];
-                    if (p < 0 || p >= a.slab.num_pages) { record_error(err, DFL_ERR_INVALID_ARG); p = 0; }
-                    pcell = (p * a.slab.Hkv + pp.hs / a.subs) * a.slab.cells + in / KV4_CELL_TOKENS;
-                }
+                if (k < pp.len) pcell = ka_cell(a, pp.n, pp.head, k, err);
             }
             const int cell = __shfl_sync(0xFFFFFFFFu, pcell, pp.u - pbase);
-            if (lane == 0) {
+            if (elect_one()) {
                 const int s = issued % KA_SLOTS;
                 mbar_arrive_expect_tx(&full[s], Cfg::CELL);
                 bulk_g2s(ring + s * Cfg::CELL, a.slab.data + (int64_t)cell * Cfg::CELL, Cfg::CELL, &full[s]);
             }
             ++issued;
             --pleft;
-            if (++pp.u == pp.nu) pp.next_triple(a, err);   // cannot happen: the last unit is the block's own
+            if (++pp.u == pp.nu) pp.next_triple(a);   // cannot happen: the last unit is the block's own
             return;
         }
     };
@@ -209,7 +202,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     int x = x0;
     #pragma unroll 1
     while (x < x1) {
-        const int head = pos.hs / a.subs, row0 = (pos.hs - head * a.subs) * Cfg::ROWS;
+        const int head = pos.head, row0 = pos.tile * Cfg::ROWS;
         const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
         // ---- Q of this triple: lane (g, t) holds row g's quarter t of each 8-row tile
         uint32_t q[NT][2 * Cfg::KSTEPS];
@@ -219,7 +212,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
             const int r = row0 + nt * 8 + g;
             uint32_t mx = 0;
             const uint4* src = reinterpret_cast<const uint4*>(
-                a.Q + ((int64_t)(pos.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + t * (HD / 4));
+                a.Q + ka_row(a, pos.n, head, r, HD) + t * (HD / 4));
             #pragma unroll
             for (int i = 0; i < HD / 32; ++i) {
                 const uint4 w = r < a.R ? src[i] : make_uint4(0, 0, 0, 0);
@@ -394,7 +387,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
                 for (int nt = 0; nt < NT; ++nt) {
                     const int r = row0 + nt * 8 + g;
                     const uint4 qw = r < a.R ? reinterpret_cast<const uint4*>(
-                        a.Q + ((int64_t)(pos.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + t * (HD / 4))[i] : z;
+                        a.Q + ka_row(a, pos.n, head, r, HD) + t * (HD / 4))[i] : z;
                     mma_b16(s[nt], f0, qw.x, qw.y);
                     mma_b16(s[nt], f1, qw.z, qw.w);
                 }
@@ -468,8 +461,8 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
                     o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                 }
                 if (whole) {
-                    const float inv = a.v_pow2 / L;
-                    const int64_t at = ((int64_t)(pos.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + c;
+                    const float inv = __fdividef(a.v_pow2, L);
+                    const int64_t at = ka_row(a, pos.n, head, r, HD) + c;
                     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
                         *reinterpret_cast<uint2*>(a.O + at) =
                             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
@@ -485,7 +478,7 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
         __syncthreads();
         x += u1 - u0;
         pos.u = u1;
-        if (u1 == pos.nu) pos.next_triple(a, err);
+        if (u1 == pos.nu) pos.next_triple(a);
     }
     // After a wait that ran out: let the copies in flight land before the CTA's shared memory goes.
     for (; taken < issued; ++taken) mbar_wait(&full[taken % KA_SLOTS], (taken / KA_SLOTS) & 1, err);
@@ -525,13 +518,18 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.N = pg.N; a.B = B; a.Hq = Hq; a.G = G; a.R = R;
     a.subs = (R + rows - 1) / rows;
     a.HS = pool.Hkv * a.subs;
+    a.g_inv = (((uint64_t)1 << 40) + G - 1) / G;
+    a.cells_inv = (((uint64_t)1 << 36) + a.slab.cells - 1) / a.slab.cells;
     a.Q = static_cast<const __nv_bfloat16*>(Q);
     a.Kb = static_cast<const __nv_bfloat16*>(Kb);
     a.Vb = static_cast<const __nv_bfloat16*>(Vb);
     a.O = static_cast<__nv_bfloat16*>(O);
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)pool.hd);
-    a.k_pow2 = kv4_exp2i(pool.k_exp); a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
-    const int64_t units = ((int64_t)pg.max_pages * pool.page / KA_UNIT + 2) * pg.N * a.HS;
+    a.k_pow2 = kv4_exp2i(pool.k_exp); a.k_inv = kv4_exp2i(-pool.k_exp);
+    a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
+    a.unit_log2 = tc ? kv4_attn_tc_unit_log2(R, pool.hd) : 6;   // KA_UNIT
+    static_assert(KA_UNIT == 64, "unit_log2");
+    const int64_t units = (((int64_t)pg.max_pages * pool.page >> a.unit_log2) + 2) * pg.N * a.HS;
     if (units >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, st);
     const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * rows;

@@ -16,6 +16,9 @@ struct KaArgs {
     int N, B, Hq, G, R;
     int subs;                 // row tiles per K/V head
     int HS;                   // Hkv * subs
+    int unit_log2;            // keys per unit
+    uint64_t g_inv;           // ceil(2^40 / G)
+    uint64_t cells_inv;       // ceil(2^36 / cells of a page)
     const __nv_bfloat16* Q;   // [N*B][Hq][hd]
     const __nv_bfloat16* Kb;  // [N*B][Hkv][hd]
     const __nv_bfloat16* Vb;
@@ -23,77 +26,149 @@ struct KaArgs {
     float* Opart;             // [2 * grid][rows][hd]
     float2* ml;               // [2 * grid][rows] (maximum in log2 units, sum)
     float scale_log2;         // log2(e) / sqrt(hd)
-    float k_pow2, v_pow2, v_inv;   // 2^k_exp, 2^v_exp, 2^-v_exp
+    float k_pow2, k_inv, v_pow2, v_inv;   // 2^k_exp, 2^-k_exp, 2^v_exp, 2^-v_exp
 };
 
 // The tensor-memory kernel (kv4_attn_tc.cu): rows of its triples, scratch, launch
 // (a complete but for Opart and ml; `units` an upper bound on the line).
 inline int kv4_attn_tc_rows(int R) { return R <= 64 ? 64 : 128; }
+int kv4_attn_tc_unit_log2(int R, int hd);
 size_t kv4_attn_tc_ws_bytes(int R, int hd);
 dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, cudaStream_t st);
 
 namespace {
 
-constexpr int KA_UNIT = 64;        // keys per unit
 constexpr float KA_LAZY = 8.f;     // rescale when a maximum grows by more (log2)
 constexpr float KA_LIFT = 7.f;     // P is 2^7 above its nominal value
 
-__device__ __forceinline__ int ka_len(const KaArgs& a, int n, const DevErr& err) {
-    const int l = a.len[n], cap = a.max_pages * a.slab.page;
-    if (l >= 0 && l <= cap) return l;
-    record_error(err, DFL_ERR_INVALID_ARG);
-    return min(max(l, 0), cap);
+// One lane of a converged warp.  What it issues (copies, products) has operands
+// the compiler knows to be uniform, at half the clocks of a lane in a divergent
+// branch.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
-__device__ __forceinline__ int ka_units(int len) { return (len + KA_UNIT - 1) / KA_UNIT + 1; }
+// Two of the block's own bf16 elements in units of the pool's power of two
+// (inv: its inverse), as fp16.  bf16's 8 bits survive from 2^-14 of the unit
+// up; finite values past fp16's range become its largest, as the cache's
+// become its own.
+__device__ __forceinline__ uint32_t block_half2(uint32_t w, float inv) {
+    float x[2] = {bf16lo(w) * inv, bf16hi(w) * inv};
+    #pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (fabsf(x[i]) > 65504.f && fabsf(x[i]) < INFINITY) x[i] = copysignf(65504.f, x[i]);
+    const __half2 h = __floats2half2_rn(x[0], x[1]);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 
-// The line of units and where position x falls on it.
+// Block row and head of query row r of a group: element offset of its Q and O.
+__device__ __forceinline__ int64_t ka_row(const KaArgs& a, int n, int head, int r, int hd) {
+    const int b = (int)(((uint64_t)(uint32_t)r * a.g_inv) >> 40);   // r / G: r G < 2^40
+    return ((int64_t)(n * a.B + b) * a.Hq + head * a.G + (r - b * a.G)) * hd;
+}
+
+// Pool cell of token k (a multiple of 16) of sequence n for a K/V head; a page
+// out of range is recorded and read as page 0.
+__device__ __forceinline__ int ka_cell(const KaArgs& a, int n, int head, int k, const DevErr& err) {
+    const uint32_t t = (uint32_t)k / KV4_CELL_TOKENS;
+    const int j = (int)((t * a.cells_inv) >> 36);                   // t / cells: t cells < 2^36
+    int p = a.table[(int64_t)n * a.max_pages + j];
+    if (p < 0 || p >= a.slab.num_pages) { record_error(err, DFL_ERR_INVALID_ARG); p = 0; }
+    return (p * a.slab.Hkv + head) * a.slab.cells + (int)t - j * a.slab.cells;
+}
+
+// Length of sequence n; one out of range is read as the nearest in range.
+__device__ __forceinline__ int ka_len(const KaArgs& a, int n) { return min(max(a.len[n], 0), a.max_pages * a.slab.page); }
+
+// Lengths out of range, recorded by the grid's first block.
+template <int THREADS>
+__device__ __forceinline__ void ka_check_lengths(const KaArgs& a, const DevErr& err) {
+    if (blockIdx.x != 0) return;
+    #pragma unroll 1
+    for (int n = threadIdx.x; n < a.N; n += THREADS)
+        if (a.len[n] != ka_len(a, n)) record_error(err, DFL_ERR_INVALID_ARG);
+}
+
+// Units of a sequence: its tokens, then the block's own keys.
+__device__ __forceinline__ int ka_units(const KaArgs& a, int len) { return ((len + (1 << a.unit_log2) - 1) >> a.unit_log2) + 1; }
+
+// The line of units, cut into ranges of `per`, and where positions on it fall.
 struct KaLine {
     int total, per;     // units in all, per range
-    int n, before;      // sequence that holds x, units of the line before it
 };
 
-template <int THREADS>
+// Found by ka_locate: the sequence that holds a position, the units of the
+// line before it, its length.
+struct KaFound {
+    int n, before, len, next;
+};
+
+template <int THREADS, int P>
 struct KaLineSmem {
     int red[THREADS / 32];
-    int n, before;
+    KaFound at[P];
 };
 
-// The line cut into `ranges`; x = at(per, total) is located when 0 <= x < total.
-// All threads of the block call.
-template <int THREADS, typename At>
-__device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineSmem<THREADS>& sm, const DevErr& err, At at) {
+// The line cut into `ranges`; of the P positions at(i, per, total), those in
+// 0 .. total - 1 are located in sm.at[i].  All threads of the block call; one
+// read of the lengths when there are no more sequences than threads.
+template <int THREADS, int P, typename At>
+__device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineSmem<THREADS, P>& sm, At at) {
     const int chunk = (a.N + THREADS - 1) / THREADS;
     const int n0 = min(a.N, (int)threadIdx.x * chunk), n1 = min(a.N, n0 + chunk);
-    int sum = 0;
-    for (int n = n0; n < n1; ++n) sum += ka_units(ka_len(a, n, err));
+    const int len0 = n0 < n1 ? ka_len(a, n0) : 0, len1 = n0 + 1 < a.N ? ka_len(a, n0 + 1) : 0;
+    int sum = n0 < n1 ? ka_units(a, len0) : 0;
+    #pragma unroll 1
+    for (int n = n0 + 1; n < n1; ++n) sum += ka_units(a, ka_len(a, n));
     sum *= a.HS;
     KaLine l;
     const int pre = block_exscan<THREADS>(sum, sm.red, &l.total);
     l.per = max(1, (l.total + ranges - 1) / ranges);
-    const int x = at(l.per, l.total);
-    if (x >= pre && x < pre + sum) {
-        int p = pre;
-        for (int n = n0; n < n1; ++n) {
-            const int w = ka_units(ka_len(a, n, err)) * a.HS;
-            if (x < p + w) { sm.n = n; sm.before = p; break; }
+    #pragma unroll 1
+    for (int i = 0; i < P; ++i) {
+        const int x = at(i, l.per, l.total);
+        if (x < pre || x >= pre + sum) continue;
+        int p = pre, len = len0, next = len1;
+        #pragma unroll 1
+        for (int n = n0; ; ++n) {
+            const int w = ka_units(a, len) * a.HS;
+            if (x < p + w) { sm.at[i] = KaFound{n, p, len, next}; break; }
             p += w;
+            len = next;
+            next = n + 2 < a.N ? ka_len(a, n + 2) : 0;
         }
     }
     __syncthreads();
-    l.n = sm.n;
-    l.before = sm.before;
     return l;
 }
 
-// A position on the line as (sequence, head and row tile, unit).
+// A position on the line as (sequence, head and row tile, unit).  The next
+// sequence's length is read ahead.
 struct KaPos {
-    int n, hs, u, nu, len;
-    __device__ __forceinline__ void next_triple(const KaArgs& a, const DevErr& err) {
+    int n, hs, head, tile, u, nu, len, next;
+    // Position x of the line, which ka_locate found.
+    __device__ __forceinline__ void set(const KaArgs& a, const KaFound& f, int x) {
+        n = f.n;
+        len = f.len;
+        next = f.next;
+        nu = ka_units(a, len);
+        hs = (x - f.before) / nu;
+        u = x - f.before - hs * nu;
+        head = hs / a.subs;
+        tile = hs - head * a.subs;
+    }
+    __device__ __forceinline__ void next_triple(const KaArgs& a) {
         u = 0;
-        if (++hs == a.HS) {
-            hs = 0;
-            if (++n < a.N) { len = ka_len(a, n, err); nu = ka_units(len); }
+        ++hs;
+        if (++tile == a.subs) { tile = 0; ++head; }
+        if (hs == a.HS) {
+            hs = head = 0;
+            ++n;
+            len = next;
+            nu = ka_units(a, len);
+            next = n + 1 < a.N ? ka_len(a, n + 1) : 0;
         }
     }
 };
@@ -105,24 +180,26 @@ constexpr int KJ_ROWS = 8;
 template <int HD, int ROWS>
 __global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
     constexpr int TPR = HD / 4, THREADS = TPR * KJ_ROWS;
-    __shared__ KaLineSmem<THREADS> line_sm;
+    __shared__ KaLineSmem<THREADS, 1> line_sm;
     grid_dep_begin();
-    const KaLine line = ka_locate<THREADS>(a, gridDim.x, line_sm, err, [&](int per, int total) {
+    const KaLine line = ka_locate<THREADS, 1>(a, gridDim.x, line_sm, [&](int, int per, int total) {
         const int64_t end = ((int64_t)blockIdx.x + 1) * per;   // a triple crosses the border before `end`
         return end < total ? (int)end : -1;
     });
     const int64_t endl = ((int64_t)blockIdx.x + 1) * line.per;
     if (endl >= line.total) return;
     const int end = (int)endl;
-    const int nu = ka_units(ka_len(a, line.n, err));
-    const int hs = (end - line.before) / nu;
-    const int p0 = line.before + hs * nu, p1 = p0 + nu;   // the triple holding unit `end`
+    const KaFound f = line_sm.at[0];
+    const int nu = ka_units(a, f.len);
+    const int hs = (end - f.before) / nu;
+    const int p0 = f.before + hs * nu, p1 = p0 + nu;   // the triple holding unit `end`
     if (p0 == end || p0 < end - line.per) return;          // none crosses, or it started before this CTA
     const int first = blockIdx.x, last = (p1 - 1) / line.per;
     const int head = hs / a.subs, row0 = (hs - head * a.subs) * ROWS;
     const int row = blockIdx.y * KJ_ROWS + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;
     if (row >= ROWS || r >= a.R) return;
     float M = -INFINITY, L = 0.f;
+    #pragma unroll 4
     for (int j = first; j <= last; ++j) M = fmaxf(M, a.ml[(2 * j + (j == first)) * ROWS + row].x);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     #pragma unroll 4
@@ -134,8 +211,8 @@ __global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const K
         L += f * ml.y;
         o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
     }
-    const float inv = a.v_pow2 / L;
-    const int64_t at = ((int64_t)(line.n * a.B + r / a.G) * a.Hq + head * a.G + r % a.G) * HD + c;
+    const float inv = __fdividef(a.v_pow2, L);
+    const int64_t at = ka_row(a, f.n, head, r, HD) + c;
     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
         *reinterpret_cast<uint2*>(a.O + at) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));

@@ -3,25 +3,29 @@
 // units as kv4_attn.cu, with up to 128 rows to a triple, where products and
 // exponentials, not bytes, are most of the work.
 //
-// One CTA per SM, two pipelines of ten warps, each with a range of the line of
+// One CTA per SM, two pipelines of eight warps, each with a range of the line of
 // its own, so that one pipeline's products run under the other's exponentials:
-//   producer (1 warp)   bulk copies of a unit's cells (4-bit) into a ring;
-//   expanders (4 warps) one cell each: codes * scales in fp16 into a K tile
-//                       and a V tile [64 keys][hd] with 128-byte swizzle; the
-//                       block's own keys come as bf16 straight from memory;
-//   issuer (1 thread)   S = Q K^T (M = 64 or 128 rows, N = 64), then
-//                       O += P V (N = hd); Q and P are A operands in tensor
-//                       memory, so the products read only K and V tiles from
-//                       shared memory;
-//   softmax (4 warps)   Q into tensor memory (fp16, and bf16 for the block's
-//                       own unit), running maximum and sum, P over S's
-//                       columns, the triple's output.
-// What bounds it: a unit's tiles (hd = 128) are 32 KB written by the expanders
-// and read by the products, with 18 KB of codes in and out: 650 clocks of
-// shared memory at 128 B per clock, against 390 of HBM at its measured rate.
-// 256 tensor-memory columns per pipeline: S (64), Q (hd / 2), O (hd); at
-// hd = 128 a second S buffer has no room, so S of a unit follows P V of the
-// one before, and the other pipeline fills the gap.
+//   expanders (4 warps) two for K, two for V, half of a unit's tokens each: bulk
+//                       copies of half cells into a ring of the warp's own,
+//                       then codes * scales in fp16 into a tile [keys][hd] with
+//                       128-byte swizzle; the block's own rows come straight
+//                       from memory;
+//   softmax (4 warps)   Q as fp16 into shared memory, running maximum and sum,
+//                       P over S's columns, the triple's output.  The first of
+//                       them issues the products: S = Q K^T (M = 64 or 128
+//                       rows, N = keys) and O += P V (N = hd, P from tensor
+//                       memory).
+// The issuing warp has nothing else to do between its P and the next S, which
+// needs that P V to have read S's columns; a warp of its own would take the
+// fifth place on its scheduler and with it 32 registers from every thread.
+//
+// What bounds it: the turns between the roles.  The bare chain of waits,
+// commits and issues of a unit takes about 1,000 clocks with nothing else in
+// it, so a unit is 128 keys where shared and tensor memory allow (64 at
+// hd = 128 with 128 rows); expansion and softmax of 64 keys by 64 rows are
+// about 2,300 warp instructions, 575 clocks of the four schedulers; the tiles
+// (hd = 128) are 32 KB per 64 keys written and read beside Q, 700 clocks of
+// shared memory at 128 B per clock, against 390 of HBM for the 9 KB of codes.
 #include "internal.h"
 #include "kv4_attn.cuh"
 #include "paged.h"
@@ -31,28 +35,34 @@ namespace dfl {
 namespace {
 
 constexpr int KT_PIPES = 2;
-constexpr int KT_WARPS = KT_PIPES * 8 + 4;     // softmax, expanders; producers and issuers
+constexpr int KT_WARPS = KT_PIPES * 8;         // softmax, expanders
 constexpr int KT_THREADS = KT_WARPS * 32;
+
+// Keys per unit.
+constexpr int kt_unit(int hd, int mm) { return hd == 128 && mm == 128 ? 64 : 128; }
 
 template <int HD, int MM>
 struct KtCfg {
+    static constexpr int KU = kt_unit(HD, MM);
     static constexpr int KB = HD / 64;                  // 128-byte blocks of a tile row
-    static constexpr int TKB = 64 * 128;                // bytes of one such block of a tile
+    static constexpr int TKB = KU * 128;                // bytes of one such block of a K or V tile
+    static constexpr int QKB = MM * 128;                // of Q
     static constexpr int TILE = KB * TKB;
+    static constexpr int Q = KB * QKB;
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
-    static constexpr int RAW = 4 * CELL;                // a unit's cells
-    static constexpr int RST = 4, KST = 2, VST = 2;     // slots per pipeline
-    static constexpr int PIPE = (KST + VST) * TILE + RST * RAW;
-    static constexpr int S_COL = 0, Q_COL = 64, O_COL = 128, COLS = 256;
+    // slots per pipeline: 32 tokens of codes per expander, K tiles, V tiles
+    static constexpr int RST = HD == 128 ? 3 : 4, KST = HD == 64 ? 2 : 1, VST = KST;
+    static constexpr int PIPE = Q + (KST + VST) * TILE + RST * 4 * CELL;
+    static constexpr int S_COL = 0, O_COL = 128, COLS = 256;
     static constexpr int SMEM = 1024 + KT_PIPES * PIPE;
-    static_assert(O_COL + HD <= COLS && Q_COL + HD / 2 <= O_COL, "tensor memory columns");
-    static_assert(SMEM <= 226 * 1024, "shared memory");
+    static_assert(KU <= O_COL && O_COL + HD <= COLS, "tensor memory columns");
+    static_assert(SMEM <= 225 * 1024, "shared memory");
     static_assert(PIPE % 1024 == 0, "tiles start on 1024-byte boundaries");
 };
 
 template <int RST, int KST, int VST>
 struct KtBars {
-    uint64_t raw_full[RST], raw_empty[RST];
+    uint64_t raw_full[4][RST];   // of each expander
     uint64_t k_full[KST], k_empty[KST];
     uint64_t v_full[VST], v_empty[VST];
     uint64_t q_full, s_full, p_full, pv_done, o_empty, drain;
@@ -62,21 +72,19 @@ __host__ __device__ constexpr uint32_t kt_idesc_f16(int M, int N) {   // fp16 A 
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Wait as mbar_wait, and give up when another role of the CTA has.
+// Wait as mbar_wait, and give up when another role of the CTA has.  Few
+// instructions: the roles' waits are a good part of the kernel's code, and its
+// loops barely fit the instruction cache.
 __device__ __forceinline__ bool kt_wait(uint64_t* bar, uint32_t parity, const DevErr& e, volatile int* abort) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    while (true) {
-        #pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > e.limit_ns) {
-            record_error(e, DFL_ERR_TIMEOUT);
-            *abort = 1;
-            return false;
-        }
-    }
+    #pragma unroll 1
+    do {
+        if (mbar_try_wait_for(bar, parity, 20000)) return true;
+    } while (*abort == 0 && globaltimer_ns() - t0 <= e.limit_ns);
+    if (*abort == 0) record_error(e, DFL_ERR_TIMEOUT);
+    *abort = 1;
+    return false;
 }
 
 // Position in a ring of N slots and its parity.
@@ -95,74 +103,298 @@ __device__ __forceinline__ uint4 kt_expand(uint32_t codes, uint32_t s) {
     return make_uint4(hmul2u(h[0], s), hmul2u(h[1], s), hmul2u(h[2], s), hmul2u(h[3], s));
 }
 
-// One cell's K codes into rows 16 w .. of a K tile.  A quarter warp writes the
-// eight 16-byte pieces of one tile row: no bank conflicts on either side.
-template <int HD>
-__device__ __forceinline__ void kt_expand_k(const uint8_t* cell, uint8_t* tile, int lane) {
-    using Cell = Kv4Cell<HD>;
-    constexpr int WPR = HD / 8;             // words (8 codes) of a row
-    constexpr int RPL = 32 / WPR;           // rows per warp-wide load
-    const int c = lane % WPR, h = lane / WPR;
-    uint8_t* kb = tile + (c >> 3) * 64 * 128;
-    #pragma unroll
-    for (int i = 0; i < 8 / RPL; ++i) {     // slots s and s + 8
-        const int s = RPL * i + h, tok = Cell::token(s);
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(cell + Cell::K_CODES + s * Cell::ROW + 4 * c);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(cell + Cell::K_CODES + (s + 8) * Cell::ROW + 4 * c);
-        uint32_t s0, s1;
-        if constexpr (HD == 128) {
-            const uint32_t sw = *reinterpret_cast<const uint32_t*>(cell + Cell::K_SCALES + (s * 4 + (c >> 2)) * 4);
-            const uint32_t sel = c & 2 ? 0x3232u : 0x1010u;
-            const uint32_t h0 = e4m3x2_to_half(sw & 0xFFFFu), h1 = e4m3x2_to_half(sw >> 16);
-            s0 = __byte_perm(h0, h0, sel);
-            s1 = __byte_perm(h1, h1, sel);
-        } else {
-            const uint32_t hp = e4m3x2_to_half(*reinterpret_cast<const uint16_t*>(cell + Cell::K_SCALES + (s * 4 + (c >> 1)) * 2));
-            s0 = __byte_perm(hp, hp, 0x1010);
-            s1 = __byte_perm(hp, hp, 0x3232);
-        }
-        uint8_t* d = kb + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
-        *reinterpret_cast<uint4*>(d) = kt_expand(w0, s0);
-        *reinterpret_cast<uint4*>(d + 8 * 128) = kt_expand(w1, s1);
-    }
+// The expanders' shared-memory accesses by 32-bit address.  Volatile: they keep
+// the order they are written in.
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// The same for V; tokens from `left` on become zeros (a weight of 0 times
-// whatever is stored there must add nothing).
-template <int HD>
-__device__ __forceinline__ void kt_expand_v(const uint8_t* cell, uint8_t* tile, int lane, int left) {
-    using Cell = Kv4Cell<HD>;
-    constexpr int WPR = HD / 8, RPL = 32 / WPR;
-    const int pos = lane % WPR, h = lane / WPR;
-    #pragma unroll
-    for (int b = 0; b < 4 / RPL; ++b) {     // tokens t, 4 + t, 8 + t, 12 + t
-        const int t = RPL * b + h;
-        const int c = HD == 128 ? pos ^ (t & 2 ? 8 : 0) : pos;
-        const uint32_t sw = *reinterpret_cast<const uint32_t*>(cell + Cell::V_SCALES + (c >> 1) * 16 + t * 4);
-        const uint32_t sp[2] = {e4m3x2_to_half(sw & 0xFFFFu), e4m3x2_to_half(sw >> 16)};
-        uint8_t* kb = tile + (c >> 3) * 64 * 128;
+// Where lane's piece c (16 bytes, 8 dims) of tile row `row` lies: KU rows of 128
+// bytes, 128-byte swizzle, blocks of 64 dims one after the other.  Rows that
+// differ in bits the start row has clear: (at ^ bits << 4) + rows * 128.
+template <int KU>
+__device__ __forceinline__ uint32_t kt_piece(uint32_t tile, int row, int c) {
+    return tile + (c >> 3) * KU * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// Expansion of the K or V half of a cell into 16 rows of a tile.  A quarter
+// warp writes the eight 16-byte pieces of one tile row: no bank conflicts on
+// either side.  The loops stay rolled: four roles share each scheduler's
+// instruction cache, and unrolled the warps wait for instructions more than
+// they gain (Qwen-shaped block attention 75 against 60 us).
+template <int HD, int KU>
+struct KtExpandK {   // scores of tokens past the length are masked
+    static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane) {
+        using Cell = Kv4Cell<HD>;
+        constexpr int WPR = HD / 8, RPL = 32 / WPR;   // words (8 codes) of a row, rows per warp-wide load
+        constexpr int D = HD == 128 ? 1 : 2;          // slot s + RPL i is token + D i
+        const int c = lane % WPR, h = lane / WPR;
+        const uint32_t codes = half + h * Cell::ROW + 4 * c;
+        const uint32_t scales = half + Cell::K_SCALES + (HD == 128 ? h * 16 + (c >> 2) * 4 : h * 8 + (c >> 1) * 2);
+        const uint32_t at = kt_piece<KU>(tile, Cell::token(h), c);
+        #pragma unroll 1
+        for (int i = 0; i < 8 / RPL; ++i) {           // slots s and s + 8, s = RPL i + h
+            const uint32_t w0 = lds32(codes + RPL * i * Cell::ROW), w1 = lds32(codes + (RPL * i + 8) * Cell::ROW);
+            uint32_t s0, s1;
+            if constexpr (HD == 128) {
+                const uint32_t sw = lds32(scales + RPL * i * 16), sel = c & 2 ? 0x3232u : 0x1010u;
+                const uint32_t h0 = e4m3x2_to_half(sw & 0xFFFFu), h1 = e4m3x2_to_half(sw >> 16);
+                s0 = __byte_perm(h0, h0, sel);
+                s1 = __byte_perm(h1, h1, sel);
+            } else {
+                const uint32_t hp = e4m3x2_to_half(lds16(scales + RPL * i * 8));
+                s0 = __byte_perm(hp, hp, 0x1010);
+                s1 = __byte_perm(hp, hp, 0x3232);
+            }
+            const uint32_t d = (at ^ (D * i << 4)) + D * i * 128;
+            sts128(d, kt_expand(w0, s0));
+            sts128(d + 8 * 128, kt_expand(w1, s1));
+        }
+    }
+};
+
+template <int HD, int KU>
+struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times whatever is stored there must add nothing
+    static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane, int left) {
+        using Cell = Kv4Cell<HD>;
+        constexpr int WPR = HD / 8, RPL = 32 / WPR;
+        const int pos = lane % WPR, h = lane / WPR;
+        const uint32_t codes = half + h * Cell::ROW + 4 * pos;
+        const uint32_t scales = half + (Cell::V_SCALES - Cell::V_CODES) + h * 4;
+        #pragma unroll 1
+        for (int b = 0; b < 4 / RPL; ++b) {           // tokens t, 4 + t, 8 + t, 12 + t, t = RPL b + h
+            const int c = HD == 128 && b ? pos ^ 8 : pos;   // tokens 2 and 3 of four: the row's halves trade places
+            const uint32_t sw = lds32(scales + (c >> 1) * 16 + RPL * b * 4);
+            uint32_t w[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = lds32(codes + (4 * i + RPL * b) * Cell::ROW);
+            const uint32_t at = kt_piece<KU>(tile, h, c);
+            const uint32_t sp[2] = {e4m3x2_to_half(sw & 0xFFFFu), e4m3x2_to_half(sw >> 16)};
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * i + RPL * b;
+                uint32_t s = __byte_perm(sp[i >> 1], sp[i >> 1], i & 1 ? 0x3232 : 0x1010);
+                if (r + h >= left) s = 0;
+                sts128((at ^ ((r & 7) << 4)) + r * 128, kt_expand(w[i], s));
+            }
+        }
+    }
+};
+
+// 16 rows of a tile from bf16 rows of the block (zeros from `left` on), as fp16
+// in units of the pool's power of two, like the cached values.
+template <int HD, int KU>
+__device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t row_stride, uint32_t tile, int lane, int left,
+                                              float inv) {
+    constexpr int WPR = HD / 8, RPL = 32 / WPR, NR = 16 / RPL;
+    const int c = lane % WPR, h = lane / WPR;
+    const uint32_t at = kt_piece<KU>(tile, h, c);
+    if (left <= 0) {
+        #pragma unroll
+        for (int i = 0; i < NR; ++i) sts128((at ^ (((RPL * i) & 7) << 4)) + RPL * i * 128, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    #pragma unroll 1
+    for (int i0 = 0; i0 < NR; i0 += 4) {
+        uint4 v[4];
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int tok = 4 * i + t;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(cell + Cell::V_CODES + tok * Cell::ROW + 4 * pos);
-            uint32_t s = __byte_perm(sp[i >> 1], sp[i >> 1], i & 1 ? 0x3232 : 0x1010);
-            if (tok >= left) s = 0;
-            *reinterpret_cast<uint4*>(kb + tok * 128 + (((c & 7) ^ (tok & 7)) << 4)) = kt_expand(w, s);
+            const int tok = RPL * (i0 + i) + h;
+            v[i] = tok < left ? *reinterpret_cast<const uint4*>(src + tok * row_stride + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = RPL * (i0 + i);
+            sts128((at ^ ((r & 7) << 4)) + r * 128, make_uint4(block_half2(v[i].x, inv), block_half2(v[i].y, inv),
+                                                              block_half2(v[i].z, inv), block_half2(v[i].w, inv)));
         }
     }
 }
 
-// Rows 16 w .. 16 w + 15 of a tile from bf16 rows of the block (zeros past B).
-template <int HD>
-__device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t row_stride, uint8_t* tile, int lane, int left) {
-    constexpr int WPR = HD / 8, RPL = 32 / WPR;
+// Bulk copies of the half cells that one expander warp needs, 32 tokens per
+// ring slot, ahead of their use.  A warp's share of a unit (KU keys) is its
+// half c, G steps of 32 tokens; steps are numbered along a sequence.
+template <int HD, int KU, int RST>
+struct KtFeed {
+    static constexpr int HALF = Kv4Cell<HD>::BYTES / 2, G = KU / 64;
+    const KaArgs& a;
+    const DevErr& err;
+    uint8_t* ring;
+    uint64_t* full;
+    const uint8_t* base;       // the pool's first half cell of this kind
+    int c, lane;
+    KaPos pos;                 // the segment after the one being copied
+    int x, x1;                 // units of the range up to it, and in all
+    int st = 0, end = 0, win = 0, len = 0, n = 0, head = 0;   // step copied next, end of the segment's, first of the window
+    int cells = 0;             // lane 2 i + j: pool cell j of step win + i
+    uint32_t slot = 0, issued = 0;
+
+    __device__ __forceinline__ KtFeed(const KaArgs& a_, const DevErr& err_, uint8_t* ring_, uint64_t* full_, int half, int c_,
+                                      int lane_, const KaPos& pos_, int x0, int x1_)
+        : a(a_), err(err_), ring(ring_), full(full_), base(a_.slab.data + half * HALF), c(c_), lane(lane_), pos(pos_), x(x0),
+          x1(x1_) {}
+
+    __device__ __forceinline__ int key(int step) const { return step / G * KU + c * (KU / 2) + step % G * 32; }
+
+    __device__ __forceinline__ void window() {
+        win = st;
+        const int k = key(st + (lane >> 1)) + (lane & 1) * KV4_CELL_TOKENS;
+        if (k < len) cells = ka_cell(a, n, head, k, err);
+    }
+    // Whether a step with a token is left; moves to it.
+    __device__ __forceinline__ bool more() {
+        #pragma unroll 1
+        while (st == end) {
+            if (x >= x1) return false;
+            const int u1 = min(pos.nu, pos.u + (x1 - x));
+            st = pos.u * G;
+            len = pos.len; n = pos.n; head = pos.head;
+            // steps with a token, up to the segment's end
+            end = max(st, min(u1 * G, len / KU * G + min(G, max(0, (len % KU - c * (KU / 2) + 31) / 32))));
+            x += u1 - pos.u;
+            if (u1 == pos.nu) pos.next_triple(a);
+            win = st - 16;
+        }
+        return true;
+    }
+    // That step; one slot is free.
+    __device__ __forceinline__ void produce() {
+        if (st == win + 16) window();
+        const int c0 = __shfl_sync(0xFFFFFFFFu, cells, 2 * (st - win)), c1 = __shfl_sync(0xFFFFFFFFu, cells, 2 * (st - win) + 1);
+        const bool two = key(st) + KV4_CELL_TOKENS < len;
+        if (elect_one()) {
+            uint8_t* d = ring + slot * 2 * HALF;
+            mbar_arrive_expect_tx(&full[slot], two ? 2 * HALF : HALF);
+            bulk_g2s(d, base + (int64_t)c0 * (2 * HALF), HALF, &full[slot]);
+            if (two) bulk_g2s(d + HALF, base + (int64_t)c1 * (2 * HALF), HALF, &full[slot]);
+        }
+        __syncwarp();
+        slot = slot + 1 == RST ? 0 : slot + 1;
+        ++issued;
+        ++st;
+    }
+};
+
+// One expander warp: half c of the rows of the K tiles (half = 0) or of the V
+// tiles (1) of all units of a range.  One body for both: see KtExpandK.
+template <int HD, int KU, int RST, int ST>
+__device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, volatile int* abort, int half, int c, int lane,
+                                            uint8_t* ring, uint64_t* raw_full, uint32_t tiles, int tile_bytes, uint64_t* t_full,
+                                            uint64_t* t_empty, const __nv_bfloat16* own_src, float own_inv, KaPos pos, int x0,
+                                            int x1) {
+    constexpr int HALF = Kv4Cell<HD>::BYTES / 2;
+    KtFeed<HD, KU, RST> feed(a, err, ring, raw_full, half, c, lane, pos, x0, x1);
+    KtRing<RST> r;
+    KtRing<ST> ts;
+    uint32_t taken = 0;
+    bool ok = true;
+    int x = x0, u = pos.u, u1 = min(pos.nu, u + (x1 - x0));
+    #pragma unroll 1
+    while (x < x1) {
+        const bool own = u == pos.nu - 1;
+        const int left = (own ? a.B : pos.len - u * KU) - c * (KU / 2);
+        const uint32_t t = tiles + ts.i * tile_bytes + c * (KU / 2) * 128;
+        #pragma unroll 1
+        for (int j = 0; j < KU / 32; ++j) {   // 16 tokens at a time
+            if ((j & 1) == 0) {
+                #pragma unroll 1
+                while (feed.issued < taken + RST && feed.more()) feed.produce();
+                const bool cell = !own && j * KV4_CELL_TOKENS < left;
+                ok = (j > 0 || kt_wait(&t_empty[ts.i], ts.ph ^ 1, err, abort)) && (!cell || kt_wait(&raw_full[r.i], r.ph, err, abort));
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+            }
+            if (!own && (j & ~1) * KV4_CELL_TOKENS < left) {
+                // an absent cell's words are what the slot last held
+                const uint32_t src = smem_u32(ring) + (r.i * 2 + (j & 1)) * HALF;
+                if (half) KtExpandV<HD, KU>::run(src, t + j * 16 * 128, lane, left - j * KV4_CELL_TOKENS);
+                else KtExpandK<HD, KU>::run(src, t + j * 16 * 128, lane);
+                if (j & 1) {
+                    __syncwarp();   // the slot has been read by every lane
+                    ++taken;
+                    r.step();
+                }
+            } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
+                const int64_t stride = (int64_t)a.slab.Hkv * HD;
+                kt_block_rows<HD, KU>(own_src + ((int64_t)(pos.n * a.B + c * (KU / 2) + j * 16) * a.slab.Hkv + pos.head) * HD, stride,
+                                      t + j * 16 * 128, lane, left - j * 16, own_inv);
+            }
+        }
+        if (!ok) break;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&t_full[ts.i]);
+        ts.step();
+        ++x;
+        if (++u == u1) {
+            if (u1 == pos.nu) pos.next_triple(a);
+            u = pos.u;
+            u1 = min(pos.nu, u + (x1 - x));
+            const int row = c * (KU / 2) + lane;
+            if (x < x1 && row < a.B) {   // the own rows of the next triple on their way to L2
+                const __nv_bfloat16* p = own_src + ((int64_t)(pos.n * a.B + row) * a.slab.Hkv + pos.head) * HD;
+                prefetch_l2(p);
+                if (HD == 128) prefetch_l2(p + 64);
+            }
+        }
+    }
+    // copies in flight land before the CTA's shared memory goes (they have, unless a wait ran out)
+    #pragma unroll 1
+    for (; taken < feed.issued; ++taken) mbar_wait(&raw_full[taken % RST], (taken / RST) & 1, err);
+}
+
+// Pairwise maximum of two 16-bit unsigned numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// ROWS rows of Q (rows first .. first + ROWS - 1 of the triple; past R zeros)
+// into the Q tile as fp16, each after the power of two that takes its largest
+// element to [1, 2); the powers taken out go to up[].  One warp.
+template <int HD, int MM, int ROWS>
+__device__ __forceinline__ void kt_load_q(const KaArgs& a, int n, int head, int row0, int first, uint32_t tile, float* up, int lane) {
+    constexpr int WPR = HD / 8, RPL = 32 / WPR;   // 16-byte pieces of a row, rows per warp-wide load
     const int c = lane % WPR, h = lane / WPR;
-    uint8_t* kb = tile + (c >> 3) * 64 * 128;
-    #pragma unroll
-    for (int i = 0; i < 16 / RPL; ++i) {
-        const int tok = RPL * i + h;
-        const uint4 v = tok < left ? *reinterpret_cast<const uint4*>(src + tok * row_stride + c * 8) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(kb + tok * 128 + (((c & 7) ^ (tok & 7)) << 4)) = v;
+    constexpr int NB = 4;   // loads in flight
+    #pragma unroll 1
+    for (int i0 = 0; i0 < ROWS; i0 += NB * RPL) {
+        uint4 v[NB];
+        #pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int r = row0 + first + i0 + i * RPL + h;
+            v[i] = r < a.R ? *reinterpret_cast<const uint4*>(a.Q + ka_row(a, n, head, r, HD) + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+        #pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t m2 = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                    max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+            uint32_t mx = max(m2 & 0xFFFFu, m2 >> 16), q[4];
+            #pragma unroll
+            for (int o = 1; o < WPR; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            int e = (int)(mx >> 7);
+            e = (e == 0 || e >= 254) ? 127 : e;   // zero, subnormal, huge or not finite: as it is
+            const float down = __int_as_float((254 - e) << 23);
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __half2 hw = __floats2half2_rn(bf16lo(w[j]) * down, bf16hi(w[j]) * down);
+                q[j] = *reinterpret_cast<const uint32_t*>(&hw);
+            }
+            const int row = first + i0 + i * RPL + h;
+            sts128(tile + (c >> 3) * (MM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), make_uint4(q[0], q[1], q[2], q[3]));
+            if (c == 0) up[row] = __int_as_float(e << 23);
+        }
     }
 }
 
@@ -170,86 +402,37 @@ __device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t 
 // M = 64 the 16 rows of a warp's quadrant are shared by its two half-warps,
 // each with half of a row's columns.
 template <int HD, int MM>
-struct KtRow {
-    static constexpr bool HALF = MM == 64;
-    static constexpr int KPT = HALF ? 32 : 64;          // keys per thread and unit
-    static constexpr int OPT = HALF ? HD / 2 : HD;      // O columns per thread
-    static constexpr int QPT = HALF ? HD / 4 : HD / 2;  // Q columns (pairs) per thread
-
-    // Q of one row (nullptr: no such row) -> tensor memory, as fp16 after a
-    // power of two or as it is; returns the power that was taken out.  16 words
-    // at a time, read twice: a row in registers would set the kernel's count.
-    static __device__ __forceinline__ float load_q(const __nv_bfloat16* src, int hh, bool half_form, uint32_t q_addr) {
-        const uint4* p = reinterpret_cast<const uint4*>(src + hh * (HD / 2));
-        float up = 1.f, down = 1.f;
-        if (half_form) {
-            uint32_t mx = 0;
-            #pragma unroll 4
-            for (int i = 0; i < QPT / 4; ++i) {
-                const uint4 w = src ? p[i] : make_uint4(0, 0, 0, 0);
-                mx = max(mx, max(max(w.x & 0x7FFFu, (w.x >> 16) & 0x7FFFu), max(w.y & 0x7FFFu, (w.y >> 16) & 0x7FFFu)));
-                mx = max(mx, max(max(w.z & 0x7FFFu, (w.z >> 16) & 0x7FFFu), max(w.w & 0x7FFFu, (w.w >> 16) & 0x7FFFu)));
-            }
-            if constexpr (HALF) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-            int e = (int)(mx >> 7);
-            e = (e == 0 || e >= 254) ? 127 : e;   // zero, subnormal, huge or not finite: as it is
-            down = __int_as_float((254 - e) << 23);
-            up = __int_as_float(e << 23);
-        }
-        #pragma unroll 1
-        for (int c = 0; c < QPT; c += 16) {
-            uint32_t q[16];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 w = src ? p[c / 4 + i] : make_uint4(0, 0, 0, 0);
-                q[4 * i] = w.x; q[4 * i + 1] = w.y; q[4 * i + 2] = w.z; q[4 * i + 3] = w.w;
-            }
-            if (half_form) {
-                #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const __half2 h = __floats2half2_rn(bf16lo(q[i]) * down, bf16hi(q[i]) * down);
-                    q[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-            }
-            if constexpr (HALF) tmem_st16u_hx2<QPT>(q_addr + c, q);
-            else tmem_st16(q_addr + c, q);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        return up;
-    }
-};
-
-template <int HD, int MM>
 __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs a, const DevErr err) {
     using Cfg = KtCfg<HD, MM>;
     using Bars = KtBars<Cfg::RST, Cfg::KST, Cfg::VST>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars[KT_PIPES];
-    __shared__ KaLineSmem<KT_THREADS> line_sm;
+    __shared__ KaLineSmem<KT_THREADS, KT_PIPES> line_sm;
+    __shared__ float q_up[KT_PIPES][MM];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // warps 0-7 softmax, 8-15 expanders (four of each pipeline), 16, 17 producers, 18, 19 issuers
-    const int pipe = warp < 16 ? (warp >> 2) & 1 : warp & 1;
+    // warps 0-7 softmax, 8-15 expanders, four of each pipeline
+    const int pipe = (warp >> 2) & 1;
     Bars& bb = bars[pipe];
-    uint8_t* sK = sm + pipe * Cfg::PIPE;
+    uint8_t* sQ = sm + pipe * Cfg::PIPE;
+    uint8_t* sK = sQ + Cfg::Q;
     uint8_t* sV = sK + Cfg::KST * Cfg::TILE;
     uint8_t* sR = sV + Cfg::VST * Cfg::TILE;
     volatile int* abort = &abort_flag;
 
     if (threadIdx.x < KT_PIPES) {
         Bars& b = bars[threadIdx.x];
-        for (int i = 0; i < Cfg::RST; ++i) { mbar_init(&b.raw_full[i], 1); mbar_init(&b.raw_empty[i], 4); }
-        for (int i = 0; i < Cfg::KST; ++i) { mbar_init(&b.k_full[i], 4); mbar_init(&b.k_empty[i], 1); }
-        for (int i = 0; i < Cfg::VST; ++i) { mbar_init(&b.v_full[i], 4); mbar_init(&b.v_empty[i], 1); }
-        mbar_init(&b.q_full, 128); mbar_init(&b.s_full, 1); mbar_init(&b.p_full, 128); mbar_init(&b.pv_done, 1);
-        mbar_init(&b.o_empty, 128); mbar_init(&b.drain, 1);
+        for (int i = 0; i < 4 * Cfg::RST; ++i) mbar_init(&b.raw_full[0][0] + i, 1);
+        for (int i = 0; i < Cfg::KST; ++i) { mbar_init(&b.k_full[i], 2); mbar_init(&b.k_empty[i], 1); }
+        for (int i = 0; i < Cfg::VST; ++i) { mbar_init(&b.v_full[i], 2); mbar_init(&b.v_empty[i], 1); }
+        mbar_init(&b.q_full, 4); mbar_init(&b.s_full, 1); mbar_init(&b.p_full, 4); mbar_init(&b.pv_done, 1);
+        mbar_init(&b.o_empty, 4); mbar_init(&b.drain, 1);
         if (threadIdx.x == 0) abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 16) { tmem_alloc(&tmem_holder, KT_PIPES * Cfg::COLS); tmem_relinquish(); }
+    if (warp == 8) { tmem_alloc(&tmem_holder, KT_PIPES * Cfg::COLS); tmem_relinquish(); }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -258,258 +441,212 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 
     // both pipelines' ranges: the line is cut into 2 * gridDim.x
     const int ranges = KT_PIPES * gridDim.x;
-    KaLine line;
-    for (int p = 0; p < KT_PIPES; ++p) {
-        const KaLine l = ka_locate<KT_THREADS>(a, ranges, line_sm, err, [&](int per, int total) {
-            const int64_t x = (int64_t)(KT_PIPES * blockIdx.x + p) * per;
-            return x < total ? (int)x : -1;
-        });
-        if (p == pipe) line = l;
-        __syncthreads();
-    }
+    ka_check_lengths<KT_THREADS>(a, err);
+    const KaLine line = ka_locate<KT_THREADS, KT_PIPES>(a, ranges, line_sm, [&](int p, int per, int total) {
+        const int64_t x = (int64_t)(KT_PIPES * blockIdx.x + p) * per;
+        return x < total ? (int)x : -1;
+    });
     const int range = KT_PIPES * blockIdx.x + pipe;
     const int64_t x0l = (int64_t)range * line.per;
     const bool work = x0l < line.total;
     const int x0 = work ? (int)x0l : 0, x1 = work ? x0 + min(line.total - x0, line.per) : 0;
     KaPos pos{};
-    if (work) {
-        pos.n = line.n;
-        pos.len = ka_len(a, pos.n, err);
-        pos.nu = ka_units(pos.len);
-        pos.hs = (x0 - line.before) / pos.nu;
-        pos.u = (x0 - line.before) - pos.hs * pos.nu;
-    }
-    // one unit further along the line (with the segment's bounds x < x1)
-    auto advance = [&](KaPos& p) { if (++p.u == p.nu) p.next_triple(a, err); };
+    if (work) pos.set(a, line_sm.at[pipe], x0);
 
-    if (warp >= 16 && warp < 18) {
-        // ------------------------------------------------------------ producer
-        KtRing<Cfg::RST> r;
-        unsigned issued = 0;
-        int base = -1, cells = 0;   // lane 4 i + w: pool cell w of unit base + i
-        for (int x = x0; x < x1; ++x) {
-            const int left = pos.len - pos.u * KA_UNIT;
-            if (pos.u == pos.nu - 1) { base = -1; advance(pos); continue; }   // the block's own unit
-            if (base < 0 || pos.u >= base + 8) {
-                base = pos.u;
-                const int k = base * KA_UNIT + lane * KV4_CELL_TOKENS;
-                if (k < pos.len) {
-                    const int j = k / a.slab.page, in = k - j * a.slab.page;
-                    int p = a.table[(int64_t)pos.n * a.max_pages + j];
-                    if (p < 0 || p >= a.slab.num_pages) { record_error(err, DFL_ERR_INVALID_ARG); p = 0; }
-                    cells = (p * a.slab.Hkv + pos.hs / a.subs) * a.slab.cells + in / KV4_CELL_TOKENS;
-                }
-            }
-            const int cell = __shfl_sync(0xFFFFFFFFu, cells, 4 * (pos.u - base) + (lane & 3));
-            const int count = min(4, (left + KV4_CELL_TOKENS - 1) / KV4_CELL_TOKENS);
-            const bool ok = kt_wait(&bb.raw_empty[r.i], r.ph ^ 1, err, abort);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bb.raw_full[r.i], count * Cfg::CELL);
-            __syncwarp();
-            if (lane < count)
-                bulk_g2s(sR + r.i * Cfg::RAW + lane * Cfg::CELL, a.slab.data + (int64_t)cell * Cfg::CELL, Cfg::CELL,
-                         &bb.raw_full[r.i]);
-            ++issued;
-            r.step();
-            advance(pos);
-        }
-        // copies in flight land before the CTA's shared memory goes (they have, unless a wait ran out)
-        for (unsigned i = issued > Cfg::RST ? issued - Cfg::RST : 0; i < issued; ++i)
-            mbar_wait(&bb.raw_full[i % Cfg::RST], (i / Cfg::RST) & 1, err);
-    } else if (warp >= 18) {
-        // -------------------------------------------------------------- issuer
-        if (lane == 0) {
-            KtRing<Cfg::KST> ks;
-            KtRing<Cfg::VST> vs;
-            uint32_t unit = 0, triple = 0, q_ph = 0;
-            const uint32_t k32 = smem_u32(sK), v32 = smem_u32(sV);
-            bool fresh = true, issued = false, ok = true;
-            for (int x = x0; x < x1; ++x) {
-                const bool own = pos.u == pos.nu - 1, last = own || x == x1 - 1;
-                const uint32_t id_s = own ? idesc_bf16(MM, 64) : kt_idesc_f16(MM, 64);
-                const uint32_t id_o = (own ? idesc_bf16(MM, HD) : kt_idesc_f16(MM, HD)) | (1u << 16);   // V is MN-major
-                // Q in the form this unit needs; the previous unit's P V has read S's columns
-                if (fresh || own) {
-                    if (!(ok = kt_wait(&bb.q_full, q_ph, err, abort))) break;
-                    q_ph ^= 1;
-                }
-                if (!(ok = kt_wait(&bb.k_full[ks.i], ks.ph, err, abort))) break;
-                if (unit > 0 && !(ok = kt_wait(&bb.pv_done, (unit - 1) & 1, err, abort))) break;
-                tc_fence_after();
-                issued = true;
-                #pragma unroll
-                for (int j = 0; j < HD / 16; ++j)
-                    mma_bf16_ts(tmem + Cfg::S_COL, tmem + Cfg::Q_COL + 8 * j,
-                                sw128_desc(k32 + ks.i * Cfg::TILE + (j >> 2) * Cfg::TKB + (j & 3) * 32), id_s, j > 0);
-                mma_commit(&bb.s_full);
-                mma_commit(&bb.k_empty[ks.i]);
-                if (!(ok = kt_wait(&bb.v_full[vs.i], vs.ph, err, abort))) break;
-                // O is free once the previous triple's output has been read
-                if (fresh && !(ok = kt_wait(&bb.o_empty, (triple & 1) ^ 1, err, abort))) break;
-                if (!(ok = kt_wait(&bb.p_full, unit & 1, err, abort))) break;
-                tc_fence_after();
-                #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_bf16_ts(tmem + Cfg::O_COL, tmem + Cfg::S_COL + 8 * j,
-                                sw128_desc_mn(v32 + vs.i * Cfg::TILE + j * 16 * 128, Cfg::TKB, 1024), id_o,
-                                (fresh && j == 0) ? 0 : 1);
-                mma_commit(&bb.pv_done);
-                mma_commit(&bb.v_empty[vs.i]);
-                ks.step();
-                vs.step();
-                ++unit;
-                fresh = last;
-                if (last) ++triple;
-                advance(pos);
-            }
-            if (!ok && issued) {   // products in flight end before tensor memory is released
-                mma_commit(&bb.drain);
-                mbar_wait(&bb.drain, 0, err);
-            }
-        }
-    } else if (warp >= 8) {
-        // ----------------------------------------------------------- expanders
+    if (warp >= 8) {
         const int w = warp & 3;
-        KtRing<Cfg::RST> r;
-        KtRing<Cfg::KST> ks;
-        KtRing<Cfg::VST> vs;
-        for (int x = x0; x < x1; ++x) {
-            const bool own = pos.u == pos.nu - 1;
-            const int left = (own ? a.B : pos.len - pos.u * KA_UNIT) - w * KV4_CELL_TOKENS;
-            uint8_t* kt = sK + ks.i * Cfg::TILE + w * 16 * 128;
-            uint8_t* vt = sV + vs.i * Cfg::TILE + w * 16 * 128;
-            const uint8_t* cell = sR + r.i * Cfg::RAW + w * Cfg::CELL;
-            const int head = pos.hs / a.subs;
-            const int64_t own_row = (int64_t)(pos.n * a.B + w * KV4_CELL_TOKENS) * a.slab.Hkv + head;
-            bool ok = own || kt_wait(&bb.raw_full[r.i], r.ph, err, abort);
-            ok = ok && kt_wait(&bb.k_empty[ks.i], ks.ph ^ 1, err, abort);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (own) kt_block_rows<HD>(a.Kb + own_row * HD, (int64_t)a.slab.Hkv * HD, kt, lane, left);
-            else if (left > 0) kt_expand_k<HD>(cell, kt, lane);   // rows without a key: masked scores
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bb.k_full[ks.i]);
-            ok = kt_wait(&bb.v_empty[vs.i], vs.ph ^ 1, err, abort);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (own || left <= 0) kt_block_rows<HD>(a.Vb + own_row * HD, (int64_t)a.slab.Hkv * HD, vt, lane, left);
-            else kt_expand_v<HD>(cell, vt, lane, left);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bb.v_full[vs.i]);
-                if (!own) mbar_arrive(&bb.raw_empty[r.i]);
-            }
-            if (!own) r.step();
-            ks.step();
-            vs.step();
-            advance(pos);
-        }
+        uint8_t* ring = sR + w * Cfg::RST * Cfg::CELL;
+        const int half = w >> 1;   // two warps for K tiles, two for V tiles
+        static_assert(Cfg::KST == Cfg::VST, "one body for both");
+        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::KST>(a, err, abort, half, w & 1, lane, ring, bb.raw_full[w], smem_u32(half ? sV : sK),
+                                                     Cfg::TILE, half ? bb.v_full : bb.k_full, half ? bb.v_empty : bb.k_empty,
+                                                     half ? a.Vb : a.Kb, half ? a.v_inv : a.k_inv, pos, x0, x1);
     } else {
         // ------------------------------------------------------------- softmax
-        using Row = KtRow<HD, MM>;
-        constexpr bool HALF = Row::HALF;
-        constexpr int KPT = Row::KPT, OPT = Row::OPT;
+        constexpr bool HALF = MM == 64;
+        constexpr int KU = Cfg::KU;
+        constexpr int KPT = HALF ? KU / 2 : KU;      // keys per thread and unit
+        constexpr int OPT = HALF ? HD / 2 : HD;      // O columns per thread
+        constexpr int RPW = HALF ? 16 : 32;          // rows per warp
         const int q4 = warp & 3, hh = HALF ? lane >> 4 : 0;
-        const int row = HALF ? 16 * q4 + (lane & 15) : 32 * q4 + lane;   // row of the triple held by this thread
-        const uint32_t my = tmem + ((uint32_t)(q4 * 32) << 16);
-        uint32_t unit = 0;
-        bool ok = true;
+        const int row = RPW * q4 + (HALF ? lane & 15 : lane);   // row of the triple held by this thread
+        const uint32_t my = tmem + ((uint32_t)(q4 * 32) << 16), s_at = my + Cfg::S_COL;
+        uint32_t unit = 0, triple = 0;
+        bool ok = true, issued = false;
+        // ---- products, by the first warp: one elected lane issues them (operands
+        // the compiler knows to be uniform cost half the clocks per product of
+        // those of a lone lane in a divergent branch, 8 products 214 against 510)
+        const bool issuer = q4 == 0;
+        KtRing<Cfg::KST> ks;
+        KtRing<Cfg::VST> vs;
+        // descriptors of slot 0; slots and K blocks are added to the address field (16-byte units)
+        const uint64_t qd = sw128_desc(smem_u32(sQ)), kd = sw128_desc(smem_u32(sK));
+        const uint64_t vd = sw128_desc_mn(smem_u32(sV), Cfg::TKB, 1024);
+        auto issue_s = [&](bool first) {   // S of the next unit; S's columns are free
+            const bool ready = kt_wait(&bb.k_full[ks.i], ks.ph, err, abort) &&
+                               (!first || kt_wait(&bb.q_full, triple & 1, err, abort));
+            if (!__all_sync(0xFFFFFFFFu, ready)) return false;
+            tc_fence_after();
+            const uint64_t kdi = kd + ks.i * (Cfg::TILE >> 4);
+            if (elect_one()) {
+                #pragma unroll
+                for (int j = 0; j < HD / 16; ++j)
+                    mma_bf16(tmem + Cfg::S_COL, qd + (j >> 2) * (Cfg::QKB >> 4) + (j & 3) * 2,
+                             kdi + (j >> 2) * (Cfg::TKB >> 4) + (j & 3) * 2, kt_idesc_f16(MM, KU), j > 0);
+                mma_commit(&bb.s_full);
+                mma_commit(&bb.k_empty[ks.i]);
+            }
+            __syncwarp();
+            issued = true;
+            ks.step();
+            return true;
+        };
+        auto issue_pv = [&](bool first) {   // P of the unit written by all four warps
+            const bool ready = kt_wait(&bb.v_full[vs.i], vs.ph, err, abort) &&
+                               // O is free once the previous triple's output has been read
+                               (!first || kt_wait(&bb.o_empty, (triple & 1) ^ 1, err, abort)) &&
+                               kt_wait(&bb.p_full, unit & 1, err, abort);
+            if (!__all_sync(0xFFFFFFFFu, ready)) return false;
+            tc_fence_after();
+            const uint64_t vdi = vd + vs.i * (Cfg::TILE >> 4);
+            if (elect_one()) {
+                #pragma unroll
+                for (int j = 0; j < KU / 16; ++j)   // V is MN-major
+                    mma_bf16_ts(tmem + Cfg::O_COL, tmem + Cfg::S_COL + 8 * j, vdi + j * (16 * 128 >> 4),
+                                kt_idesc_f16(MM, HD) | (1u << 16), j > 0 || !first);
+                mma_commit(&bb.pv_done);
+                mma_commit(&bb.v_empty[vs.i]);
+            }
+            __syncwarp();
+            vs.step();
+            return true;
+        };
         int x = x0;
         while (x < x1) {
-            const int head = pos.hs / a.subs, row0 = (pos.hs - head * a.subs) * MM;
+            const int head = pos.head, row0 = pos.tile * MM;
             const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
-            const bool pad = row0 + (HALF ? 16 : 32) * q4 >= a.R;   // the warp holds no row of the block
-            const int rr = row0 + row;
-            const bool real = rr < a.R;
-            const int64_t qrow = real ? (int64_t)(pos.n * a.B + rr / a.G) * a.Hq + head * a.G + rr % a.G : 0;
-            const __nv_bfloat16* qsrc = real ? a.Q + qrow * HD : nullptr;
-            float mult = 0.f, m = -INFINITY, l = 0.f;
-            for (int u = u0; u < u1; ++u) {
-                const bool own = u == pos.nu - 1;
-                if (u == u0 || own) {   // the products that read Q before have ended: their S has been read
-                    if (!pad) mult = Row::load_q(qsrc, hh, !own, my + Cfg::Q_COL) * a.scale_log2 * (own ? 1.f : a.k_pow2);
-                    mbar_arrive(&bb.q_full);
+            const bool pad = row0 + RPW * q4 >= a.R;   // the warp holds no row of the block
+            // the products that read the previous Q have ended: their S has been read
+            kt_load_q<HD, MM, RPW>(a, pos.n, head, row0, RPW * q4, smem_u32(sQ), q_up[pipe], lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&bb.q_full);
+            if (issuer && !issue_s(true)) { ok = false; break; }
+            const float mult = q_up[pipe][row] * a.scale_log2 * a.k_pow2;
+            if (x + u1 - u0 < x1) {   // the next triple's Q on its way to L2
+                const bool wrap = pos.hs + 1 == a.HS;
+                const int hs = wrap ? 0 : pos.hs + 1, nn = pos.n + wrap;
+                const int nrow = (hs % a.subs) * MM + row;
+                if (nrow < a.R) {
+                    const __nv_bfloat16* p = a.Q + ka_row(a, nn, hs / a.subs, nrow, HD);
+                    prefetch_l2(p + hh * (HD / 2));
+                    if (!HALF && HD == 128) prefetch_l2(p + HD / 2);
                 }
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int u = u0; u < u1; ++u) {
                 ok = kt_wait(&bb.s_full, unit & 1, err, abort);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
                 if (!pad) {
-                    // scores 32 at a time (at M = 128 read twice, once for the maximum: 64 in
-                    // registers beside their weights spill)
-                    float s[32], mt = -INFINITY;
-                    auto load = [&](int k0) {
-                        if constexpr (HALF) tmem_ld32_hx2<32>(my + Cfg::S_COL, s);
-                        else tmem_ld32(my + Cfg::S_COL + k0, s);
-                        const int valid = (own ? a.B : pos.len - u * KA_UNIT) - (HALF ? hh * 32 : k0);
-                        if (valid < 32) {
+                    // The maximum first: O is rescaled only where it grows by more than 2^8
+                    // (S of this unit was issued after the P V of the units before had ended).
+                    const int keys = (u == pos.nu - 1 ? a.B : pos.len - u * KU) - hh * KPT;   // from this thread's first on
+                    if (__any_sync(0xFFFFFFFFu, keys < KPT)) {   // a unit's keys past the last: their scores become -inf
+                        #pragma unroll 1
+                        for (int k0 = 0; k0 < KPT; k0 += 16) {
+                            float s[16];
+                            if constexpr (HALF) tmem_ld16_hx2<KPT>(s_at + k0, s);
+                            else tmem_ld16(s_at + k0, s);
+                            uint32_t v[16];
                             #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j >= valid) s[j] = -INFINITY;
+                            for (int j = 0; j < 16; ++j) v[j] = k0 + j < keys ? __float_as_uint(s[j]) : 0xFF800000u;
+                            if constexpr (HALF) tmem_st16u_hx2<KPT>(s_at + k0, v);
+                            else tmem_st16(s_at + k0, v);
                         }
-                    };
+                        tmem_st_wait();
+                    }
+                    float mt = -INFINITY;
                     #pragma unroll 1
                     for (int k0 = 0; k0 < KPT; k0 += 32) {
-                        load(k0);
-                        float m4[4] = {s[0], s[1], s[2], s[3]};
+                        float s[32];
+                        if constexpr (HALF) tmem_ld32_hx2<KPT>(s_at + k0, s);
+                        else tmem_ld32(s_at + k0, s);
+                        float m4[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
                         #pragma unroll
-                        for (int j = 4; j < 32; j += 4) {
-                            m4[0] = fmaxf(m4[0], s[j]); m4[1] = fmaxf(m4[1], s[j + 1]);
-                            m4[2] = fmaxf(m4[2], s[j + 2]); m4[3] = fmaxf(m4[3], s[j + 3]);
-                        }
-                        mt = fmaxf(mt, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                        for (int j = 0; j < 32; j += 2) m4[(j >> 1) & 3] = max3(m4[(j >> 1) & 3], s[j], s[j + 1]);
+                        mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                     }
                     if constexpr (HALF) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 16));
                     mt *= mult;   // mult > 0: the maximum commutes
                     const bool need = mt > m + KA_LAZY;
-                    if (u == u0) {
-                        m = mt;
-                    } else if (__any_sync(0xFFFFFFFFu, need)) {
-                        // O holds the units before (S of this one was issued after their P V had ended)
+                    if (__any_sync(0xFFFFFFFFu, need)) {
                         const float mn = need ? mt : m, al = mn == m ? 1.f : ex2_ftz(m - mn);
-                        #pragma unroll 1
-                        for (int c = 0; c < OPT; c += 32) {
-                            float o[32];
-                            if constexpr (HALF) tmem_ld32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
-                            else tmem_ld32(my + Cfg::O_COL + c, o);
-                            #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= al;
-                            if constexpr (HALF) tmem_st32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
-                            else tmem_st32(my + Cfg::O_COL + c, o);
+                        if (u > u0) {
+                            #pragma unroll 1
+                            for (int c = 0; c < OPT; c += 32) {
+                                float o[32];
+                                if constexpr (HALF) tmem_ld32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
+                                else tmem_ld32(my + Cfg::O_COL + c, o);
+                                #pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] *= al;
+                                if constexpr (HALF) tmem_st32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
+                                else tmem_st32(my + Cfg::O_COL + c, o);
+                            }
                         }
-                        tmem_st_wait();
                         l *= al;
                         m = mn;
                     }
-                    const float off = KA_LIFT - m;
-                    #pragma unroll 1
-                    for (int k0 = 0; k0 < KPT; k0 += 32) {
-                        if (!HALF) load(k0);
-                        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 off2 = make_float2(KA_LIFT - m, KA_LIFT - m), mult2 = make_float2(mult, mult);
+                    float2 l2[2] = {};
+                    auto weigh16 = [&](int k0, uint32_t* pk) {   // weights of 16 of this thread's keys, two per word
+                        float s[16];
+                        if constexpr (HALF) tmem_ld16_hx2<KPT>(s_at + k0, s);
+                        else tmem_ld16(s_at + k0, s);
                         #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            s[j] = ex2_ftz(fmaf(s[j], mult, off));
-                            l4[j & 3] += s[j];
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 e = fma_f32x2(make_float2(s[j], s[j + 1]), mult2, off2);
+                            const float2 p = make_float2(ex2_ftz(e.x), ex2_ftz(e.y));
+                            l2[(j >> 1) & 1] = add_f32x2(l2[(j >> 1) & 1], p);
+                            const __half2 h = __floats2half2_rn(p.x, p.y);
+                            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
                         }
-                        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                        uint32_t pk[16];
-                        if (own) {   // O is kept in units of 2^v_exp
+                    };
+                    // P, two keys per column, over the first half of S's columns
+                    if constexpr (HALF) {   // both halves of a row share its columns: all of S is read first
+                        uint32_t pk[KPT / 16][8];
+                        #pragma unroll
+                        for (int g = 0; g < KPT / 16; ++g) weigh16(16 * g, pk[g]);
+                        __syncwarp();
+                        #pragma unroll
+                        for (int g = 0; g < KPT / 16; g += 2) {
+                            uint32_t v[16];
                             #pragma unroll
-                            for (int j = 0; j < 32; j += 2) pk[j / 2] = pack_bf16(s[j] * a.v_inv, s[j + 1] * a.v_inv);
-                        } else {
-                            #pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const __half2 h = __floats2half2_rn(s[j], s[j + 1]);
-                                pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                            }
+                            for (int j = 0; j < 16; ++j) v[j] = pk[g + j / 8][j % 8];
+                            tmem_st16u_hx2<KPT / 2>(s_at + 8 * g, v);
                         }
-                        // P of 32 keys over 16 of S's columns that have been read
-                        if constexpr (HALF) tmem_st16u_hx2<16>(my + Cfg::S_COL, pk);
-                        else tmem_st16(my + Cfg::S_COL + k0 / 2, pk);
+                    } else {
+                        #pragma unroll 1
+                        for (int k0 = 0; k0 < KPT; k0 += 16) {   // over columns already read
+                            uint32_t pk[8];
+                            weigh16(k0, pk);
+                            tmem_st8u(s_at + k0 / 2, pk);
+                        }
                     }
+                    l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
                     tmem_st_wait();
                 }
                 tc_fence_before();
-                mbar_arrive(&bb.p_full);
+                __syncwarp();
+                if (elect_one()) mbar_arrive(&bb.p_full);
+                if (issuer) {
+                    ok = issue_pv(u == u0);
+                    if (ok && u + 1 < u1) {
+                        ok = kt_wait(&bb.pv_done, unit & 1, err, abort);
+                        ok = __all_sync(0xFFFFFFFFu, ok) && issue_s(false);
+                    }
+                    if (!ok) break;
+                }
                 ++unit;
             }
             if (!ok) break;
@@ -517,9 +654,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
             const bool whole = u0 == 0 && u1 == pos.nu;
+            const int rr = row0 + row;
+            const bool real = rr < a.R;
+            const int64_t qrow = real ? ka_row(a, pos.n, head, rr, 1) : 0;
             const int64_t part = ((int64_t)2 * range + (u0 == 0 ? 1 : 0)) * MM + row;
             if constexpr (HALF) l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            const float inv = whole ? a.v_pow2 / l : 1.f;
+            const float inv = whole ? __fdividef(a.v_pow2, l) : 1.f;
             #pragma unroll 1
             for (int c0 = 0; c0 < OPT && !pad; c0 += 32) {
                 float o[32];
@@ -546,17 +686,23 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             }
             if (real && !whole && hh == 0 && DFL_IN_BOUNDS(err.word, part, (int64_t)2 * ranges * MM))
                 a.ml[part] = make_float2(m, l);
-            __syncwarp();
             tc_fence_before();
-            mbar_arrive(&bb.o_empty);
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&bb.o_empty);
             x += u1 - u0;
             pos.u = u1;
-            if (u1 == pos.nu) pos.next_triple(a, err);
+            if (u1 == pos.nu) pos.next_triple(a);
+            ++triple;
+        }
+        if (!ok && issued) {   // products in flight end before tensor memory is released
+            if (elect_one()) mma_commit(&bb.drain);
+            __syncwarp();
+            mbar_wait(&bb.drain, 0, err);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem_holder, KT_PIPES * Cfg::COLS);
     }
@@ -569,6 +715,8 @@ int kt_grid(int64_t units) { return (int)std::min<int64_t>((units + KT_PIPES - 1
 inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 }  // namespace
+
+int kv4_attn_tc_unit_log2(int R, int hd) { return kt_unit(hd, kv4_attn_tc_rows(R)) == 128 ? 7 : 6; }
 
 size_t kv4_attn_tc_ws_bytes(int R, int hd) {
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * kv4_attn_tc_rows(R);
