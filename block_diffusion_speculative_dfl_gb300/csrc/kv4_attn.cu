@@ -157,11 +157,13 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
         return x < total ? (int)x : -1;
     });
     const int64_t x0l = (int64_t)blockIdx.x * line.per;
-    if (x0l >= line.total) return;
-    const int x0 = (int)x0l, x1 = min(line.total - x0, line.per) + x0;
+    if (line.whole ? (int)blockIdx.x >= a.N * a.HS : x0l >= line.total) return;
+    const int x0 = line.whole ? 0 : (int)x0l;
 
     KaPos pos;   // the triple being computed
-    pos.set(a, line_sm.at[0], x0);
+    if (line.whole) pos.set_triple(a, blockIdx.x);
+    else pos.set(a, line_sm.at[0], x0);
+    const int x1 = line.whole ? pos.nu : min(line.total - x0, line.per) + x0;
 
     // Producer: walks the same units ahead of the computation.  Lane i holds
     // the pool cell of this warp's tokens in unit pbase + i.
@@ -489,6 +491,7 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 // Row tiles of 8 query rows when a group has at most 8, of 16 up to 16: a wider
 // tile expands each key for more rows at once.  More rows go to the
 // tensor-memory kernel.
+constexpr int KA_SEAM = 8;
 constexpr int KA_MAX_ROWS = 16;
 int ka_nt(int R) { return R <= 8 ? 1 : 2; }
 
@@ -528,6 +531,7 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.k_pow2 = kv4_exp2i(pool.k_exp); a.k_inv = kv4_exp2i(-pool.k_exp);
     a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
     a.unit_log2 = tc ? kv4_attn_tc_unit_log2(R, pool.hd) : 6;   // KA_UNIT
+    a.seam = tc ? kv4_attn_tc_seam() : KA_SEAM;
     static_assert(KA_UNIT == 64, "unit_log2");
     const int64_t units = (((int64_t)pg.max_pages * pool.page >> a.unit_log2) + 2) * pg.N * a.HS;
     if (units >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;

@@ -17,6 +17,7 @@ struct KaArgs {
     int subs;                 // row tiles per K/V head
     int HS;                   // Hkv * subs
     int unit_log2;            // keys per unit
+    int seam;                 // see KaLine
     uint64_t g_inv;           // ceil(2^40 / G)
     uint64_t cells_inv;       // ceil(2^36 / cells of a page)
     const __nv_bfloat16* Q;   // [N*B][Hq][hd]
@@ -33,6 +34,7 @@ struct KaArgs {
 // (a complete but for Opart and ml; `units` an upper bound on the line).
 inline int kv4_attn_tc_rows(int R) { return R <= 64 ? 64 : 128; }
 int kv4_attn_tc_unit_log2(int R, int hd);
+int kv4_attn_tc_seam();
 size_t kv4_attn_tc_ws_bytes(int R, int hd);
 dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, cudaStream_t st);
 
@@ -94,9 +96,14 @@ __device__ __forceinline__ void ka_check_lengths(const KaArgs& a, const DevErr& 
 // Units of a sequence: its tokens, then the block's own keys.
 __device__ __forceinline__ int ka_units(const KaArgs& a, int len) { return ((len + (1 << a.unit_log2) - 1) >> a.unit_log2) + 1; }
 
-// The line of units, cut into ranges of `per`, and where positions on it fall.
+// The line of units and how it is cut: into ranges of `per` units, or, when
+// there are no more triples than ranges and none is much longer than the rest,
+// one whole triple per range.  Whole triples leave no partials to write, read
+// and add up, and each range pays for one start and one end; `seam` is what a
+// cut line costs a range beyond that, in units.
 struct KaLine {
     int total, per;     // units in all, per range
+    bool whole;
 };
 
 // Found by ka_locate: the sequence that holds a position, the units of the
@@ -107,7 +114,7 @@ struct KaFound {
 
 template <int THREADS, int P>
 struct KaLineSmem {
-    int red[THREADS / 32];
+    int red[THREADS / 32], longest[THREADS / 32];
     KaFound at[P];
 };
 
@@ -119,13 +126,23 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
     const int chunk = (a.N + THREADS - 1) / THREADS;
     const int n0 = min(a.N, (int)threadIdx.x * chunk), n1 = min(a.N, n0 + chunk);
     const int len0 = n0 < n1 ? ka_len(a, n0) : 0, len1 = n0 + 1 < a.N ? ka_len(a, n0 + 1) : 0;
-    int sum = n0 < n1 ? ka_units(a, len0) : 0;
+    int sum = n0 < n1 ? ka_units(a, len0) : 0, longest = sum;
     #pragma unroll 1
-    for (int n = n0 + 1; n < n1; ++n) sum += ka_units(a, ka_len(a, n));
+    for (int n = n0 + 1; n < n1; ++n) {
+        const int nu = ka_units(a, ka_len(a, n));
+        sum += nu;
+        longest = max(longest, nu);
+    }
     sum *= a.HS;
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    if ((threadIdx.x & 31) == 0) sm.longest[threadIdx.x >> 5] = longest;
     KaLine l;
     const int pre = block_exscan<THREADS>(sum, sm.red, &l.total);
     l.per = max(1, (l.total + ranges - 1) / ranges);
+    longest = (threadIdx.x & 31) < THREADS / 32 ? sm.longest[threadIdx.x & 31] : 0;
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    l.whole = (int64_t)a.N * a.HS <= ranges && longest <= l.per + a.seam;
+    if (l.whole) return l;
     #pragma unroll 1
     for (int i = 0; i < P; ++i) {
         const int x = at(i, l.per, l.total);
@@ -159,6 +176,17 @@ struct KaPos {
         head = hs / a.subs;
         tile = hs - head * a.subs;
     }
+    // The start of triple t of all.
+    __device__ __forceinline__ void set_triple(const KaArgs& a, int t) {
+        n = t / a.HS;
+        hs = t - n * a.HS;
+        len = ka_len(a, n);
+        next = 0;
+        nu = ka_units(a, len);
+        u = 0;
+        head = hs / a.subs;
+        tile = hs - head * a.subs;
+    }
     __device__ __forceinline__ void next_triple(const KaArgs& a) {
         u = 0;
         ++hs;
@@ -187,7 +215,7 @@ __global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const K
         return end < total ? (int)end : -1;
     });
     const int64_t endl = ((int64_t)blockIdx.x + 1) * line.per;
-    if (endl >= line.total) return;
+    if (line.whole || endl >= line.total) return;
     const int end = (int)endl;
     const KaFound f = line_sm.at[0];
     const int nu = ka_units(a, f.len);

@@ -448,10 +448,18 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     });
     const int range = KT_PIPES * blockIdx.x + pipe;
     const int64_t x0l = (int64_t)range * line.per;
-    const bool work = x0l < line.total;
-    const int x0 = work ? (int)x0l : 0, x1 = work ? x0 + min(line.total - x0, line.per) : 0;
     KaPos pos{};
-    if (work) pos.set(a, line_sm.at[pipe], x0);
+    int x0 = 0, x1 = 0;   // the range's units (none: x0 = x1)
+    if (line.whole) {
+        if (range < a.N * a.HS) {
+            pos.set_triple(a, range);
+            x1 = pos.nu;
+        }
+    } else if (x0l < line.total) {
+        x0 = (int)x0l;
+        x1 = x0 + min(line.total - x0, line.per);
+        pos.set(a, line_sm.at[pipe], x0);
+    }
 
     if (warp >= 8) {
         const int w = warp & 3;
@@ -708,6 +716,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     }
 }
 
+constexpr int KT_SEAM = 8;
 constexpr int KT_SMS = 152;   // SMs of a GB300
 
 int kt_grid(int64_t units) { return (int)std::min<int64_t>((units + KT_PIPES - 1) / KT_PIPES, KT_SMS); }
@@ -717,6 +726,8 @@ inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 }  // namespace
 
 int kv4_attn_tc_unit_log2(int R, int hd) { return kt_unit(hd, kv4_attn_tc_rows(R)) == 128 ? 7 : 6; }
+
+int kv4_attn_tc_seam() { return KT_SEAM; }
 
 size_t kv4_attn_tc_ws_bytes(int R, int hd) {
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * kv4_attn_tc_rows(R);
