@@ -8,17 +8,19 @@
 // Work.  The keys of a sequence are cut into units of 64: ceil(len / 64)
 // context units and one unit of the block's own keys.  All units of all
 // (sequence, K/V head, row tile) triples in order form one line, cut into
-// equal ranges, one per CTA, whatever the lengths: no CTA waits for a longer
+// equal ranges, whatever the lengths: no range waits for a longer
 // sequence, and the scratch depends on the grid alone.  A triple that lies
-// within one CTA's range is written directly; one that crosses borders leaves
-// one partial (sum, maximum, unnormalised O) per CTA, and a second kernel adds
+// within one range is written directly; one that crosses borders leaves
+// one partial (sum, maximum, unnormalised O) per range, and a second kernel adds
 // a triple's partials in the order of the keys, so results repeat bit for bit.
 //
-// A CTA is four warps; warp w takes tokens 16w .. 16w + 15 (one cell) of every
-// unit of its range with its own running maximum, sum and O, so the warps meet
-// only at the end of a triple.  Each warp keeps a ring of cells in flight
-// (one bulk copy of 18 hd bytes each, K, V and scales together) and expands
-// codes in registers straight into operand fragments:
+// A range belongs to a group of four warps; warp w takes tokens 16w .. 16w + 15
+// (one cell) of every unit with its own running maximum, sum and O, so the
+// warps meet only at the end of a triple.  One CTA per SM holds four such groups
+// (three with 16 rows): as CTAs of their own the hardware put five on one SM
+// and three on another, and all waited for the five.  Each warp keeps a ring of
+// cells in flight (one bulk copy of 18 hd bytes each, K, V and scales together)
+// and expands codes in registers straight into operand fragments:
 //   S^T (16 tokens x 8 rows)  = K Q^T,  A = K codes * scale in fp16
 //   O^T (hd x 8 rows)        += V^T P^T, A = V codes * scale in fp16
 // with m16n8k16 warp products.  At these row counts the kernel is bound by
@@ -32,9 +34,9 @@
 // survive, elements below 2^-14 of the largest lose bits that are under 2^-24
 // of it.  P = 2^(s - m + 7) is rounded to fp16 (11 bits; the 7 keeps weights
 // down to 2^-31 of the largest, m trails the true maximum by at most 8); sums
-// of P are fp32 of the unrounded values.  The block's own keys and values use
-// bf16 products, which take their range.  Maxima are per row; O is rescaled
-// only when a maximum grows by more than 2^8.
+// of P are fp32 of the unrounded values.  The block's own keys and values are
+// taken to fp16 in units of the pool's powers of two (block_half2).  Maxima are
+// per row; O is rescaled only when a maximum grows by more than 2^8.
 #include "internal.h"
 #include "kv4_attn.cuh"
 #include "paged.h"
@@ -44,18 +46,12 @@ namespace dfl {
 namespace {
 
 constexpr int KA_UNIT = 64;        // keys per unit
-constexpr int KA_WARPS = 4;        // one cell of 16 keys per warp and unit
+constexpr int KA_WARPS = 4;        // of a group: one cell of 16 keys per warp and unit
 constexpr int KA_THREADS = KA_WARPS * 32;
 constexpr int KA_SLOTS = 4;        // cells in flight per warp
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_b16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -78,13 +74,75 @@ struct KaCfg {
     static constexpr int MT = HD / 16;                // 16-dim tiles of O^T
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
     static constexpr int PITCH = HD + 4;              // floats per row of the warps' O in shared memory
+    static constexpr int GROUPS = NT == 1 ? 4 : 3;    // per CTA (registers)
+    static constexpr int THREADS = GROUPS * KA_THREADS;
     static constexpr int RING = KA_WARPS * KA_SLOTS * CELL;
     static constexpr int MERGE = KA_WARPS * ROWS * PITCH * 4;
     static constexpr int ML = KA_WARPS * ROWS * 8;
-    static constexpr int SMEM = RING + MERGE + ML + KA_WARPS * KA_SLOTS * 8;
-    static constexpr int CTAS = NT == 1 ? 4 : 3;      // per SM (registers)
-    static_assert(CTAS * (SMEM + 1024) <= 227 * 1024, "shared memory");
+    static constexpr int GROUP = (RING + MERGE + ML + KA_WARPS * KA_SLOTS * 8 + 127) / 128 * 128;
+    static constexpr int SMEM = GROUPS * GROUP;
+    static_assert(SMEM <= 226 * 1024, "shared memory");
 };
+
+// The cells of one warp, copied ahead of their use.  Lane i holds the pool cell
+// of the warp's tokens in unit win + i.
+template <int HD, int ROWS>
+struct KaFeed {
+    static constexpr int CELL = Kv4Cell<HD>::BYTES;
+    const KaArgs& a;
+    const DevErr& err;
+    uint8_t* ring;
+    uint64_t* full;
+    int w, lane;
+    KaPos pos;                 // the segment after the one being copied
+    int x, x1;                 // units of the range up to it, and in all
+    int u = 0, end = 0, win = 0, cells = 0, len = 0, n = 0, head = 0;
+    uint32_t issued = 0;
+
+    __device__ __forceinline__ KaFeed(const KaArgs& a_, const DevErr& err_, uint8_t* ring_, uint64_t* full_, int w_, int lane_,
+                                      const KaPos& pos_, int x0, int x1_)
+        : a(a_), err(err_), ring(ring_), full(full_), w(w_), lane(lane_), pos(pos_), x(x0), x1(x1_) {}
+
+    // The next cell into a free slot, if any is left.
+    __device__ __forceinline__ void produce() {
+        #pragma unroll 1
+        while (u == end) {
+            if (!pos.enter(x, x1)) return;
+            u = pos.u;
+            len = pos.len; n = pos.n; head = pos.head;
+            const int u1 = min(pos.nu, u + (x1 - x));
+            end = max(u, min(u1, (len - w * KV4_CELL_TOKENS + KA_UNIT - 1) / KA_UNIT));   // units with a token of this warp's
+            x += u1 - u;
+            // this triple's queries and own rows on their way to L2
+            const int r = pos.tile * ROWS + 8 * w + lane / 4, b = w * KV4_CELL_TOKENS + lane / 2;
+            if (8 * w < ROWS && r < a.R) prefetch_l2(a.Q + ka_row(a, n, head, r, HD) + lane % 4 * (HD / 4));
+            if (u1 == pos.nu && b < a.B) {
+                const int64_t at = ((int64_t)(n * a.B + b) * a.slab.Hkv + head) * HD + lane % 2 * (HD / 2);
+                prefetch_l2(a.Kb + at);
+                prefetch_l2(a.Vb + at);
+            }
+            if (u1 == pos.nu) pos.next_triple(a);
+            win = u - 32;
+        }
+        if (u == win + 32) {
+            win = u;
+            const int k = (u + lane) * KA_UNIT + w * KV4_CELL_TOKENS;
+            if (k < len) cells = ka_cell(a, n, head, k, err);
+        }
+        const int cell = __shfl_sync(0xFFFFFFFFu, cells, u - win);
+        if (elect_one()) {
+            const uint32_t s = issued % KA_SLOTS;
+            mbar_arrive_expect_tx(&full[s], CELL);
+            bulk_g2s(ring + s * CELL, a.slab.data + (int64_t)cell * CELL, CELL, &full[s]);
+        }
+        __syncwarp();
+        ++issued;
+        ++u;
+    }
+};
+
+// All threads of one group.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" :: "r"(group + 1) : "memory"); }
 
 // State of one warp over one triple: per lane, for query rows 2t and 2t + 1 of
 // each 8-row tile (t = lane % 4).
@@ -132,14 +190,15 @@ __device__ __forceinline__ void ka_softmax(KaAcc<HD, NT>& acc, float (&s)[NT][4]
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(KA_THREADS, KaCfg<HD, NT>::CTAS)
-kv4_attn_kernel(const KaArgs a, const DevErr err) {
+__global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(const KaArgs a, const DevErr err) {
     using Cfg = KaCfg<HD, NT>;
     using Cell = Kv4Cell<HD>;
     constexpr int KW = HD / 32;          // words of a lane's quarter of a K row (codes)
-    extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ KaLineSmem<KA_THREADS, 1> line_sm;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ KaLineSmem<Cfg::THREADS, Cfg::GROUPS> line_sm;
+    const int group = threadIdx.x / KA_THREADS, tid = threadIdx.x % KA_THREADS;
+    const int warp = tid >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint8_t* sm = smem + group * Cfg::GROUP;
     uint8_t* ring = sm + warp * KA_SLOTS * Cfg::CELL;
     float* merge = reinterpret_cast<float*>(sm + Cfg::RING);
     float2* mlsm = reinterpret_cast<float2*>(sm + Cfg::RING + Cfg::MERGE);
@@ -151,59 +210,31 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
     __syncwarp();
     grid_dep_begin();
 
-    ka_check_lengths<KA_THREADS>(a, err);
-    const KaLine line = ka_locate<KA_THREADS, 1>(a, gridDim.x, line_sm, [&](int, int per, int total) {
-        const int64_t x = (int64_t)blockIdx.x * per;
+    ka_check_lengths<Cfg::THREADS>(a, err);
+    // ranges go round the CTAs, so that a few of them spread over the SMs
+    const int ranges = Cfg::GROUPS * gridDim.x, range = group * gridDim.x + blockIdx.x;
+    const KaLine line = ka_locate<Cfg::THREADS, Cfg::GROUPS>(a, ranges, line_sm, [&](int i, int per, int total) {
+        const int64_t x = (int64_t)(i * gridDim.x + blockIdx.x) * per;
         return x < total ? (int)x : -1;
     });
-    const int64_t x0l = (int64_t)blockIdx.x * line.per;
-    if (line.whole ? (int)blockIdx.x >= a.N * a.HS : x0l >= line.total) return;
+    const int64_t x0l = (int64_t)range * line.per;
+    if (line.whole ? range >= a.N * a.HS : x0l >= line.total) return;   // no block-wide barrier follows
     const int x0 = line.whole ? 0 : (int)x0l;
 
     KaPos pos;   // the triple being computed
-    if (line.whole) pos.set_triple(a, blockIdx.x);
-    else pos.set(a, line_sm.at[0], x0);
+    if (line.whole) pos.set_triple(a, range);
+    else pos.set(a, line_sm.at[group], x0);
     const int x1 = line.whole ? pos.nu : min(line.total - x0, line.per) + x0;
 
-    // Producer: walks the same units ahead of the computation.  Lane i holds
-    // the pool cell of this warp's tokens in unit pbase + i.
-    KaPos pp = pos;
-    int pleft = x1 - x0;       // units the producer has not passed
-    int pbase = -1, pcell = 0;
-    unsigned issued = 0, taken = 0;
+    KaFeed<HD, Cfg::ROWS> feed(a, err, ring, full, warp, lane, pos, x0, x1);
+    uint32_t taken = 0;
     bool dead = false;         // a wait ran out: no more copies, no more computation
-    auto produce = [&]() {     // issue this warp's next cell, if any is left
-        while (pleft > 0) {
-            const int key = pp.u * KA_UNIT + warp * KV4_CELL_TOKENS;
-            if (key >= pp.len) {   // past the context (the block's own unit, or a short last unit): next unit
-                --pleft;
-                if (++pp.u == pp.nu) pp.next_triple(a);
-                pbase = -1;
-                continue;
-            }
-            if (pbase < 0 || pp.u >= pbase + 32) {
-                pbase = pp.u;
-                const int k = (pbase + lane) * KA_UNIT + warp * KV4_CELL_TOKENS;
-                if (k < pp.len) pcell = ka_cell(a, pp.n, pp.head, k, err);
-            }
-            const int cell = __shfl_sync(0xFFFFFFFFu, pcell, pp.u - pbase);
-            if (elect_one()) {
-                const int s = issued % KA_SLOTS;
-                mbar_arrive_expect_tx(&full[s], Cfg::CELL);
-                bulk_g2s(ring + s * Cfg::CELL, a.slab.data + (int64_t)cell * Cfg::CELL, Cfg::CELL, &full[s]);
-            }
-            ++issued;
-            --pleft;
-            if (++pp.u == pp.nu) pp.next_triple(a);   // cannot happen: the last unit is the block's own
-            return;
-        }
-    };
     #pragma unroll 1
-    for (int i = 0; i < KA_SLOTS; ++i) produce();
+    for (int i = 0; i < KA_SLOTS; ++i) feed.produce();
 
     int x = x0;
     #pragma unroll 1
-    while (x < x1) {
+    while (pos.enter(x, x1)) {
         const int head = pos.head, row0 = pos.tile * Cfg::ROWS;
         const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
         // ---- Q of this triple: lane (g, t) holds row g's quarter t of each 8-row tile
@@ -369,9 +400,9 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
                 }
             }
             __syncwarp();   // the slot has been read by every lane
-            produce();
+            feed.produce();
         }
-        // ---- the block's own keys (bf16), 16 per warp
+        // ---- the block's own keys, 16 per warp
         if (u1 == pos.nu && warp * KV4_CELL_TOKENS < a.B && !dead) {
             const int Hkv = a.slab.Hkv;
             float s[NT][4];
@@ -384,44 +415,44 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
             for (int i = 0; i < HD / 32; ++i) {
                 const uint4 z = make_uint4(0, 0, 0, 0);
                 const uint4 w0 = b0 < a.B ? k0[i] : z, w1 = b1 < a.B ? k1[i] : z;
-                const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
+                const uint32_t f0[4] = {block_half2(w0.x, a.k_inv), block_half2(w1.x, a.k_inv), block_half2(w0.y, a.k_inv),
+                                        block_half2(w1.y, a.k_inv)};
+                const uint32_t f1[4] = {block_half2(w0.z, a.k_inv), block_half2(w1.z, a.k_inv), block_half2(w0.w, a.k_inv),
+                                        block_half2(w1.w, a.k_inv)};
                 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int r = row0 + nt * 8 + g;
-                    const uint4 qw = r < a.R ? reinterpret_cast<const uint4*>(
-                        a.Q + ka_row(a, pos.n, head, r, HD) + t * (HD / 4))[i] : z;
-                    mma_b16(s[nt], f0, qw.x, qw.y);
-                    mma_b16(s[nt], f1, qw.z, qw.w);
+                    mma_f16(s[nt], f0, q[nt][4 * i], q[nt][4 * i + 1]);
+                    mma_f16(s[nt], f1, q[nt][4 * i + 2], q[nt][4 * i + 3]);
                 }
             }
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[nt][c] = (c < 2 ? b0 : b1) < a.B ? s[nt][c] * a.scale_log2 : -INFINITY;
+                for (int c = 0; c < 4; ++c) s[nt][c] = (c < 2 ? b0 : b1) < a.B ? s[nt][c] * mult[nt][c & 1] : -INFINITY;
             ka_softmax<HD, NT>(acc, s);
             uint32_t pb[NT][2];
             #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {   // O is kept in units of 2^v_exp
-                pb[nt][0] = transpose8x8(pack_bf16(s[nt][0] * a.v_inv, s[nt][1] * a.v_inv));
-                pb[nt][1] = transpose8x8(pack_bf16(s[nt][2] * a.v_inv, s[nt][3] * a.v_inv));
+            for (int nt = 0; nt < NT; ++nt) {
+                pb[nt][0] = transpose8x8(pack_half(s[nt][0], s[nt][1]));
+                pb[nt][1] = transpose8x8(pack_half(s[nt][2], s[nt][3]));
             }
             #pragma unroll
             for (int w = 0; w < HD / 64; ++w) {   // 8 dims of the lane's eighth at a time
-                uint4 v[4];
+                uint32_t v[4][4];
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int b = warp * KV4_CELL_TOKENS + 4 * i + t;
-                    v[i] = b < a.B ? *reinterpret_cast<const uint4*>(
+                    const uint4 x4 = b < a.B ? *reinterpret_cast<const uint4*>(
                         a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0);
+                    v[i][0] = block_half2(x4.x, a.v_inv); v[i][1] = block_half2(x4.y, a.v_inv);
+                    v[i][2] = block_half2(x4.z, a.v_inv); v[i][3] = block_half2(x4.w, a.v_inv);
                 }
-                const uint32_t* v0 = &v[0].x; const uint32_t* v1 = &v[1].x;
-                const uint32_t* v2 = &v[2].x; const uint32_t* v3 = &v[3].x;
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t af[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
-                                            __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632)};
+                    const uint32_t af[4] = {__byte_perm(v[0][i], v[1][i], 0x5410), __byte_perm(v[0][i], v[1][i], 0x7632),
+                                            __byte_perm(v[2][i], v[3][i], 0x5410), __byte_perm(v[2][i], v[3][i], 0x7632)};
                     #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_b16(acc.o[nt][4 * w + i], af, pb[nt][0], pb[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc.o[nt][4 * w + i], af, pb[nt][0], pb[nt][1]);
                 }
             }
         }
@@ -441,14 +472,14 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
                     *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc.o[nt][i][r], acc.o[nt][i][r + 2],
                                                                           acc.o[nt][i + 1][r], acc.o[nt][i + 1][r + 2]);
             }
-        __syncthreads();
+        group_sync(group);
         {
             const bool whole = u0 == 0 && u1 == pos.nu;
-            const int part = 2 * (int)blockIdx.x + (u0 == 0 ? 1 : 0);
+            const int part = 2 * range + (u0 == 0 ? 1 : 0);
             constexpr int TPR = HD / 4;   // threads per row
             #pragma unroll 1
-            for (int row = threadIdx.x / TPR; row < Cfg::ROWS; row += KA_THREADS / TPR) {
-                const int r = row0 + row, c = (threadIdx.x % TPR) * 4;
+            for (int row = tid / TPR; row < Cfg::ROWS; row += KA_THREADS / TPR) {
+                const int r = row0 + row, c = (tid % TPR) * 4;
                 if (r >= a.R) break;
                 float2 ml[KA_WARPS];
                 float M = -INFINITY, L = 0.f;
@@ -470,20 +501,21 @@ kv4_attn_kernel(const KaArgs a, const DevErr err) {
                             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
                 } else {
                     const int64_t at = ((int64_t)part * Cfg::ROWS + row) * HD + c;
-                    if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)2 * gridDim.x * Cfg::ROWS * HD)) {
+                    if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)2 * ranges * Cfg::ROWS * HD)) {
                         *reinterpret_cast<float4*>(a.Opart + at) = o;
                         if (c == 0) a.ml[part * Cfg::ROWS + row] = make_float2(M, L);
                     }
                 }
             }
         }
-        __syncthreads();
+        group_sync(group);
         x += u1 - u0;
         pos.u = u1;
         if (u1 == pos.nu) pos.next_triple(a);
     }
     // After a wait that ran out: let the copies in flight land before the CTA's shared memory goes.
-    for (; taken < issued; ++taken) mbar_wait(&full[taken % KA_SLOTS], (taken / KA_SLOTS) & 1, err);
+    #pragma unroll 1
+    for (; taken < feed.issued; ++taken) mbar_wait(&full[taken % KA_SLOTS], (taken / KA_SLOTS) & 1, err);
 }
 
 constexpr int KA_SMS = 152;   // SMs of a GB300
@@ -492,11 +524,14 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 // tile expands each key for more rows at once.  More rows go to the
 // tensor-memory kernel.
 constexpr int KA_SEAM = 8;
+constexpr int KA_WEIGHT = 4;
 constexpr int KA_MAX_ROWS = 16;
 int ka_nt(int R) { return R <= 8 ? 1 : 2; }
 
-// CTAs of the launch: every SM full, or one per unit when there are fewer.
-int ka_grid(int64_t units, int nt) { return (int)std::min<int64_t>(units, KA_SMS * (nt == 1 ? 4 : 3)); }
+int ka_groups(int nt) { return nt == 1 ? KaCfg<128, 1>::GROUPS : KaCfg<128, 2>::GROUPS; }
+
+// CTAs of the launch: one per SM, fewer when there are fewer units.
+int ka_grid(int64_t units) { return (int)std::min<int64_t>(units, KA_SMS); }
 
 inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
@@ -506,7 +541,7 @@ size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
     if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
     const int R = B * (Hq / Hkv), nt = ka_nt(R);
     if (R > KA_MAX_ROWS) return kv4_attn_tc_ws_bytes(R, hd);
-    const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * 8 * nt;
+    const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * 8 * nt;
     return al256(parts * hd * 4) + al256(parts * 8);
 }
 
@@ -531,15 +566,16 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.k_pow2 = kv4_exp2i(pool.k_exp); a.k_inv = kv4_exp2i(-pool.k_exp);
     a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
     a.unit_log2 = tc ? kv4_attn_tc_unit_log2(R, pool.hd) : 6;   // KA_UNIT
+    a.weight = tc ? kv4_attn_tc_weight() : KA_WEIGHT;
     a.seam = tc ? kv4_attn_tc_seam() : KA_SEAM;
     static_assert(KA_UNIT == 64, "unit_log2");
-    const int64_t units = (((int64_t)pg.max_pages * pool.page >> a.unit_log2) + 2) * pg.N * a.HS;
+    const int64_t units = (((int64_t)pg.max_pages * pool.page >> a.unit_log2) + 2 + a.weight) * pg.N * a.HS;
     if (units >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, st);
-    const size_t parts = 2 * (size_t)ka_grid(INT64_MAX, nt) * rows;
+    const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * rows;
     a.Opart = static_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
-    const int grid = ka_grid(units, nt);
+    const int grid = ka_grid(units), groups = ka_groups(nt);
     const DevErr err = dev_err(ctx);
     auto run = [&](auto kern, auto join, int smem, int slot) -> dfl_status {
         if (!ctx->kv4_attr_set[slot]) {
@@ -549,11 +585,11 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
         }
         {
             ProfScope ps("kv4_attn", st);
-            const dfl_status rc = launch_pdl(kern, grid, KA_THREADS, smem, st, a, err);
+            const dfl_status rc = launch_pdl(kern, grid, groups * KA_THREADS, smem, st, a, err);
             if (rc != DFL_OK) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
-        return launch_pdl(join, dim3(grid, rows / KJ_ROWS), pool.hd / 4 * KJ_ROWS, 0, st, a, err);
+        return launch_pdl(join, dim3(grid * groups, rows / KJ_ROWS), pool.hd / 4 * KJ_ROWS, 0, st, a, err);
     };
     if (pool.hd == 128)
         return nt == 1 ? run(kv4_attn_kernel<128, 1>, kv4_attn_join_kernel<128, 8>, KaCfg<128, 1>::SMEM, 0)

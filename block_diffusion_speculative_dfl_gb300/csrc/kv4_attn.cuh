@@ -17,7 +17,7 @@ struct KaArgs {
     int subs;                 // row tiles per K/V head
     int HS;                   // Hkv * subs
     int unit_log2;            // keys per unit
-    int seam;                 // see KaLine
+    int weight, seam;         // see KaLine
     uint64_t g_inv;           // ceil(2^40 / G)
     uint64_t cells_inv;       // ceil(2^36 / cells of a page)
     const __nv_bfloat16* Q;   // [N*B][Hq][hd]
@@ -35,6 +35,7 @@ struct KaArgs {
 inline int kv4_attn_tc_rows(int R) { return R <= 64 ? 64 : 128; }
 int kv4_attn_tc_unit_log2(int R, int hd);
 int kv4_attn_tc_seam();
+int kv4_attn_tc_weight();
 size_t kv4_attn_tc_ws_bytes(int R, int hd);
 dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, cudaStream_t st);
 
@@ -98,11 +99,14 @@ __device__ __forceinline__ int ka_units(const KaArgs& a, int len) { return ((len
 
 // The line of units and how it is cut: into ranges of `per` units, or, when
 // there are no more triples than ranges and none is much longer than the rest,
-// one whole triple per range.  Whole triples leave no partials to write, read
-// and add up, and each range pays for one start and one end; `seam` is what a
-// cut line costs a range beyond that, in units.
+// one whole triple per range.  A triple takes `weight` places on the line ahead
+// of its units, for what it costs however short it is (queries, own keys, the
+// end): without them a range of many short sequences ended long after the
+// others.  Whole triples leave no partials to write, read and add up, and each
+// range pays for one start and one end; `seam` is what a cut line costs a range
+// beyond that, in units.
 struct KaLine {
-    int total, per;     // units in all, per range
+    int total, per;     // places in all, per range
     bool whole;
 };
 
@@ -126,10 +130,10 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
     const int chunk = (a.N + THREADS - 1) / THREADS;
     const int n0 = min(a.N, (int)threadIdx.x * chunk), n1 = min(a.N, n0 + chunk);
     const int len0 = n0 < n1 ? ka_len(a, n0) : 0, len1 = n0 + 1 < a.N ? ka_len(a, n0 + 1) : 0;
-    int sum = n0 < n1 ? ka_units(a, len0) : 0, longest = sum;
+    int sum = n0 < n1 ? ka_units(a, len0) + a.weight : 0, longest = sum;
     #pragma unroll 1
     for (int n = n0 + 1; n < n1; ++n) {
-        const int nu = ka_units(a, ka_len(a, n));
+        const int nu = ka_units(a, ka_len(a, n)) + a.weight;
         sum += nu;
         longest = max(longest, nu);
     }
@@ -150,7 +154,7 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
         int p = pre, len = len0, next = len1;
         #pragma unroll 1
         for (int n = n0; ; ++n) {
-            const int w = ka_units(a, len) * a.HS;
+            const int w = (ka_units(a, len) + a.weight) * a.HS;
             if (x < p + w) { sm.at[i] = KaFound{n, p, len, next}; break; }
             p += w;
             len = next;
@@ -161,8 +165,8 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
     return l;
 }
 
-// A position on the line as (sequence, head and row tile, unit).  The next
-// sequence's length is read ahead.
+// A position on the line as (sequence, head and row tile, unit); u < 0 in the
+// places ahead of a triple's units.  The next sequence's length is read ahead.
 struct KaPos {
     int n, hs, head, tile, u, nu, len, next;
     // Position x of the line, which ka_locate found.
@@ -171,8 +175,8 @@ struct KaPos {
         len = f.len;
         next = f.next;
         nu = ka_units(a, len);
-        hs = (x - f.before) / nu;
-        u = x - f.before - hs * nu;
+        hs = (x - f.before) / (nu + a.weight);
+        u = x - f.before - hs * (nu + a.weight) - a.weight;
         head = hs / a.subs;
         tile = hs - head * a.subs;
     }
@@ -187,8 +191,14 @@ struct KaPos {
         head = hs / a.subs;
         tile = hs - head * a.subs;
     }
+    // From place x to the unit that follows; false at the range's end x1.
+    __device__ __forceinline__ bool enter(int& x, int x1) {
+        x -= min(u, 0);
+        u = max(u, 0);
+        return x < x1;
+    }
     __device__ __forceinline__ void next_triple(const KaArgs& a) {
-        u = 0;
+        u = -a.weight;
         ++hs;
         if (++tile == a.subs) { tile = 0; ++head; }
         if (hs == a.HS) {
@@ -219,9 +229,9 @@ __global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const K
     const int end = (int)endl;
     const KaFound f = line_sm.at[0];
     const int nu = ka_units(a, f.len);
-    const int hs = (end - f.before) / nu;
-    const int p0 = f.before + hs * nu, p1 = p0 + nu;   // the triple holding unit `end`
-    if (p0 == end || p0 < end - line.per) return;          // none crosses, or it started before this CTA
+    const int hs = (end - f.before) / (nu + a.weight);
+    const int p0 = f.before + hs * (nu + a.weight) + a.weight, p1 = p0 + nu;   // units of the triple at `end`
+    if (p0 >= end || p0 < end - line.per) return;          // none crosses, or it started before this range
     const int first = blockIdx.x, last = (p1 - 1) / line.per;
     const int head = hs / a.subs, row0 = (hs - head * a.subs) * ROWS;
     const int row = blockIdx.y * KJ_ROWS + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;

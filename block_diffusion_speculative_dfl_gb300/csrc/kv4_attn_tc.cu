@@ -255,7 +255,7 @@ struct KtFeed {
     __device__ __forceinline__ bool more() {
         #pragma unroll 1
         while (st == end) {
-            if (x >= x1) return false;
+            if (!pos.enter(x, x1)) return false;
             const int u1 = min(pos.nu, pos.u + (x1 - x));
             st = pos.u * G;
             len = pos.len; n = pos.n; head = pos.head;
@@ -298,7 +298,9 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
     KtRing<ST> ts;
     uint32_t taken = 0;
     bool ok = true;
-    int x = x0, u = pos.u, u1 = min(pos.nu, u + (x1 - x0));
+    int x = x0;
+    pos.enter(x, x1);
+    int u = pos.u, u1 = min(pos.nu, u + (x1 - x));
     #pragma unroll 1
     while (x < x1) {
         const bool own = u == pos.nu - 1;
@@ -337,6 +339,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         ++x;
         if (++u == u1) {
             if (u1 == pos.nu) pos.next_triple(a);
+            pos.enter(x, x1);
             u = pos.u;
             u1 = min(pos.nu, u + (x1 - x));
             const int row = c * (KU / 2) + lane;
@@ -439,14 +442,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     const uint32_t tmem = tmem_holder + pipe * Cfg::COLS;
     grid_dep_begin();
 
-    // both pipelines' ranges: the line is cut into 2 * gridDim.x
+    // ranges go round the CTAs, so that a few of them spread over the SMs
     const int ranges = KT_PIPES * gridDim.x;
     ka_check_lengths<KT_THREADS>(a, err);
     const KaLine line = ka_locate<KT_THREADS, KT_PIPES>(a, ranges, line_sm, [&](int p, int per, int total) {
-        const int64_t x = (int64_t)(KT_PIPES * blockIdx.x + p) * per;
+        const int64_t x = (int64_t)(p * gridDim.x + blockIdx.x) * per;
         return x < total ? (int)x : -1;
     });
-    const int range = KT_PIPES * blockIdx.x + pipe;
+    const int range = pipe * gridDim.x + blockIdx.x;
     const int64_t x0l = (int64_t)range * line.per;
     KaPos pos{};
     int x0 = 0, x1 = 0;   // the range's units (none: x0 = x1)
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             return true;
         };
         int x = x0;
-        while (x < x1) {
+        while (pos.enter(x, x1)) {
             const int head = pos.head, row0 = pos.tile * MM;
             const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
             const bool pad = row0 + RPW * q4 >= a.R;   // the warp holds no row of the block
@@ -717,9 +720,10 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 }
 
 constexpr int KT_SEAM = 8;
+constexpr int KT_WEIGHT = 1;
 constexpr int KT_SMS = 152;   // SMs of a GB300
 
-int kt_grid(int64_t units) { return (int)std::min<int64_t>((units + KT_PIPES - 1) / KT_PIPES, KT_SMS); }
+int kt_grid(int64_t units) { return (int)std::min<int64_t>(units, KT_SMS); }
 
 inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
@@ -728,6 +732,8 @@ inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 int kv4_attn_tc_unit_log2(int R, int hd) { return kt_unit(hd, kv4_attn_tc_rows(R)) == 128 ? 7 : 6; }
 
 int kv4_attn_tc_seam() { return KT_SEAM; }
+
+int kv4_attn_tc_weight() { return KT_WEIGHT; }
 
 size_t kv4_attn_tc_ws_bytes(int R, int hd) {
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * kv4_attn_tc_rows(R);
