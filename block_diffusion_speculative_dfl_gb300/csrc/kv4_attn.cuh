@@ -236,18 +236,33 @@ __global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const K
     const int head = hs / a.subs, row0 = (hs - head * a.subs) * ROWS;
     const int row = blockIdx.y * KJ_ROWS + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;
     if (row >= ROWS || r >= a.R) return;
+    // eight partials are read at once: a long triple waits for memory once per eight
+    constexpr int BATCH = 8;
     float M = -INFINITY, L = 0.f;
-    #pragma unroll 4
-    for (int j = first; j <= last; ++j) M = fmaxf(M, a.ml[(2 * j + (j == first)) * ROWS + row].x);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    #pragma unroll 4
-    for (int j = first; j <= last; ++j) {
-        const int64_t at = (int64_t)(2 * j + (j == first)) * ROWS + row;
-        const float2 ml = a.ml[at];
-        const float4 v = *reinterpret_cast<const float4*>(a.Opart + at * HD + c);
-        const float f = ml.x == -INFINITY ? 0.f : ex2_ftz(ml.x - M);
-        L += f * ml.y;
-        o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+    #pragma unroll 1
+    for (int j0 = first; j0 <= last; j0 += BATCH) {
+        float2 ml[BATCH];
+        float4 v[BATCH];
+        float mn = M;
+        #pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int j = min(j0 + i, last);
+            const int64_t at = (int64_t)(2 * j + (j == first)) * ROWS + row;
+            ml[i] = a.ml[at];
+            v[i] = *reinterpret_cast<const float4*>(a.Opart + at * HD + c);
+        }
+        #pragma unroll
+        for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, ml[i].x);
+        const float old = M == -INFINITY ? 0.f : ex2_ftz(M - mn);
+        M = mn;
+        L *= old; o.x *= old; o.y *= old; o.z *= old; o.w *= old;
+        #pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float f = ml[i].x == -INFINITY || j0 + i > last ? 0.f : ex2_ftz(ml[i].x - M);
+            L += f * ml[i].y;
+            o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
+        }
     }
     const float inv = __fdividef(a.v_pow2, L);
     const int64_t at = ka_row(a, f.n, head, r, HD) + c;
