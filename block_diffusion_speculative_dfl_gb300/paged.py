@@ -42,7 +42,8 @@ class PagedCache:
         self.table = self.book[:N * max_pages].view(N, max_pages)
         self.len = self.book[N * max_pages:N * max_pages + N]
         self.ref = self.book[N * max_pages + N:]
-        self._index = self.book.device.index
+        self._index = self.book.get_device()
+        self._lib = _lib.load()
         self.table.fill_(-1)
         self.start = torch.zeros((N,), dtype=torch.int32, device=dev)
         self.map = torch.zeros((num_pages,), dtype=torch.int32, device=dev)
@@ -55,43 +56,47 @@ class PagedCache:
                             _lib.workspace_size(_lib.DFL_OP_PAGES_REMAP, N=N, pages=max_pages),
                             _lib.workspace_size(_lib.DFL_OP_PAGES_COMPACT, pages=num_pages))
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
-        self._attn_ws = {}
+        self._start, self._map, self._live, self._ws = (_lib.ptr(x) for x in (self.start, self.map, self.live, self.ws))
+        self._attn_ws = {}   # (B, Hq) -> scratch, its address and size
 
     def _st(self, stream):
         if torch.cuda.current_device() != self._index:
             raise ValueError(f"the cache lives on cuda:{self._index}, which is not the current device")
+        if stream is None:   # the current stream's handle, without a Stream object (3 us of a call's 10)
+            return torch._C._cuda_getCurrentRawStream(self._index)
         return _lib._stream(stream)
 
     def _i32(self, x, what):
-        if x.dtype != torch.int32 or not x.is_contiguous() or x.device != self.book.device or x.numel() != self.N:
+        if x.dtype is not torch.int32 or not x.is_contiguous() or x.get_device() != self._index or x.numel() != self.N:
             raise ValueError(f"{what} must be a contiguous int32 tensor of {self.N} elements on {self.book.device}")
         return x.data_ptr()
 
-    def _rows(self, x, what, rows=None):
-        """Check a bf16 [N, R, heads, hd] tensor; returns its pointer."""
-        if x.dtype != torch.bfloat16 or not x.is_contiguous() or x.device != self.book.device or x.dim() != 4 or \
-                x.shape[0] != self.N or x.shape[3] != self.hd or x.shape[2] != (rows or x.shape[2]):
-            raise ValueError(f"{what} must be a contiguous bf16 tensor [{self.N}, rows, {rows or 'heads'}, {self.hd}] "
-                             f"on {self.book.device}")
-        return x.data_ptr()
+    def _rows(self, x, what, heads=None, rows=None):
+        """Check a bf16 [N, rows, heads, hd] tensor; returns its pointer and rows."""
+        shape = x.shape
+        if x.dtype is not torch.bfloat16 or not x.is_contiguous() or x.get_device() != self._index or len(shape) != 4 or \
+                shape[0] != self.N or shape[3] != self.hd or (heads and shape[2] != heads) or (rows and shape[1] != rows):
+            raise ValueError(f"{what} must be a contiguous bf16 tensor [{self.N}, {rows or 'rows'}, {heads or 'heads'}, "
+                             f"{self.hd}] on {self.book.device}")
+        return x.data_ptr(), shape[1]
 
     def append(self, layer, K, V, start, n_new, stream=None):
         """Rows K[n, i], V[n, i] (i < n_new[n]) to positions start[n] + i; K, V bf16 [N, R, Hkv, hd]."""
-        k, v = self._rows(K, "K", self.Hkv), self._rows(V, "V", self.Hkv)
-        if K.shape != V.shape:
-            raise ValueError("K and V differ in shape")
-        _lib._check("dfl_kv4_append", _lib.load().dfl_kv4_append(
-            self._pool, layer, self._pages, self._i32(start, "start"), self._i32(n_new, "n_new"), K.shape[1], k, v,
-            self._st(stream)))
+        k, R = self._rows(K, "K", self.Hkv)
+        v, _ = self._rows(V, "V", self.Hkv, R)
+        rc = self._lib.dfl_kv4_append(self._pool, layer, self._pages, self._i32(start, "start"),
+                                      self._i32(n_new, "n_new"), R, k, v, self._st(stream))
+        if rc:
+            _lib._check("dfl_kv4_append", rc)
 
     def read(self, layer, start, count, K, V, stream=None):
         """Positions start[n] .. start[n] + count[n] - 1 into K[n, i], V[n, i] (other rows keep what they hold)."""
-        k, v = self._rows(K, "K", self.Hkv), self._rows(V, "V", self.Hkv)
-        if K.shape != V.shape:
-            raise ValueError("K and V differ in shape")
-        _lib._check("dfl_kv4_read", _lib.load().dfl_kv4_read(
-            self._pool, layer, self._pages, self._i32(start, "start"), self._i32(count, "count"), K.shape[1], k, v,
-            self._st(stream)))
+        k, R = self._rows(K, "K", self.Hkv)
+        v, _ = self._rows(V, "V", self.Hkv, R)
+        rc = self._lib.dfl_kv4_read(self._pool, layer, self._pages, self._i32(start, "start"),
+                                    self._i32(count, "count"), R, k, v, self._st(stream))
+        if rc:
+            _lib._check("dfl_kv4_read", rc)
         return K, V
 
     def attn(self, layer, Q, Kb, Vb, out=None, stream=None):
@@ -99,40 +104,43 @@ class PagedCache:
 
         Q bf16 [N, B, Hq, hd], Kb, Vb bf16 [N, B, Hkv, hd]; returns O bf16 [N, B, Hq, hd].
         """
-        B, Hq = Q.shape[1], Q.shape[2]
-        q, k, v = self._rows(Q, "Q"), self._rows(Kb, "Kb", self.Hkv), self._rows(Vb, "Vb", self.Hkv)
-        if Kb.shape[1] != B or Vb.shape[1] != B:
-            raise ValueError("Kb and Vb must have Q's rows")
+        q, B = self._rows(Q, "Q")
+        Hq = Q.shape[2]
+        k, _ = self._rows(Kb, "Kb", self.Hkv, B)
+        v, _ = self._rows(Vb, "Vb", self.Hkv, B)
         if out is None:
             out = torch.empty_like(Q)
-        o = self._rows(out, "out", Hq)
-        if out.shape != Q.shape:
-            raise ValueError("out must have Q's shape")
+        o, _ = self._rows(out, "out", Hq, B)
         ws = self._attn_ws.get((B, Hq))
         if ws is None:
             need = _lib.workspace_size(_lib.DFL_OP_KV4_ATTN, N=self.N, B=B, Hq=Hq, Hkv=self.Hkv, hd=self.hd)
-            ws = self._attn_ws[(B, Hq)] = torch.empty(max(need, 16), dtype=torch.uint8, device=self.book.device)
-        _lib._check("dfl_kv4_attn", _lib.load().dfl_kv4_attn(
-            self._pool, layer, self._pages, q, k, v, B, Hq, o, ws.data_ptr(), ws.numel(), self._st(stream)))
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.book.device)
+            ws = self._attn_ws[(B, Hq)] = (ws, ws.data_ptr(), ws.numel())
+        rc = self._lib.dfl_kv4_attn(self._pool, layer, self._pages, q, k, v, B, Hq, o, ws[1], ws[2], self._st(stream))
+        if rc:
+            _lib._check("dfl_kv4_attn", rc)
         return out
 
     def reserve(self, n_new, stream=None):
         """Pages for n_new[n] more tokens; returns ``start`` (a buffer of the cache): the old lengths, -1 where not served."""
-        _lib._check("dfl_pages_reserve", _lib.load().dfl_pages_reserve(
-            self._pool, self._pages, self._i32(n_new, "n_new"), self.start.data_ptr(), self.ws.data_ptr(),
-            self.ws_bytes, self._st(stream)))
+        rc = self._lib.dfl_pages_reserve(self._pool, self._pages, self._i32(n_new, "n_new"), self._start, self._ws,
+                                         self.ws_bytes, self._st(stream))
+        if rc:
+            _lib._check("dfl_pages_reserve", rc)
         return self.start
 
     def remap(self, parent, keep_len=None, stream=None):
         """Sequence n becomes sequence parent[n] cut to keep_len[n] tokens (fork, reorder, roll back, end: -1)."""
-        _lib._check("dfl_pages_remap", _lib.load().dfl_pages_remap(
-            self._pool, self._pages, self._i32(parent, "parent"),
-            None if keep_len is None else self._i32(keep_len, "keep_len"), self.ws.data_ptr(), self.ws_bytes,
-            self._st(stream)))
+        keep = None if keep_len is None else self._i32(keep_len, "keep_len")
+        rc = self._lib.dfl_pages_remap(self._pool, self._pages, self._i32(parent, "parent"), keep, self._ws,
+                                       self.ws_bytes, self._st(stream))
+        if rc:
+            _lib._check("dfl_pages_remap", rc)
 
     def compact(self, stream=None):
         """Used pages to the pool's low end; returns (map, live), buffers of the cache."""
-        _lib._check("dfl_pages_compact", _lib.load().dfl_pages_compact(
-            self._pool, self._pages, self.map.data_ptr(), self.live.data_ptr(), self.ws.data_ptr(), self.ws_bytes,
-            self._st(stream)))
+        rc = self._lib.dfl_pages_compact(self._pool, self._pages, self._map, self._live, self._ws, self.ws_bytes,
+                                         self._st(stream))
+        if rc:
+            _lib._check("dfl_pages_compact", rc)
         return self.map, self.live
