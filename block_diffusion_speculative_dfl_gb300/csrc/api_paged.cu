@@ -14,6 +14,7 @@ dfl_status kv4_check(const dfl_kv4_pool* pool, int layer, const dfl_pages* pg) {
     const int64_t bytes = dfl_kv4_page_bytes(pool->page, pool->Hkv, pool->hd);
     if (bytes == 0) return DFL_ERR_UNSUPPORTED_SHAPE;
     if ((int64_t)pool->num_pages * pool->Hkv * (pool->page / 16) >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if ((int64_t)pool->Hkv * pool->hd >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (pool->layer_stride < bytes * pool->num_pages) return DFL_ERR_INVALID_ARG;
     if (!aligned16(pool->data) || pool->layer_stride % 16 != 0) return DFL_ERR_MISALIGNED;
     if (!pg) return DFL_OK;

@@ -98,6 +98,11 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ float2 half2_to_float2(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }

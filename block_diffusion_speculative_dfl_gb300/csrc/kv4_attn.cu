@@ -62,11 +62,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 template <int HD, int NT>
 struct KaCfg {
     static constexpr int ROWS = 8 * NT;               // query rows of a tile

@@ -2,19 +2,24 @@
 //
 // Append, per 16 dimensions x of one token and K/V head (a group):
 //   s = max(2^-9, e4m3(min(448, max|x| 2^-e / 6))),   c = e2m1(x / (s 2^e)).
-// The rounding of c is decided by comparing |x| with the seven borders between
-// neighbouring magnitudes times s 2^e: border (3 bits) x s (4 bits) x a power
-// of two is exact in fp32, so a value on a border goes to the even code as the
-// definition has it; a quotient or a reciprocal would round first.  The
-// quotient max|x| / 6 may round: e4m3's own borders have 5 bits and a bf16 max
-// 8, so an unequal pair differs by more than 2^-13, far above fp32's rounding.
+// x / (s 2^e) is taken as x times the correctly rounded reciprocal and rounded to
+// fp16 before the rounding to e2m1; that decides as the exact quotient would.
+// The borders between e2m1's numbers have 3 bits and s 4, so a border times s
+// 2^e has at most 7 and x, a bf16, has 8: where they differ they do so by 2^-8
+// of their size at least, which neither fp32's 2^-23 nor fp16's 2^-11 moves
+// across; where they are equal the product is within 2^-23 of the border, which
+// fp16 makes the border itself, and it goes to the even code.  The quotient
+// max|x| / 6 may round: e4m3's own borders have 5 bits and a bf16 max 8, so an
+// unequal pair differs by more than 2^-13, far above fp32's rounding.
 // A group with an infinity or a NaN stores the scale NaN: all of it reads back
 // as NaN, and attention to it gives NaN, as a bf16 cache would.
 //
 // Both calls move bytes: 2 B in and 9/16 B out per element (append), the
 // reverse (read).  One thread per group of K and of V: 64 B of loads in flight
 // per thread, 32-byte sectors whole on the bf16 side and 8-byte pieces that
-// neighbouring lanes complete to whole rows on the 4-bit side.
+// neighbouring lanes complete to whole rows on the 4-bit side.  A block takes
+// 256 neighbouring groups of one sequence, so the 64-bit index arithmetic is
+// once per block.
 #include "internal.h"
 #include "kv4.cuh"
 #include "paged.h"
@@ -23,35 +28,72 @@ namespace dfl {
 
 namespace {
 
+constexpr int KR_THREADS = 256;
+
 struct Kv4Rows {
     Kv4Slab slab;
     const int32_t* table;   // [N][max_pages]
     int max_pages;
     const int32_t* start;   // [N] position of row 0 (negative: the sequence is skipped)
     const int32_t* count;   // [N] rows of each sequence
-    int N, R;
+    int R;
+    int width;              // groups of a row: Hkv * hd / 16
+    int64_t items, chunks;  // chunks of KR_THREADS groups in all, per sequence
+    uint64_t cells_inv;     // ceil(2^36 / cells of a page)
     int k_exp, v_exp;
 };
 
-// Position of row i of sequence n -> its cell, or nullptr (row past the
-// count, sequence skipped, or, recorded, a length or page out of range).
+// The group a thread has in chunk `item`.
+struct Kv4Item {
+    int n, i, head, group;  // sequence, row, head, group of the head
+    int64_t at;             // the group among all of K
+    int start;              // position of row 0
+    bool on;                // the row exists
+};
+
 template <int HD>
-__device__ __forceinline__ uint8_t* row_cell(const Kv4Rows& a, int n, int i, int head, const DevErr& err, int& tok) {
-    const int s = a.start[n], m = a.count[n];
-    if (s < 0 && m >= 0 && m <= a.R) return nullptr;
-    if (m < 0 || m > a.R || s > a.max_pages * a.slab.page - m) {
-        if (i == 0 && head == 0) record_error(err, DFL_ERR_INVALID_ARG);
-        return nullptr;
-    }
-    if (i >= m) return nullptr;
-    const int pos = s + i, j = pos / a.slab.page, in = pos - j * a.slab.page;
-    const int p = a.table[(int64_t)n * a.max_pages + j];
+__device__ __forceinline__ Kv4Item kv4_item(const Kv4Rows& a, int64_t item, const DevErr& err) {
+    constexpr int GROUPS = Kv4Cell<HD>::GROUPS;
+    Kv4Item t;
+    t.n = (int)(item / a.chunks);
+    const int64_t first = (item - t.n * a.chunks) * KR_THREADS;   // of the sequence's groups
+    const int64_t row0 = first / a.width;
+    const int y = (int)(first - row0 * a.width) + (int)threadIdx.x;
+    const int down = y / a.width, x = y - down * a.width;
+    t.head = x / GROUPS;
+    t.group = x % GROUPS;
+    t.start = a.start[t.n];
+    const int m = a.count[t.n];
+    const int64_t i = row0 + down;
+    bool ok = m >= 0 && m <= a.R && (t.start < 0 || t.start <= a.max_pages * a.slab.page - m);
+    if (!ok && first == 0 && threadIdx.x == 0) record_error(err, DFL_ERR_INVALID_ARG);
+    t.on = ok && t.start >= 0 && i < m;
+    t.i = (int)i;
+    t.at = ((int64_t)t.n * a.R + i) * a.width + x;
+    return t;
+}
+
+// The cell of a row that exists, or nullptr (its page is out of range: recorded).
+template <int HD>
+__device__ __forceinline__ uint8_t* row_cell(const Kv4Rows& a, const Kv4Item& t, const DevErr& err, int& tok) {
+    const int pos = t.start + t.i;
+    const uint32_t c = (uint32_t)pos / KV4_CELL_TOKENS;
+    const int j = (int)((c * a.cells_inv) >> 36);   // c / cells: c < 2^27, cells <= 64
+    const int p = a.table[(int64_t)t.n * a.max_pages + j];
     if (p < 0 || p >= a.slab.num_pages) {
         record_error(err, DFL_ERR_INVALID_ARG);
         return nullptr;
     }
-    tok = in & (KV4_CELL_TOKENS - 1);
-    return a.slab.data + (((int64_t)p * a.slab.Hkv + head) * a.slab.cells + in / KV4_CELL_TOKENS) * Kv4Cell<HD>::BYTES;
+    tok = pos & (KV4_CELL_TOKENS - 1);
+    const int cell = (p * a.slab.Hkv + t.head) * a.slab.cells + ((int)c - j * a.slab.cells);   // < 2^31 (checked)
+    return a.slab.data + (int64_t)cell * Kv4Cell<HD>::BYTES;
+}
+
+// Two floats -> two e2m1 codes (a in the low nibble), nearest, ties to even, larger ones to 6.
+__device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\tcvt.u32.u8 %0, t;\n\t}" : "=r"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 __device__ __forceinline__ void quantise16(const uint4 lo, const uint4 hi, int e, uint2& codes, uint8_t& scale) {
@@ -65,46 +107,45 @@ __device__ __forceinline__ void quantise16(const uint4 lo, const uint4 hi, int e
     uint16_t sb;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.f), "f"(q));
     scale = max((int)(sb & 0xFF), 1);   // code 1 is 2^-9, the smallest scale
-    const float t = half2_to_float2(e4m3x2_to_half(scale)).x * kv4_exp2i(e);
-    uint32_t c[2] = {0, 0};
+    const float r = __frcp_rn(half2_to_float2(e4m3x2_to_half(scale)).x * kv4_exp2i(e));
+    uint32_t c[2];
     #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const uint32_t b = i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16;
-        const float a = fabsf(__uint_as_float(b));
-        uint32_t k = (a > 0.25f * t) + (a >= 0.75f * t) + (a > 1.25f * t) + (a >= 1.75f * t) + (a > 2.5f * t) +
-                     (a >= 3.5f * t) + (a > 5.f * t);
-        k |= (b >> 28) & 8u;
-        c[i / 8] |= k << (4 * (i % 8));
+    for (int j = 0; j < 2; ++j) {
+        uint32_t b[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t h = pack_half(bf16lo(w[4 * j + i]) * r, bf16hi(w[4 * j + i]) * r);
+            const float2 f = half2_to_float2(h);
+            b[i] = e2m1x2(f.x, f.y);
+        }
+        c[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     }
     codes = make_uint2(c[0], c[1]);
 }
 
 template <int HD>
-__global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Rows a, const uint4* K, const uint4* V, const DevErr err) {
+__global__ void __launch_bounds__(KR_THREADS) kv4_append_kernel(const Kv4Rows a, const uint4* K, const uint4* V, const DevErr err) {
     grid_dep_begin();
     using Cell = Kv4Cell<HD>;
-    const int64_t total = (int64_t)a.N * a.R * a.slab.Hkv * Cell::GROUPS;
-    for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < total; x += (int64_t)gridDim.x * blockDim.x) {
-        const int group = (int)(x % Cell::GROUPS);
-        const int64_t rh = x / Cell::GROUPS;
-        const int head = (int)(rh % a.slab.Hkv);
-        const int64_t row = rh / a.slab.Hkv;
-        const int n = (int)(row / a.R), i = (int)(row - (int64_t)n * a.R);
+    #pragma unroll 1
+    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+        const Kv4Item t = kv4_item<HD>(a, item, err);
+        if (!t.on) continue;
+        const uint4 k0 = K[2 * t.at], k1 = K[2 * t.at + 1], v0 = V[2 * t.at], v1 = V[2 * t.at + 1];
         int tok;
-        uint8_t* cell = row_cell<HD>(a, n, i, head, err, tok);
+        uint8_t* cell = row_cell<HD>(a, t, err, tok);
         if (!cell) continue;
-        const uint4 k0 = K[2 * x], k1 = K[2 * x + 1], v0 = V[2 * x], v1 = V[2 * x + 1];
         if (!DFL_IN_BOUNDS(err.word, cell - a.slab.data,
                            (int64_t)a.slab.num_pages * a.slab.Hkv * a.slab.cells * Cell::BYTES))
             continue;
         uint2 c;
         uint8_t s;
         quantise16(k0, k1, a.k_exp, c, s);
-        *reinterpret_cast<uint2*>(cell + Cell::k_code(tok, group)) = c;
-        cell[Cell::k_scale(tok, group)] = s;
+        *reinterpret_cast<uint2*>(cell + Cell::k_code(tok, t.group)) = c;
+        cell[Cell::k_scale(tok, t.group)] = s;
         quantise16(v0, v1, a.v_exp, c, s);
-        *reinterpret_cast<uint2*>(cell + Cell::v_code(tok, group)) = c;
-        cell[Cell::v_scale(tok, group)] = s;
+        *reinterpret_cast<uint2*>(cell + Cell::v_code(tok, t.group)) = c;
+        cell[Cell::v_scale(tok, t.group)] = s;
     }
 }
 
@@ -126,40 +167,43 @@ __device__ __forceinline__ void expand16(uint2 codes, uint8_t scale, float pow2,
 }
 
 template <int HD>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4Rows a, uint4* K, uint4* V, const DevErr err) {
+__global__ void __launch_bounds__(KR_THREADS) kv4_read_kernel(const Kv4Rows a, uint4* K, uint4* V, const DevErr err) {
     grid_dep_begin();
     using Cell = Kv4Cell<HD>;
     const float pk = kv4_exp2i(a.k_exp), pv = kv4_exp2i(a.v_exp);
-    const int64_t total = (int64_t)a.N * a.R * a.slab.Hkv * Cell::GROUPS;
-    for (int64_t x = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; x < total; x += (int64_t)gridDim.x * blockDim.x) {
-        const int group = (int)(x % Cell::GROUPS);
-        const int64_t rh = x / Cell::GROUPS;
-        const int head = (int)(rh % a.slab.Hkv);
-        const int64_t row = rh / a.slab.Hkv;
-        const int n = (int)(row / a.R), i = (int)(row - (int64_t)n * a.R);
+    #pragma unroll 1
+    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+        const Kv4Item t = kv4_item<HD>(a, item, err);
+        if (!t.on) continue;
         int tok;
-        const uint8_t* cell = row_cell<HD>(a, n, i, head, err, tok);
+        const uint8_t* cell = row_cell<HD>(a, t, err, tok);
         if (!cell) continue;
-        const uint2 kc = *reinterpret_cast<const uint2*>(cell + Cell::k_code(tok, group));
-        const uint2 vc = *reinterpret_cast<const uint2*>(cell + Cell::v_code(tok, group));
+        const uint2 kc = *reinterpret_cast<const uint2*>(cell + Cell::k_code(tok, t.group));
+        const uint2 vc = *reinterpret_cast<const uint2*>(cell + Cell::v_code(tok, t.group));
         uint4 lo, hi;
-        expand16(kc, cell[Cell::k_scale(tok, group)], pk, lo, hi);
-        K[2 * x] = lo;
-        K[2 * x + 1] = hi;
-        expand16(vc, cell[Cell::v_scale(tok, group)], pv, lo, hi);
-        V[2 * x] = lo;
-        V[2 * x + 1] = hi;
+        expand16(kc, cell[Cell::k_scale(tok, t.group)], pk, lo, hi);
+        K[2 * t.at] = lo;
+        K[2 * t.at + 1] = hi;
+        expand16(vc, cell[Cell::v_scale(tok, t.group)], pv, lo, hi);
+        V[2 * t.at] = lo;
+        V[2 * t.at + 1] = hi;
     }
 }
 
 Kv4Rows rows_args(const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const int32_t* start, const int32_t* count,
                   int R) {
-    return Kv4Rows{kv4_slab(pool, layer), pg.table, pg.max_pages, start, count, pg.N, R, pool.k_exp, pool.v_exp};
+    Kv4Rows a{kv4_slab(pool, layer), pg.table, pg.max_pages, start, count, R};
+    a.width = pool.Hkv * (pool.hd / 16);
+    a.chunks = ((int64_t)R * a.width + KR_THREADS - 1) / KR_THREADS;
+    a.items = a.chunks * pg.N;
+    a.cells_inv = (((uint64_t)1 << 36) + a.slab.cells - 1) / a.slab.cells;
+    a.k_exp = pool.k_exp;
+    a.v_exp = pool.v_exp;
+    return a;
 }
 
-unsigned rows_grid(const DeviceCtx* ctx, const Kv4Rows& a, int hd) {
-    const int64_t total = (int64_t)a.N * a.R * a.slab.Hkv * (hd / 16);
-    return (unsigned)std::min<int64_t>((total + 255) / 256, (int64_t)ctx->sm_count * 64);
+unsigned rows_grid(const DeviceCtx* ctx, const Kv4Rows& a) {
+    return (unsigned)std::min<int64_t>(a.items, (int64_t)ctx->sm_count * 64);
 }
 
 }  // namespace
@@ -170,7 +214,7 @@ dfl_status kv4_append_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, c
     ProfScope ps("kv4_append", st);
     const Kv4Rows a = rows_args(pool, layer, pg, start, n_new, R);
     auto kern = pool.hd == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>;
-    return launch_pdl(kern, rows_grid(ctx, a, pool.hd), 256, 0, st, a, static_cast<const uint4*>(K),
+    return launch_pdl(kern, rows_grid(ctx, a), KR_THREADS, 0, st, a, static_cast<const uint4*>(K),
                       static_cast<const uint4*>(V), dev_err(ctx));
 }
 
@@ -179,7 +223,7 @@ dfl_status kv4_read_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     ProfScope ps("kv4_read", st);
     const Kv4Rows a = rows_args(pool, layer, pg, start, count, R);
     auto kern = pool.hd == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
-    return launch_pdl(kern, rows_grid(ctx, a, pool.hd), 256, 0, st, a, static_cast<uint4*>(K), static_cast<uint4*>(V),
+    return launch_pdl(kern, rows_grid(ctx, a), KR_THREADS, 0, st, a, static_cast<uint4*>(K), static_cast<uint4*>(V),
                       dev_err(ctx));
 }
 
