@@ -19,6 +19,7 @@ namespace {
 
 constexpr int PG_PLAN = 1024;        // threads of a planning block
 constexpr int PG_PASS = PG_PLAN * 32;  // pages per pass
+constexpr int PG_FEW = 4096;         // free pages that are handed out from shared memory
 constexpr int PG_PIECE = 16384;      // bytes a block copies at a time
 constexpr int PG_THREADS = 256;
 
@@ -77,18 +78,25 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
                                                                     int32_t* start, const ReservePlan p,
                                                                     const DevErr err) {
     __shared__ int red[PG_PLAN / 32];
+    __shared__ int cows;
+    __shared__ int32_t few[PG_FEW];
     grid_dep_begin();
+    if (threadIdx.x == 0) cows = 0;
+    const bool one = a.N <= PG_PLAN;   // a sequence per thread: what it asks for stays in registers
+    // the first counts are read while the requests are looked up
+    const uint32_t used0 = used_mask(a.ref, a.num_pages, 0);
     // what each sequence asks for, on the counts as they were before the call
-    int asked = 0;
+    int asked = 0, need = 0, off = 0, tail = -1, l = 0, m = 0;
     for (int base = 0; base < a.N; base += PG_PLAN) {
         const int n = base + threadIdx.x;
-        int need = 0;
+        need = 0;
+        tail = -1;
         if (n < a.N) {
-            const int l = a.len[n], m = n_new[n];
-            int tail = -1;
+            l = a.len[n];
+            m = n_new[n];
             if (l < 0 || m < 0 || m > max_new || l > a.max_pages * a.page - m) {
                 record_error(err, DFL_ERR_INVALID_ARG);
-                p.need[n] = -1;
+                need = -1;
             } else {
                 const int have = (l + a.page - 1) / a.page;
                 need = (l + m + a.page - 1) / a.page - have;
@@ -97,56 +105,60 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
                     if (t < 0 || t >= a.num_pages) record_error(err, DFL_ERR_INVALID_ARG);
                     else if (a.ref[t] > 1) { tail = t; ++need; }
                 }
-                p.need[n] = need;
             }
-            p.tail[n] = tail;
         }
         int sum;
-        const int pre = block_exscan<PG_PLAN>(need, red, &sum);
-        if (n < a.N) p.off[n] = asked + pre;
+        off = asked + block_exscan<PG_PLAN>(max(need, 0), red, &sum);
         asked += sum;
+        if (!one && n < a.N) { p.off[n] = off; p.need[n] = need; p.tail[n] = tail; }
     }
     // the first `asked` free pages
+    int32_t* free_ = asked <= PG_FEW ? few : p.free_;
     int found = 0;
     for (int base = 0; base < a.num_pages && found < asked; base += PG_PASS) {
         const int first = base + (int)threadIdx.x * 32;
-        uint32_t f = ~used_mask(a.ref, a.num_pages, base) & low_bits(valid_count(a.num_pages, first));
+        const uint32_t u = base == 0 ? used0 : used_mask(a.ref, a.num_pages, base);
+        uint32_t f = ~u & low_bits(valid_count(a.num_pages, first));
         int sum;
         int k = found + block_exscan<PG_PLAN>(__popc(f), red, &sum);
-        for (; f && k < asked; f &= f - 1) p.free_[k++] = first + __ffs(f) - 1;
+        for (; f && k < asked; f &= f - 1) free_[k++] = first + __ffs(f) - 1;
         found += sum;
     }
     __syncthreads();   // the lists are read by other threads (and the counts are written) from here on
-    // hand the pages out, a warp per sequence
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* cows = red;
-    if (threadIdx.x == 0) *cows = 0;
-    __syncthreads();
-    for (int n = warp; n < a.N; n += PG_PLAN / 32) {
-        const int need = p.need[n], off = p.off[n], tail = p.tail[n];
-        const bool served = need == 0 || (need > 0 && off + need <= found);
-        const int l = a.len[n];
-        if (served) {
-            const int first = (l + a.page - 1) / a.page - (tail >= 0 ? 1 : 0);
-            for (int k = lane; k < need; k += 32) {
-                const int f = p.free_[off + k];
-                a.table[(int64_t)n * a.max_pages + first + k] = f;
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < a.N; base += PG_PLAN) {
+        const int n = base + threadIdx.x;
+        if (!one && n < a.N) {
+            off = p.off[n]; need = p.need[n]; tail = p.tail[n];
+            l = a.len[n];
+            m = need < 0 ? 0 : n_new[n];
+        }
+        const bool served = n < a.N && (need == 0 || (need > 0 && off + need <= found));
+        if (served && tail >= 0) {
+            const int c = atomicAdd(&cows, 1);   // the order of copies does not matter
+            p.cow.src[c] = tail;
+            p.cow.dst[c] = free_[off];
+            atomicSub(&a.ref[tail], 1);
+        }
+        if (n < a.N) {
+            start[n] = served ? l : -1;
+            if (served) a.len[n] = l + m;
+        }
+        // the pages of a warp's sequences, one sequence after another, a page per lane
+        const int first = (l + a.page - 1) / a.page - (tail >= 0 ? 1 : 0);
+        for (uint32_t who = __ballot_sync(0xFFFFFFFFu, served && need > 0); who; who &= who - 1) {
+            const int j = __ffs(who) - 1;
+            const int nj = __shfl_sync(0xFFFFFFFFu, need, j), oj = __shfl_sync(0xFFFFFFFFu, off, j);
+            int32_t* row = a.table + (int64_t)(n - lane + j) * a.max_pages + __shfl_sync(0xFFFFFFFFu, first, j);
+            for (int k = lane; k < nj; k += 32) {
+                const int f = free_[oj + k];
+                row[k] = f;
                 a.ref[f] = 1;
             }
-            if (lane == 0 && tail >= 0) {
-                const int c = atomicAdd(cows, 1);   // the order of copies does not matter
-                p.cow.src[c] = tail;
-                p.cow.dst[c] = p.free_[off];
-                atomicSub(&a.ref[tail], 1);
-            }
-        }
-        if (lane == 0) {
-            start[n] = served ? l : -1;
-            if (served) a.len[n] = l + n_new[n];
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) *p.cow.count = *cows;
+    if (threadIdx.x == 0) *p.cow.count = cows;
 }
 
 // Copies whole pages src[k] -> dst[k] of every layer, in pieces.
@@ -229,16 +241,17 @@ __global__ void __launch_bounds__(PG_PLAN) pages_compact_plan_kernel(const PgArg
                                                                     const PgMoves mv) {
     __shared__ int red[PG_PLAN / 32];
     grid_dep_begin();
-    int cnt = 0;
-    for (int base = 0; base < a.num_pages; base += PG_PASS) cnt += __popc(used_mask(a.ref, a.num_pages, base));
+    const uint32_t used0 = used_mask(a.ref, a.num_pages, 0);
+    int cnt = __popc(used0);
+    for (int base = PG_PASS; base < a.num_pages; base += PG_PASS) cnt += __popc(used_mask(a.ref, a.num_pages, base));
     int m;
     block_exscan<PG_PLAN>(cnt, red, &m);   // m: live pages, the new size of the pool's used part
     // holes below m take the live pages from m on, both in order
+    const int lane = threadIdx.x & 31;
     int holes = 0, movers = 0;
     for (int base = 0; base < a.num_pages; base += PG_PASS) {
         const int first = base + (int)threadIdx.x * 32;
-        const int nv = valid_count(a.num_pages, first);
-        const uint32_t u = used_mask(a.ref, a.num_pages, base);
+        const uint32_t u = base == 0 ? used0 : used_mask(a.ref, a.num_pages, base);
         const uint32_t low = low_bits(valid_count(m, first));   // the pages below m (m <= num_pages)
         const uint32_t h = ~u & low, v = u & ~low;
         int sh, sv;
@@ -246,12 +259,17 @@ __global__ void __launch_bounds__(PG_PLAN) pages_compact_plan_kernel(const PgArg
         int kv = movers + block_exscan<PG_PLAN>(__popc(v), red, &sv);
         for (uint32_t f = h; f; f &= f - 1) mv.dst[kh++] = first + __ffs(f) - 1;
         for (uint32_t f = v; f; f &= f - 1) mv.src[kv++] = first + __ffs(f) - 1;
-        for (int i = 0; i < nv; ++i)
-            if (!(v >> i & 1)) map[first + i] = u >> i & 1 ? first + i : -1;
+        const int first0 = first - 32 * lane;   // of the warp's 1024 pages
+        for (int i = 0; i < 32 && first0 + 32 * i < a.num_pages; ++i) {
+            const int pg = first0 + 32 * i + lane;
+            const bool used = __shfl_sync(0xFFFFFFFFu, u, i) >> lane & 1;
+            if (pg < a.num_pages) map[pg] = used ? pg : -1;   // pages that move: below
+        }
         holes += sh;
         movers += sv;
     }
     __syncthreads();
+    #pragma unroll 4
     for (int k = threadIdx.x; k < movers; k += PG_PLAN) {
         const int s = mv.src[k], d = mv.dst[k];
         map[s] = d;
