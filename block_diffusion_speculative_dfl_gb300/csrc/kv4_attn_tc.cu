@@ -50,9 +50,10 @@ struct KtCfg {
     static constexpr int TILE = KB * TKB;
     static constexpr int Q = KB * QKB;
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
-    // slots per pipeline: 32 tokens of codes per expander, K tiles, V tiles
-    static constexpr int RST = HD == 128 ? 3 : 4, KST = HD == 64 ? 2 : 1, VST = KST;
-    static constexpr int PIPE = Q + (KST + VST) * TILE + RST * 4 * CELL;
+    // slots per pipeline: K or V codes of an expander's share of a unit, K and V tiles
+    static constexpr int RST = HD == 128 ? (KU == 128 ? 3 : 6) : 4, ST = HD == 64 ? 2 : 1;
+    static constexpr int SLOT = KU / 4 / KV4_CELL_TOKENS * CELL / 2;
+    static constexpr int PIPE = Q + 2 * ST * TILE + RST * 4 * SLOT;
     static constexpr int S_COL = 0, O_COL = 128, COLS = 256;
     static constexpr int SMEM = 1024 + KT_PIPES * PIPE;
     static_assert(KU <= O_COL && O_COL + HD <= COLS, "tensor memory columns");
@@ -60,11 +61,10 @@ struct KtCfg {
     static_assert(PIPE % 1024 == 0, "tiles start on 1024-byte boundaries");
 };
 
-template <int RST, int KST, int VST>
+template <int RST, int ST>
 struct KtBars {
     uint64_t raw_full[4][RST];   // of each expander
-    uint64_t k_full[KST], k_empty[KST];
-    uint64_t v_full[VST], v_empty[VST];
+    uint64_t t_full[2][ST], t_empty[2][ST];   // of the K and the V tiles
     uint64_t q_full, s_full, p_full, pv_done, o_empty, drain;
 };
 
@@ -142,23 +142,31 @@ struct KtExpandK {   // scores of tokens past the length are masked
         const uint32_t codes = half + h * Cell::ROW + 4 * c;
         const uint32_t scales = half + Cell::K_SCALES + (HD == 128 ? h * 16 + (c >> 2) * 4 : h * 8 + (c >> 1) * 2);
         const uint32_t at = kt_piece<KU>(tile, Cell::token(h), c);
-        #pragma unroll 1
-        for (int i = 0; i < 8 / RPL; ++i) {           // slots s and s + 8, s = RPL i + h
-            const uint32_t w0 = lds32(codes + RPL * i * Cell::ROW), w1 = lds32(codes + (RPL * i + 8) * Cell::ROW);
+        constexpr int NI = 8 / RPL;
+        uint32_t w[2 * NI], sw[NI];                   // all of the lane's codes and scales are on their way before the first is used
+        #pragma unroll
+        for (int i = 0; i < NI; ++i) {                // slots s and s + 8, s = RPL i + h
+            if constexpr (HD == 128) sw[i] = lds32(scales + RPL * i * 16);
+            else sw[i] = lds16(scales + RPL * i * 8);
+            w[2 * i] = lds32(codes + RPL * i * Cell::ROW);
+            w[2 * i + 1] = lds32(codes + (RPL * i + 8) * Cell::ROW);
+        }
+        #pragma unroll
+        for (int i = 0; i < NI; ++i) {
             uint32_t s0, s1;
             if constexpr (HD == 128) {
-                const uint32_t sw = lds32(scales + RPL * i * 16), sel = c & 2 ? 0x3232u : 0x1010u;
-                const uint32_t h0 = e4m3x2_to_half(sw & 0xFFFFu), h1 = e4m3x2_to_half(sw >> 16);
+                const uint32_t sel = c & 2 ? 0x3232u : 0x1010u;
+                const uint32_t h0 = e4m3x2_to_half(sw[i] & 0xFFFFu), h1 = e4m3x2_to_half(sw[i] >> 16);
                 s0 = __byte_perm(h0, h0, sel);
                 s1 = __byte_perm(h1, h1, sel);
             } else {
-                const uint32_t hp = e4m3x2_to_half(lds16(scales + RPL * i * 8));
+                const uint32_t hp = e4m3x2_to_half(sw[i]);
                 s0 = __byte_perm(hp, hp, 0x1010);
                 s1 = __byte_perm(hp, hp, 0x3232);
             }
             const uint32_t d = (at ^ (D * i << 4)) + D * i * 128;
-            sts128(d, kt_expand(w0, s0));
-            sts128(d + 8 * 128, kt_expand(w1, s1));
+            sts128(d, kt_expand(w[2 * i], s0));
+            sts128(d + 8 * 128, kt_expand(w[2 * i + 1], s1));
         }
     }
 };
@@ -171,21 +179,26 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
         const int pos = lane % WPR, h = lane / WPR;
         const uint32_t codes = half + h * Cell::ROW + 4 * pos;
         const uint32_t scales = half + (Cell::V_SCALES - Cell::V_CODES) + h * 4;
-        #pragma unroll 1
-        for (int b = 0; b < 4 / RPL; ++b) {           // tokens t, 4 + t, 8 + t, 12 + t, t = RPL b + h
+        constexpr int NB = 4 / RPL;
+        uint32_t w[4 * NB], sw[NB];
+        #pragma unroll
+        for (int b = 0; b < NB; ++b) {                // tokens t, 4 + t, 8 + t, 12 + t, t = RPL b + h
             const int c = HD == 128 && b ? pos ^ 8 : pos;   // tokens 2 and 3 of four: the row's halves trade places
-            const uint32_t sw = lds32(scales + (c >> 1) * 16 + RPL * b * 4);
-            uint32_t w[4];
+            sw[b] = lds32(scales + (c >> 1) * 16 + RPL * b * 4);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = lds32(codes + (4 * i + RPL * b) * Cell::ROW);
+            for (int i = 0; i < 4; ++i) w[4 * b + i] = lds32(codes + (4 * i + RPL * b) * Cell::ROW);
+        }
+        #pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int c = HD == 128 && b ? pos ^ 8 : pos;
             const uint32_t at = kt_piece<KU>(tile, h, c);
-            const uint32_t sp[2] = {e4m3x2_to_half(sw & 0xFFFFu), e4m3x2_to_half(sw >> 16)};
+            const uint32_t sp[2] = {e4m3x2_to_half(sw[b] & 0xFFFFu), e4m3x2_to_half(sw[b] >> 16)};
             #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 4 * i + RPL * b;
                 uint32_t s = __byte_perm(sp[i >> 1], sp[i >> 1], i & 1 ? 0x3232 : 0x1010);
                 if (r + h >= left) s = 0;
-                sts128((at ^ ((r & 7) << 4)) + r * 128, kt_expand(w[i], s));
+                sts128((at ^ ((r & 7) << 4)) + r * 128, kt_expand(w[4 * b + i], s));
             }
         }
     }
@@ -204,51 +217,45 @@ __device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t 
         for (int i = 0; i < NR; ++i) sts128((at ^ (((RPL * i) & 7) << 4)) + RPL * i * 128, make_uint4(0, 0, 0, 0));
         return;
     }
-    #pragma unroll 1
-    for (int i0 = 0; i0 < NR; i0 += 4) {
-        uint4 v[4];
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = RPL * (i0 + i) + h;
-            v[i] = tok < left ? *reinterpret_cast<const uint4*>(src + tok * row_stride + c * 8) : make_uint4(0, 0, 0, 0);
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = RPL * (i0 + i);
-            sts128((at ^ ((r & 7) << 4)) + r * 128, make_uint4(block_half2(v[i].x, inv), block_half2(v[i].y, inv),
-                                                              block_half2(v[i].z, inv), block_half2(v[i].w, inv)));
-        }
+    uint4 v[NR];   // all on their way before the first is used
+    #pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int tok = RPL * i + h;
+        v[i] = tok < left ? *reinterpret_cast<const uint4*>(src + tok * row_stride + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+    #pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int r = RPL * i;
+        sts128((at ^ ((r & 7) << 4)) + r * 128, make_uint4(block_half2(v[i].x, inv), block_half2(v[i].y, inv),
+                                                          block_half2(v[i].z, inv), block_half2(v[i].w, inv)));
     }
 }
 
-// Bulk copies of the half cells that one expander warp needs, 32 tokens per
-// ring slot, ahead of their use.  A warp's share of a unit (KU keys) is its
-// half c, G steps of 32 tokens; steps are numbered along a sequence.
+// Bulk copies of the half cells that one expander warp needs, ahead of their use.
+// A warp's share of a unit is KU / 4 keys; its K half cells are one ring slot
+// and one step, its V half cells the next.  Steps are numbered along a sequence.
 template <int HD, int KU, int RST>
 struct KtFeed {
-    static constexpr int HALF = Kv4Cell<HD>::BYTES / 2, G = KU / 64;
+    static constexpr int HALF = Kv4Cell<HD>::BYTES / 2, SHARE = KU / 4, NC = SHARE / KV4_CELL_TOKENS;
+    static constexpr int WIN = 32 / NC;   // units whose cells the lanes hold
     const KaArgs& a;
     const DevErr& err;
     uint8_t* ring;
     uint64_t* full;
-    const uint8_t* base;       // the pool's first half cell of this kind
-    int c, lane;
+    int w, lane;
     KaPos pos;                 // the segment after the one being copied
     int x, x1;                 // units of the range up to it, and in all
-    int st = 0, end = 0, win = 0, len = 0, n = 0, head = 0;   // step copied next, end of the segment's, first of the window
-    int cells = 0;             // lane 2 i + j: pool cell j of step win + i
+    int st = 0, end = 0, win = 0, len = 0, n = 0, head = 0;   // step copied next, end of the segment's, first unit of the window
+    int cells = 0;             // lane NC i + j: pool cell j of the warp's in unit win + i
     uint32_t slot = 0, issued = 0;
 
-    __device__ __forceinline__ KtFeed(const KaArgs& a_, const DevErr& err_, uint8_t* ring_, uint64_t* full_, int half, int c_,
-                                      int lane_, const KaPos& pos_, int x0, int x1_)
-        : a(a_), err(err_), ring(ring_), full(full_), base(a_.slab.data + half * HALF), c(c_), lane(lane_), pos(pos_), x(x0),
-          x1(x1_) {}
+    __device__ __forceinline__ KtFeed(const KaArgs& a_, const DevErr& err_, uint8_t* ring_, uint64_t* full_, int w_, int lane_,
+                                      const KaPos& pos_, int x0, int x1_)
+        : a(a_), err(err_), ring(ring_), full(full_), w(w_), lane(lane_), pos(pos_), x(x0), x1(x1_) {}
 
-    __device__ __forceinline__ int key(int step) const { return step / G * KU + c * (KU / 2) + step % G * 32; }
-
-    __device__ __forceinline__ void window() {
-        win = st;
-        const int k = key(st + (lane >> 1)) + (lane & 1) * KV4_CELL_TOKENS;
+    __device__ __forceinline__ void window(int u) {
+        win = u;
+        const int k = (u + lane / NC) * KU + w * SHARE + lane % NC * KV4_CELL_TOKENS;
         if (k < len) cells = ka_cell(a, n, head, k, err);
     }
     // Whether a step with a token is left; moves to it.
@@ -257,26 +264,28 @@ struct KtFeed {
         while (st == end) {
             if (!pos.enter(x, x1)) return false;
             const int u1 = min(pos.nu, pos.u + (x1 - x));
-            st = pos.u * G;
+            st = 2 * pos.u;
             len = pos.len; n = pos.n; head = pos.head;
-            // steps with a token, up to the segment's end
-            end = max(st, min(u1 * G, len / KU * G + min(G, max(0, (len % KU - c * (KU / 2) + 31) / 32))));
+            end = max(st, 2 * min(u1, (len - w * SHARE + KU - 1) / KU));   // units with a token of this warp's
             x += u1 - pos.u;
             if (u1 == pos.nu) pos.next_triple(a);
-            win = st - 16;
+            win = (st >> 1) - WIN;
         }
         return true;
     }
     // That step; one slot is free.
     __device__ __forceinline__ void produce() {
-        if (st == win + 16) window();
-        const int c0 = __shfl_sync(0xFFFFFFFFu, cells, 2 * (st - win)), c1 = __shfl_sync(0xFFFFFFFFu, cells, 2 * (st - win) + 1);
-        const bool two = key(st) + KV4_CELL_TOKENS < len;
+        const int u = st >> 1;
+        if (u == win + WIN) window(u);
+        const int c0 = __shfl_sync(0xFFFFFFFFu, cells, NC * (u - win));
+        const int c1 = NC == 2 ? __shfl_sync(0xFFFFFFFFu, cells, NC * (u - win) + 1) : 0;
+        const bool more_than_one = NC == 2 && u * KU + w * SHARE + KV4_CELL_TOKENS < len;
         if (elect_one()) {
-            uint8_t* d = ring + slot * 2 * HALF;
-            mbar_arrive_expect_tx(&full[slot], two ? 2 * HALF : HALF);
+            uint8_t* d = ring + slot * NC * HALF;
+            const uint8_t* base = a.slab.data + (st & 1) * HALF;
+            mbar_arrive_expect_tx(&full[slot], more_than_one ? 2 * HALF : HALF);
             bulk_g2s(d, base + (int64_t)c0 * (2 * HALF), HALF, &full[slot]);
-            if (two) bulk_g2s(d + HALF, base + (int64_t)c1 * (2 * HALF), HALF, &full[slot]);
+            if (more_than_one) bulk_g2s(d + HALF, base + (int64_t)c1 * (2 * HALF), HALF, &full[slot]);
         }
         __syncwarp();
         slot = slot + 1 == RST ? 0 : slot + 1;
@@ -285,15 +294,16 @@ struct KtFeed {
     }
 };
 
-// One expander warp: half c of the rows of the K tiles (half = 0) or of the V
-// tiles (1) of all units of a range.  One body for both: see KtExpandK.
+// One expander warp: a quarter of the keys of the K tile, then of the V tile, of
+// all units of a range.
 template <int HD, int KU, int RST, int ST>
-__device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, volatile int* abort, int half, int c, int lane,
-                                            uint8_t* ring, uint64_t* raw_full, uint32_t tiles, int tile_bytes, uint64_t* t_full,
-                                            uint64_t* t_empty, const __nv_bfloat16* own_src, float own_inv, KaPos pos, int x0,
-                                            int x1) {
+__device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, volatile int* abort, int w, int lane,
+                                            uint8_t* ring, uint64_t* raw_full, uint32_t tiles, int tile_bytes,
+                                            uint64_t (*t_full)[ST], uint64_t (*t_empty)[ST], KaPos pos, int x0, int x1) {
     constexpr int HALF = Kv4Cell<HD>::BYTES / 2;
-    KtFeed<HD, KU, RST> feed(a, err, ring, raw_full, half, c, lane, pos, x0, x1);
+    using Feed = KtFeed<HD, KU, RST>;
+    constexpr int SHARE = Feed::SHARE, NC = Feed::NC;
+    Feed feed(a, err, ring, raw_full, w, lane, pos, x0, x1);
     KtRing<RST> r;
     KtRing<ST> ts;
     uint32_t taken = 0;
@@ -301,40 +311,45 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
     int x = x0;
     pos.enter(x, x1);
     int u = pos.u, u1 = min(pos.nu, u + (x1 - x));
+    auto own_ahead = [&] {   // the own rows of this triple on their way to L2
+        const int row = w * SHARE + lane;
+        if (lane >= SHARE || row >= a.B) return;
+        const int64_t at = ((int64_t)(pos.n * a.B + row) * a.slab.Hkv + pos.head) * HD;
+        #pragma unroll
+        for (int i = 0; i < HD; i += 64) { prefetch_l2(a.Kb + at + i); prefetch_l2(a.Vb + at + i); }
+    };
+    if (x < x1) own_ahead();
     #pragma unroll 1
     while (x < x1) {
         const bool own = u == pos.nu - 1;
-        const int left = (own ? a.B : pos.len - u * KU) - c * (KU / 2);
-        const uint32_t t = tiles + ts.i * tile_bytes + c * (KU / 2) * 128;
+        const int left = (own ? a.B : pos.len - u * KU) - w * SHARE;   // keys of the unit from this warp's first on
+        const int64_t own_at = ((int64_t)(pos.n * a.B + w * SHARE) * a.slab.Hkv + pos.head) * HD;
         #pragma unroll 1
-        for (int j = 0; j < KU / 32; ++j) {   // 16 tokens at a time
-            if ((j & 1) == 0) {
-                #pragma unroll 1
-                while (feed.issued < taken + RST && feed.more()) feed.produce();
-                const bool cell = !own && j * KV4_CELL_TOKENS < left;
-                ok = (j > 0 || kt_wait(&t_empty[ts.i], ts.ph ^ 1, err, abort)) && (!cell || kt_wait(&raw_full[r.i], r.ph, err, abort));
-                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-            }
-            if (!own && (j & ~1) * KV4_CELL_TOKENS < left) {
-                // an absent cell's words are what the slot last held
-                const uint32_t src = smem_u32(ring) + (r.i * 2 + (j & 1)) * HALF;
-                if (half) KtExpandV<HD, KU>::run(src, t + j * 16 * 128, lane, left - j * KV4_CELL_TOKENS);
-                else KtExpandK<HD, KU>::run(src, t + j * 16 * 128, lane);
-                if (j & 1) {
-                    __syncwarp();   // the slot has been read by every lane
-                    ++taken;
-                    r.step();
+        for (int half = 0; half < 2; ++half) {   // K, V
+            #pragma unroll 1
+            while (feed.issued < taken + RST && feed.more()) feed.produce();
+            const bool cell = !own && left > 0;
+            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && (!cell || kt_wait(&raw_full[r.i], r.ph, err, abort));
+            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+            const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + w * SHARE * 128;
+            const uint32_t src = smem_u32(ring) + r.i * NC * HALF;
+            #pragma unroll 1
+            for (int j = 0; j < NC; ++j) {   // 16 tokens at a time
+                const int lj = left - j * KV4_CELL_TOKENS;
+                if (!own && lj > 0) {
+                    if (half) KtExpandV<HD, KU>::run(src + j * HALF, t + j * 16 * 128, lane, lj);
+                    else KtExpandK<HD, KU>::run(src + j * HALF, t + j * 16 * 128, lane);
+                } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
+                    kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + own_at + (int64_t)j * 16 * a.slab.Hkv * HD, (int64_t)a.slab.Hkv * HD,
+                                          t + j * 16 * 128, lane, lj, half ? a.v_inv : a.k_inv);
                 }
-            } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
-                const int64_t stride = (int64_t)a.slab.Hkv * HD;
-                kt_block_rows<HD, KU>(own_src + ((int64_t)(pos.n * a.B + c * (KU / 2) + j * 16) * a.slab.Hkv + pos.head) * HD, stride,
-                                      t + j * 16 * 128, lane, left - j * 16, own_inv);
             }
+            fence_proxy_async_smem();
+            __syncwarp();   // the slot has been read, the rows are written by every lane
+            if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
+            if (cell) { ++taken; r.step(); }
         }
         if (!ok) break;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (elect_one()) mbar_arrive(&t_full[ts.i]);
         ts.step();
         ++x;
         if (++u == u1) {
@@ -342,12 +357,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
             pos.enter(x, x1);
             u = pos.u;
             u1 = min(pos.nu, u + (x1 - x));
-            const int row = c * (KU / 2) + lane;
-            if (x < x1 && row < a.B) {   // the own rows of the next triple on their way to L2
-                const __nv_bfloat16* p = own_src + ((int64_t)(pos.n * a.B + row) * a.slab.Hkv + pos.head) * HD;
-                prefetch_l2(p);
-                if (HD == 128) prefetch_l2(p + 64);
-            }
+            if (x < x1) own_ahead();
         }
     }
     // copies in flight land before the CTA's shared memory goes (they have, unless a wait ran out)
@@ -407,7 +417,7 @@ __device__ __forceinline__ void kt_load_q(const KaArgs& a, int n, int head, int 
 template <int HD, int MM>
 __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs a, const DevErr err) {
     using Cfg = KtCfg<HD, MM>;
-    using Bars = KtBars<Cfg::RST, Cfg::KST, Cfg::VST>;
+    using Bars = KtBars<Cfg::RST, Cfg::ST>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars[KT_PIPES];
     __shared__ KaLineSmem<KT_THREADS, KT_PIPES> line_sm;
@@ -421,15 +431,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     Bars& bb = bars[pipe];
     uint8_t* sQ = sm + pipe * Cfg::PIPE;
     uint8_t* sK = sQ + Cfg::Q;
-    uint8_t* sV = sK + Cfg::KST * Cfg::TILE;
-    uint8_t* sR = sV + Cfg::VST * Cfg::TILE;
+    uint8_t* sV = sK + Cfg::ST * Cfg::TILE;
+    uint8_t* sR = sV + Cfg::ST * Cfg::TILE;
     volatile int* abort = &abort_flag;
 
     if (threadIdx.x < KT_PIPES) {
         Bars& b = bars[threadIdx.x];
         for (int i = 0; i < 4 * Cfg::RST; ++i) mbar_init(&b.raw_full[0][0] + i, 1);
-        for (int i = 0; i < Cfg::KST; ++i) { mbar_init(&b.k_full[i], 2); mbar_init(&b.k_empty[i], 1); }
-        for (int i = 0; i < Cfg::VST; ++i) { mbar_init(&b.v_full[i], 2); mbar_init(&b.v_empty[i], 1); }
+        for (int i = 0; i < 2 * Cfg::ST; ++i) { mbar_init(&b.t_full[0][0] + i, 4); mbar_init(&b.t_empty[0][0] + i, 1); }
         mbar_init(&b.q_full, 4); mbar_init(&b.s_full, 1); mbar_init(&b.p_full, 4); mbar_init(&b.pv_done, 1);
         mbar_init(&b.o_empty, 4); mbar_init(&b.drain, 1);
         if (threadIdx.x == 0) abort_flag = 0;
@@ -466,12 +475,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 
     if (warp >= 8) {
         const int w = warp & 3;
-        uint8_t* ring = sR + w * Cfg::RST * Cfg::CELL;
-        const int half = w >> 1;   // two warps for K tiles, two for V tiles
-        static_assert(Cfg::KST == Cfg::VST, "one body for both");
-        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::KST>(a, err, abort, half, w & 1, lane, ring, bb.raw_full[w], smem_u32(half ? sV : sK),
-                                                     Cfg::TILE, half ? bb.v_full : bb.k_full, half ? bb.v_empty : bb.k_empty,
-                                                     half ? a.Vb : a.Kb, half ? a.v_inv : a.k_inv, pos, x0, x1);
+        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::ST>(a, err, abort, w, lane, sR + w * Cfg::RST * Cfg::SLOT, bb.raw_full[w], smem_u32(sK),
+                                                   Cfg::TILE, bb.t_full, bb.t_empty, pos, x0, x1);
     } else {
         // ------------------------------------------------------------- softmax
         constexpr bool HALF = MM == 64;
@@ -488,13 +493,12 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
         // the compiler knows to be uniform cost half the clocks per product of
         // those of a lone lane in a divergent branch, 8 products 214 against 510)
         const bool issuer = q4 == 0;
-        KtRing<Cfg::KST> ks;
-        KtRing<Cfg::VST> vs;
+        KtRing<Cfg::ST> ks, vs;
         // descriptors of slot 0; slots and K blocks are added to the address field (16-byte units)
         const uint64_t qd = sw128_desc(smem_u32(sQ)), kd = sw128_desc(smem_u32(sK));
         const uint64_t vd = sw128_desc_mn(smem_u32(sV), Cfg::TKB, 1024);
         auto issue_s = [&](bool first) {   // S of the next unit; S's columns are free
-            const bool ready = kt_wait(&bb.k_full[ks.i], ks.ph, err, abort) &&
+            const bool ready = kt_wait(&bb.t_full[0][ks.i], ks.ph, err, abort) &&
                                (!first || kt_wait(&bb.q_full, triple & 1, err, abort));
             if (!__all_sync(0xFFFFFFFFu, ready)) return false;
             tc_fence_after();
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                     mma_bf16(tmem + Cfg::S_COL, qd + (j >> 2) * (Cfg::QKB >> 4) + (j & 3) * 2,
                              kdi + (j >> 2) * (Cfg::TKB >> 4) + (j & 3) * 2, kt_idesc_f16(MM, KU), j > 0);
                 mma_commit(&bb.s_full);
-                mma_commit(&bb.k_empty[ks.i]);
+                mma_commit(&bb.t_empty[0][ks.i]);
             }
             __syncwarp();
             issued = true;
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             return true;
         };
         auto issue_pv = [&](bool first) {   // P of the unit written by all four warps
-            const bool ready = kt_wait(&bb.v_full[vs.i], vs.ph, err, abort) &&
+            const bool ready = kt_wait(&bb.t_full[1][vs.i], vs.ph, err, abort) &&
                                // O is free once the previous triple's output has been read
                                (!first || kt_wait(&bb.o_empty, (triple & 1) ^ 1, err, abort)) &&
                                kt_wait(&bb.p_full, unit & 1, err, abort);
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                     mma_bf16_ts(tmem + Cfg::O_COL, tmem + Cfg::S_COL + 8 * j, vdi + j * (16 * 128 >> 4),
                                 kt_idesc_f16(MM, HD) | (1u << 16), j > 0 || !first);
                 mma_commit(&bb.pv_done);
-                mma_commit(&bb.v_empty[vs.i]);
+                mma_commit(&bb.t_empty[1][vs.i]);
             }
             __syncwarp();
             vs.step();
