@@ -35,7 +35,7 @@
 // of it.  P = 2^(s - m + 7) is rounded to fp16 (11 bits; the 7 keeps weights
 // down to 2^-31 of the largest, m trails the true maximum by at most 8); sums
 // of P are fp32 of the unrounded values.  The block's own keys and values are
-// taken to fp16 in units of the pool's powers of two (block_half2).  Maxima are
+// taken to fp16 in units of the pool's powers of two (block_half8).  Maxima are
 // per row; O is rescaled only when a maximum grows by more than 2^8.
 #include "internal.h"
 #include "kv4_attn.cuh"
@@ -409,11 +409,8 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
             #pragma unroll
             for (int i = 0; i < HD / 32; ++i) {
                 const uint4 z = make_uint4(0, 0, 0, 0);
-                const uint4 w0 = b0 < a.B ? k0[i] : z, w1 = b1 < a.B ? k1[i] : z;
-                const uint32_t f0[4] = {block_half2(w0.x, a.k_inv), block_half2(w1.x, a.k_inv), block_half2(w0.y, a.k_inv),
-                                        block_half2(w1.y, a.k_inv)};
-                const uint32_t f1[4] = {block_half2(w0.z, a.k_inv), block_half2(w1.z, a.k_inv), block_half2(w0.w, a.k_inv),
-                                        block_half2(w1.w, a.k_inv)};
+                const uint4 w0 = block_half8(b0 < a.B ? k0[i] : z, a.k_inv), w1 = block_half8(b1 < a.B ? k1[i] : z, a.k_inv);
+                const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
                 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_f16(s[nt], f0, q[nt][4 * i], q[nt][4 * i + 1]);
@@ -437,10 +434,9 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int b = warp * KV4_CELL_TOKENS + 4 * i + t;
-                    const uint4 x4 = b < a.B ? *reinterpret_cast<const uint4*>(
-                        a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0);
-                    v[i][0] = block_half2(x4.x, a.v_inv); v[i][1] = block_half2(x4.y, a.v_inv);
-                    v[i][2] = block_half2(x4.z, a.v_inv); v[i][3] = block_half2(x4.w, a.v_inv);
+                    const uint4 x4 = block_half8(b < a.B ? *reinterpret_cast<const uint4*>(
+                        a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0), a.v_inv);
+                    v[i][0] = x4.x; v[i][1] = x4.y; v[i][2] = x4.z; v[i][3] = x4.w;
                 }
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {

@@ -53,17 +53,34 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Two of the block's own bf16 elements in units of the pool's power of two
+// Pairwise maximum of two 16-bit unsigned numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Eight of the block's own bf16 elements in units of the pool's power of two
 // (inv: its inverse), as fp16.  bf16's 8 bits survive from 2^-14 of the unit
 // up; finite values past fp16's range become its largest, as the cache's
-// become its own.
-__device__ __forceinline__ uint32_t block_half2(uint32_t w, float inv) {
-    float x[2] = {bf16lo(w) * inv, bf16hi(w) * inv};
+// become its own.  Infinities and NaN stay what they are.
+__device__ __forceinline__ uint4 block_half8(const uint4 v, float inv) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4];
     #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (fabsf(x[i]) > 65504.f && fabsf(x[i]) < INFINITY) x[i] = copysignf(65504.f, x[i]);
-    const __half2 h = __floats2half2_rn(x[0], x[1]);
-    return *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(bf16hi(w[i]) * inv), "f"(bf16lo(w[i]) * inv));
+    const uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    if (m >= 0x7F800000u || (m & 0xFFFFu) >= 0x7F80u) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+            #pragma unroll
+            for (int s = 0; s < 32; s += 16) {
+                const uint32_t x = w[i] >> s & 0xFFFFu;
+                const uint32_t y = (x & 0x8000u) | (x & 0x7Fu ? 0x7E00u : 0x7C00u);
+                if ((x & 0x7F80u) == 0x7F80u) h[i] = (h[i] & ~(0xFFFFu << s)) | y << s;
+            }
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // Block row and head of query row r of a group: element offset of its Q and O.

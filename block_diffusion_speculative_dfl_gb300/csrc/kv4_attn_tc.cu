@@ -226,8 +226,7 @@ __device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t 
     #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int r = RPL * i;
-        sts128((at ^ ((r & 7) << 4)) + r * 128, make_uint4(block_half2(v[i].x, inv), block_half2(v[i].y, inv),
-                                                          block_half2(v[i].z, inv), block_half2(v[i].w, inv)));
+        sts128((at ^ ((r & 7) << 4)) + r * 128, block_half8(v[i], inv));
     }
 }
 
@@ -322,8 +321,8 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
     #pragma unroll 1
     while (x < x1) {
         const bool own = u == pos.nu - 1;
-        const int left = (own ? a.B : pos.len - u * KU) - w * SHARE;   // keys of the unit from this warp's first on
-        const int64_t own_at = ((int64_t)(pos.n * a.B + w * SHARE) * a.slab.Hkv + pos.head) * HD;
+        const int share = w * SHARE;
+        const int left = (own ? a.B : pos.len - u * KU) - share;   // keys of the unit from this warp's first on
         #pragma unroll 1
         for (int half = 0; half < 2; ++half) {   // K, V
             #pragma unroll 1
@@ -331,7 +330,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
             const bool cell = !own && left > 0;
             ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && (!cell || kt_wait(&raw_full[r.i], r.ph, err, abort));
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-            const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + w * SHARE * 128;
+            const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
             const uint32_t src = smem_u32(ring) + r.i * NC * HALF;
             #pragma unroll 1
             for (int j = 0; j < NC; ++j) {   // 16 tokens at a time
@@ -340,8 +339,9 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
                     if (half) KtExpandV<HD, KU>::run(src + j * HALF, t + j * 16 * 128, lane, lj);
                     else KtExpandK<HD, KU>::run(src + j * HALF, t + j * 16 * 128, lane);
                 } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
-                    kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + own_at + (int64_t)j * 16 * a.slab.Hkv * HD, (int64_t)a.slab.Hkv * HD,
-                                          t + j * 16 * 128, lane, lj, half ? a.v_inv : a.k_inv);
+                    const int64_t at = ((int64_t)(pos.n * a.B + share + j * 16) * a.slab.Hkv + pos.head) * HD;
+                    kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj,
+                                          half ? a.v_inv : a.k_inv);
                 }
             }
             fence_proxy_async_smem();
@@ -363,13 +363,6 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
     // copies in flight land before the CTA's shared memory goes (they have, unless a wait ran out)
     #pragma unroll 1
     for (; taken < feed.issued; ++taken) mbar_wait(&raw_full[taken % RST], (taken / RST) & 1, err);
-}
-
-// Pairwise maximum of two 16-bit unsigned numbers.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
 }
 
 // ROWS rows of Q (rows first .. first + ROWS - 1 of the triple; past R zeros)
