@@ -18,8 +18,8 @@
 // reverse (read).  One thread per group of K and of V: 64 B of loads in flight
 // per thread, 32-byte sectors whole on the bf16 side and 8-byte pieces that
 // neighbouring lanes complete to whole rows on the 4-bit side.  A block takes
-// 256 neighbouring groups of one sequence, so the 64-bit index arithmetic is
-// once per block.
+// some whole rows of one sequence (or part of one when a row has more groups
+// than the block threads), so a thread divides once, by small numbers.
 #include "internal.h"
 #include "kv4.cuh"
 #include "paged.h"
@@ -36,41 +36,40 @@ struct Kv4Rows {
     int max_pages;
     const int32_t* start;   // [N] position of row 0 (negative: the sequence is skipped)
     const int32_t* count;   // [N] rows of each sequence
-    int R;
+    int N, R;
     int width;              // groups of a row: Hkv * hd / 16
-    int64_t items, chunks;  // chunks of KR_THREADS groups in all, per sequence
+    int rows;               // rows of a block
     uint64_t cells_inv;     // ceil(2^36 / cells of a page)
     int k_exp, v_exp;
 };
 
-// The group a thread has in chunk `item`.
+// A group that exists.
 struct Kv4Item {
     int n, i, head, group;  // sequence, row, head, group of the head
-    int64_t at;             // the group among all of K
     int start;              // position of row 0
-    bool on;                // the row exists
+    int64_t at;             // the group among all of K
 };
 
-template <int HD>
-__device__ __forceinline__ Kv4Item kv4_item(const Kv4Rows& a, int64_t item, const DevErr& err) {
+// Calls body(item) for every group of the call that exists.
+template <int HD, typename Body>
+__device__ __forceinline__ void kv4_each(const Kv4Rows& a, const DevErr& err, Body body) {
     constexpr int GROUPS = Kv4Cell<HD>::GROUPS;
-    Kv4Item t;
-    t.n = (int)(item / a.chunks);
-    const int64_t first = (item - t.n * a.chunks) * KR_THREADS;   // of the sequence's groups
-    const int64_t row0 = first / a.width;
-    const int y = (int)(first - row0 * a.width) + (int)threadIdx.x;
-    const int down = y / a.width, x = y - down * a.width;
-    t.head = x / GROUPS;
-    t.group = x % GROUPS;
-    t.start = a.start[t.n];
-    const int m = a.count[t.n];
-    const int64_t i = row0 + down;
-    bool ok = m >= 0 && m <= a.R && (t.start < 0 || t.start <= a.max_pages * a.slab.page - m);
-    if (!ok && first == 0 && threadIdx.x == 0) record_error(err, DFL_ERR_INVALID_ARG);
-    t.on = ok && t.start >= 0 && i < m;
-    t.i = (int)i;
-    t.at = ((int64_t)t.n * a.R + i) * a.width + x;
-    return t;
+    const int down = a.rows == 1 ? 0 : (int)threadIdx.x / a.width, x0 = (int)threadIdx.x - down * a.width;
+    #pragma unroll 1
+    for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
+        const int s = a.start[n], m = a.count[n];
+        if (m < 0 || m > a.R || (s >= 0 && s > a.max_pages * a.slab.page - m)) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) record_error(err, DFL_ERR_INVALID_ARG);
+            continue;
+        }
+        if (s < 0 || down >= a.rows) continue;
+        #pragma unroll 1
+        for (int64_t i = (int64_t)blockIdx.x * a.rows + down; i < m; i += (int64_t)gridDim.x * a.rows) {
+            #pragma unroll 1
+            for (int x = x0; x < a.width; x += KR_THREADS)
+                body(Kv4Item{n, (int)i, x / GROUPS, x % GROUPS, s, ((int64_t)n * a.R + i) * a.width + x});
+        }
+    }
 }
 
 // The cell of a row that exists, or nullptr (its page is out of range: recorded).
@@ -124,20 +123,17 @@ __device__ __forceinline__ void quantise16(const uint4 lo, const uint4 hi, int e
 }
 
 template <int HD>
-__global__ void __launch_bounds__(KR_THREADS) kv4_append_kernel(const Kv4Rows a, const uint4* K, const uint4* V, const DevErr err) {
+__global__ void __launch_bounds__(KR_THREADS, 5) kv4_append_kernel(const Kv4Rows a, const uint4* K, const uint4* V, const DevErr err) {
     grid_dep_begin();
     using Cell = Kv4Cell<HD>;
-    #pragma unroll 1
-    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-        const Kv4Item t = kv4_item<HD>(a, item, err);
-        if (!t.on) continue;
+    kv4_each<HD>(a, err, [&](const Kv4Item& t) {
         const uint4 k0 = K[2 * t.at], k1 = K[2 * t.at + 1], v0 = V[2 * t.at], v1 = V[2 * t.at + 1];
         int tok;
         uint8_t* cell = row_cell<HD>(a, t, err, tok);
-        if (!cell) continue;
+        if (!cell) return;
         if (!DFL_IN_BOUNDS(err.word, cell - a.slab.data,
                            (int64_t)a.slab.num_pages * a.slab.Hkv * a.slab.cells * Cell::BYTES))
-            continue;
+            return;
         uint2 c;
         uint8_t s;
         quantise16(k0, k1, a.k_exp, c, s);
@@ -146,7 +142,7 @@ __global__ void __launch_bounds__(KR_THREADS) kv4_append_kernel(const Kv4Rows a,
         quantise16(v0, v1, a.v_exp, c, s);
         *reinterpret_cast<uint2*>(cell + Cell::v_code(tok, t.group)) = c;
         cell[Cell::v_scale(tok, t.group)] = s;
-    }
+    });
 }
 
 __device__ __forceinline__ void expand16(uint2 codes, uint8_t scale, float pow2, uint4& lo, uint4& hi) {
@@ -167,17 +163,14 @@ __device__ __forceinline__ void expand16(uint2 codes, uint8_t scale, float pow2,
 }
 
 template <int HD>
-__global__ void __launch_bounds__(KR_THREADS) kv4_read_kernel(const Kv4Rows a, uint4* K, uint4* V, const DevErr err) {
+__global__ void __launch_bounds__(KR_THREADS, 5) kv4_read_kernel(const Kv4Rows a, uint4* K, uint4* V, const DevErr err) {
     grid_dep_begin();
     using Cell = Kv4Cell<HD>;
     const float pk = kv4_exp2i(a.k_exp), pv = kv4_exp2i(a.v_exp);
-    #pragma unroll 1
-    for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-        const Kv4Item t = kv4_item<HD>(a, item, err);
-        if (!t.on) continue;
+    kv4_each<HD>(a, err, [&](const Kv4Item& t) {
         int tok;
         const uint8_t* cell = row_cell<HD>(a, t, err, tok);
-        if (!cell) continue;
+        if (!cell) return;
         const uint2 kc = *reinterpret_cast<const uint2*>(cell + Cell::k_code(tok, t.group));
         const uint2 vc = *reinterpret_cast<const uint2*>(cell + Cell::v_code(tok, t.group));
         uint4 lo, hi;
@@ -187,23 +180,24 @@ __global__ void __launch_bounds__(KR_THREADS) kv4_read_kernel(const Kv4Rows a, u
         expand16(vc, cell[Cell::v_scale(tok, t.group)], pv, lo, hi);
         V[2 * t.at] = lo;
         V[2 * t.at + 1] = hi;
-    }
+    });
 }
 
 Kv4Rows rows_args(const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const int32_t* start, const int32_t* count,
                   int R) {
-    Kv4Rows a{kv4_slab(pool, layer), pg.table, pg.max_pages, start, count, R};
+    Kv4Rows a{kv4_slab(pool, layer), pg.table, pg.max_pages, start, count, pg.N, R};
     a.width = pool.Hkv * (pool.hd / 16);
-    a.chunks = ((int64_t)R * a.width + KR_THREADS - 1) / KR_THREADS;
-    a.items = a.chunks * pg.N;
+    a.rows = std::max(1, KR_THREADS / a.width);
     a.cells_inv = (((uint64_t)1 << 36) + a.slab.cells - 1) / a.slab.cells;
     a.k_exp = pool.k_exp;
     a.v_exp = pool.v_exp;
     return a;
 }
 
-unsigned rows_grid(const DeviceCtx* ctx, const Kv4Rows& a) {
-    return (unsigned)std::min<int64_t>(a.items, (int64_t)ctx->sm_count * 64);
+dim3 rows_grid(const DeviceCtx* ctx, const Kv4Rows& a) {
+    const int n = std::min(a.N, 65535);
+    const int64_t chunks = ((int64_t)a.R + a.rows - 1) / a.rows;
+    return dim3((unsigned)std::min(chunks, std::max<int64_t>(1, (int64_t)ctx->sm_count * 64 / n)), (unsigned)n);
 }
 
 }  // namespace
