@@ -240,6 +240,32 @@ def test_page_operations_write_only_theirs(N, page, num_pages, max_pages):
         same()
 
 
+@pytest.mark.parametrize("N,max_pages", [(1, 1), (3, 7), (9, 33), (4096, 1), (8, 512), (8, 513), (700, 600)])
+def test_remap_of_tables_of_every_size(N, max_pages):
+    # up to 4,096 entries are one block's
+    rng = np.random.default_rng(N)
+    page, num = 16, 5000
+    c = dfl.PagedCache(1, num, page, 1, 64, N, max_pages)
+    length = rng.integers(0, max_pages * page + 1, N)
+    table = rng.integers(0, num, (N, max_pages))
+    table[np.arange(max_pages)[None] * page >= length[:, None]] = -1
+    ref = np.bincount(table[table >= 0], minlength=num)
+    for x, v in ((c.table, table), (c.len, length), (c.ref, ref)):
+        x.copy_(i32(v))
+    b = ko.PageBook(table, length, ref, page)
+    for i in range(3):
+        parent, keep = rng.integers(-1, N, N), rng.integers(-1, max_pages * page + 9, N)
+        if i == 1:
+            parent[0] = N   # no sequence: the row stays
+        c.remap(i32(parent), None if i == 2 else i32(keep))
+        if i == 1:
+            assert dfl.dfl_get_device_error() == 1
+            parent[0], keep[0] = 0, -1
+        b.remap(parent, None if i == 2 else keep)
+        assert np.array_equal(host(c.table), b.table) and np.array_equal(host(c.len), b.len)
+        assert np.array_equal(host(c.ref), b.ref)
+
+
 @pytest.mark.parametrize("B,Hq", [(1, 16), (16, 16)])
 def test_a_pool_past_2_31_bytes(B, Hq):
     rng = np.random.default_rng(B)
