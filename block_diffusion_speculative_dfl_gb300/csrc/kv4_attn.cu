@@ -28,6 +28,11 @@
 // for tcgen05 operands would write and read 4 hd bytes per key more than the
 // 9/8 hd that arrive, and that traffic alone takes longer than the reads from
 // HBM (18 B per token and dimension pair through 128 B per clock and SM).
+// Single tokens of 48 sequences of 65 to 16,000 (8 heads of 128, 4 query heads
+// each): 98 us, 4.5 TB/s, 66 % of a copy's rate.  A cell of 16 tokens is about
+// 370 warp instructions, 192 of them the conversions, scales and products; the
+// schedulers issue in 64 % of the clocks, waiting for dependent results and for
+// the conversion pipe.  More warps do not fit (five groups spill: 130 us).
 //
 // Numbers.  Expanded codes are exact in fp16.  Q is brought to fp16 after a
 // power of two per row takes its largest element to [1, 2): bf16's 8 bits
@@ -513,7 +518,10 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 
 // Row tiles of 8 query rows when a group has at most 8, of 16 up to 16: a wider
 // tile expands each key for more rows at once.  More rows go to the
-// tensor-memory kernel.
+// tensor-memory kernel: 32 sequences of 2,048 tokens with 16 rows to a head take
+// 42 us here and 58 there, with 32 rows 64 and 58.
+// See KaLine.  The weight: a triple costs some 4.5 us beside 1.1 us per unit
+// (the batch above 107, 102 and 103 us with weights 2, 4 and 6).
 constexpr int KA_SEAM = 8;
 constexpr int KA_WEIGHT = 4;
 constexpr int KA_MAX_ROWS = 16;
@@ -530,6 +538,7 @@ inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
     if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    if ((int64_t)B * (Hq / Hkv) > KV4_MAX_HEAD_ROWS) return 0;
     const int R = B * (Hq / Hkv), nt = ka_nt(R);
     if (R > KA_MAX_ROWS) return kv4_attn_tc_ws_bytes(R, hd);
     const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * 8 * nt;
@@ -546,6 +555,7 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.table = pg.table; a.len = pg.len; a.max_pages = pg.max_pages;
     a.N = pg.N; a.B = B; a.Hq = Hq; a.G = G; a.R = R;
     a.subs = (R + rows - 1) / rows;
+    if ((int64_t)pg.N * pool.Hkv * a.subs >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
     a.HS = pool.Hkv * a.subs;
     a.g_inv = (((uint64_t)1 << 40) + G - 1) / G;
     a.cells_inv = (((uint64_t)1 << 36) + a.slab.cells - 1) / a.slab.cells;

@@ -1,15 +1,17 @@
 // Block attention over the 4-bit paged cache for many query rows per K/V head,
 // on the 5th-generation tensor cores.  The same sum and the same line of work
 // units as kv4_attn.cu, with up to 128 rows to a triple, where products and
-// exponentials, not bytes, are most of the work.
+// exponentials, not bytes, are most of the work.  A block of 16 at 4 query heads
+// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 58 us, 280 TFLOP/s
+// of products and 1.5 TB/s of cache; 64 rows of a head of 64 over 33,333 to
+// 100,001 tokens: 92 us.
 //
 // One CTA per SM, two pipelines of eight warps, each with a range of the line of
 // its own, so that one pipeline's products run under the other's exponentials:
-//   expanders (4 warps) two for K, two for V, half of a unit's tokens each: bulk
-//                       copies of half cells into a ring of the warp's own,
-//                       then codes * scales in fp16 into a tile [keys][hd] with
-//                       128-byte swizzle; the block's own rows come straight
-//                       from memory;
+//   expanders (4 warps) a quarter of a unit's keys each, K, then V: bulk copies
+//                       of half cells into a ring of the warp's own, then codes
+//                       * scales in fp16 into a tile [keys][hd] with 128-byte
+//                       swizzle; the block's own rows come straight from memory;
 //   softmax (4 warps)   Q as fp16 into shared memory, running maximum and sum,
 //                       P over S's columns, the triple's output.  The first of
 //                       them issues the products: S = Q K^T (M = 64 or 128
@@ -19,13 +21,17 @@
 // needs that P V to have read S's columns; a warp of its own would take the
 // fifth place on its scheduler and with it 32 registers from every thread.
 //
-// What bounds it: the turns between the roles.  The bare chain of waits,
-// commits and issues of a unit takes about 1,000 clocks with nothing else in
-// it, so a unit is 128 keys where shared and tensor memory allow (64 at
-// hd = 128 with 128 rows); expansion and softmax of 64 keys by 64 rows are
-// about 2,300 warp instructions, 575 clocks of the four schedulers; the tiles
-// (hd = 128) are 32 KB per 64 keys written and read beside Q, 700 clocks of
-// shared memory at 128 B per clock, against 390 of HBM for the 9 KB of codes.
+// What bounds it: how fast one warp issues, about one instruction in 4.7 clocks
+// with four warps to a scheduler (dependent instructions, branches, fetches).
+// Per unit of 128 keys and 64 rows (hd = 128) a pipeline's clocks are
+//   expanders  2 x 1,150 of expansion, 1,100 of copies ahead, 1,000 of waits
+//              and arrivals: 4,500, the longest turn;
+//   products   S 900 to its commit, softmax 1,450, P V 1,000, its end 250, the
+//              next S 380 to be seen: 4,000, hidden under it.
+// At hd = 64 the two trade places.  Hence units of 128 keys where shared and
+// tensor memory allow (64 at hd = 128 with 128 rows), and four expanders on K,
+// then on V: two on each waited for their one tile's product in turn (64-row
+// heads of 64 over long contexts 98 against 92 us).
 #include "internal.h"
 #include "kv4_attn.cuh"
 #include "paged.h"
@@ -129,9 +135,8 @@ __device__ __forceinline__ uint32_t kt_piece(uint32_t tile, int row, int c) {
 
 // Expansion of the K or V half of a cell into 16 rows of a tile.  A quarter
 // warp writes the eight 16-byte pieces of one tile row: no bank conflicts on
-// either side.  The loops stay rolled: four roles share each scheduler's
-// instruction cache, and unrolled the warps wait for instructions more than
-// they gain (Qwen-shaped block attention 75 against 60 us).
+// either side.  All of a lane's words are read before the first is expanded:
+// read one by one, each row waited for its own (the block of 16 above 67 us).
 template <int HD, int KU>
 struct KtExpandK {   // scores of tokens past the length are masked
     static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane) {
@@ -716,6 +721,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     }
 }
 
+// See KaLine.  A seam of 8 units of 128 keys: the block of 16 above takes 67 us
+// as whole triples and 70 cut (before the expansion was made faster); a weight
+// of 1, 2 or 3 gives the same times with long triples.
 constexpr int KT_SEAM = 8;
 constexpr int KT_WEIGHT = 1;
 constexpr int KT_SMS = 152;   // SMs of a GB300

@@ -31,6 +31,7 @@ dfl_status kv4_read_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
                         const int32_t* count, int R, void* K, void* V, cudaStream_t st);
 
 // Attention over the cache and the block's own keys (kv4_attn.cu).
+constexpr int KV4_MAX_HEAD_ROWS = 65536;   // query rows of a K/V head: B * Hq / Hkv
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd);
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
                         const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st);

@@ -649,13 +649,15 @@ dfl_status dfl_kv4_read(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages
  *   Kb, Vb  in, bf16 [N*B][Hkv][hd]
  *   O       out, bf16 [N*B][Hq][hd]
  *   ws      dfl_workspace_size(DFL_OP_KV4_ATTN) bytes
- *   fp32 sums, softmax weights rounded to 11 bits (8 for the block's own
- *   keys); the same inputs give the same bits.  A length outside
+ *   fp32 sums, softmax weights rounded to 11 bits.  The block's own rows are
+ *   taken to fp16 in units of 2^k_exp and 2^v_exp: bf16's 8 bits survive from
+ *   2^-14 of the unit up, finite values past 65504 units count as that.  The
+ *   same inputs give the same bits.  A length outside
  *   0..max_pages*page is read as the nearest of these, a table entry outside
  *   0..num_pages-1 as page 0, and either records DFL_ERR_INVALID_ARG in the
  *   device error word.
- *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (B above 64, hd, page, sizes),
- *   MISALIGNED, WORKSPACE.
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (B above 64, more than 65,536
+ *   query rows to a K/V head, hd, page, sizes), MISALIGNED, WORKSPACE.
  */
 dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
                         const void* Q, const void* Kb, const void* Vb, int32_t B, int32_t Hq, void* O,
