@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
         return x < total ? (int)x : -1;
     });
     const int64_t x0l = (int64_t)range * line.per;
+    if (tid == 0) a.cross[range] = KaCross{-1, 0, 0, 0};
     if (line.whole ? range >= a.N * a.HS : x0l >= line.total) return;   // no block-wide barrier follows
     const int x0 = line.whole ? 0 : (int)x0l;
 
@@ -504,6 +505,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 }
             }
         }
+        if (u0 == 0 && u1 < pos.nu && tid == 0) a.cross[range] = KaCross{pos.n, head, pos.tile, (x + pos.nu - 1) / line.per};
         group_sync(group);
         x += u1 - u0;
         pos.u = u1;
@@ -524,6 +526,7 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 // (the batch above 107, 102 and 103 us with weights 2, 4 and 6).
 constexpr int KA_SEAM = 8;
 constexpr int KA_WEIGHT = 4;
+constexpr int KJ_ROWS = KjCfg<128, 8>::AT_ONCE;
 constexpr int KA_MAX_ROWS = 16;
 int ka_nt(int R) { return R <= 8 ? 1 : 2; }
 
@@ -542,7 +545,7 @@ size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
     const int R = B * (Hq / Hkv), nt = ka_nt(R);
     if (R > KA_MAX_ROWS) return kv4_attn_tc_ws_bytes(R, hd);
     const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * 8 * nt;
-    return al256(parts * hd * 4) + al256(parts * 8);
+    return al256(parts * hd * 4) + al256(parts * 8) + al256(sizeof(KaCross) * KA_SMS * ka_groups(nt));
 }
 
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
@@ -576,6 +579,7 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * rows;
     a.Opart = static_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
+    a.cross = reinterpret_cast<KaCross*>(reinterpret_cast<uint8_t*>(a.ml) + al256(parts * 8));
     const int grid = ka_grid(units), groups = ka_groups(nt);
     const DevErr err = dev_err(ctx);
     auto run = [&](auto kern, auto join, int smem, int slot) -> dfl_status {

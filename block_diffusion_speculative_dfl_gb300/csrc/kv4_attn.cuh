@@ -8,6 +8,11 @@
 
 namespace dfl {
 
+// The triple that starts in a range and ends in range `last` behind it; n < 0: none.
+struct alignas(16) KaCross {
+    int n, head, tile, last;
+};
+
 struct KaArgs {
     Kv4Slab slab;
     const int32_t* table;
@@ -24,8 +29,9 @@ struct KaArgs {
     const __nv_bfloat16* Kb;  // [N*B][Hkv][hd]
     const __nv_bfloat16* Vb;
     __nv_bfloat16* O;         // [N*B][Hq][hd]
-    float* Opart;             // [2 * grid][rows][hd]
-    float2* ml;               // [2 * grid][rows] (maximum in log2 units, sum)
+    float* Opart;             // [2 * ranges][rows][hd]
+    float2* ml;               // [2 * ranges][rows] (maximum in log2 units, sum)
+    KaCross* cross;           // [ranges]
     float scale_log2;         // log2(e) / sqrt(hd)
     float k_pow2, k_inv, v_pow2, v_inv;   // 2^k_exp, 2^-k_exp, 2^v_exp, 2^-v_exp
 };
@@ -228,30 +234,24 @@ struct KaPos {
     }
 };
 
-// Adds up the triple that starts in range blockIdx.x and ends past it: partials
-// of that range (its second) and of the following ones (their first), in the
-// order of the keys.  gridDim.x ranges; blockIdx.y takes rows of KJ_ROWS.
-constexpr int KJ_ROWS = 8;
+// Adds up the triple that starts in range blockIdx.x and ends past it, if there
+// is one: partials of that range (its second) and of the following ones (their
+// first), in the order of the keys.  gridDim.x ranges; blockIdx.y takes some of
+// the rows.  The attention kernel says which triple that is: found again from
+// the lengths, it cost this kernel 2 us of its 4.
 template <int HD, int ROWS>
-__global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
-    constexpr int TPR = HD / 4, THREADS = TPR * KJ_ROWS;
-    __shared__ KaLineSmem<THREADS, 1> line_sm;
+struct KjCfg {
+    static constexpr int AT_ONCE = ROWS < 64 ? 8 : 16;   // rows of a block
+    static constexpr int THREADS = HD / 4 * AT_ONCE;
+};
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
+    constexpr int TPR = HD / 4;
     grid_dep_begin();
-    const KaLine line = ka_locate<THREADS, 1>(a, gridDim.x, line_sm, [&](int, int per, int total) {
-        const int64_t end = ((int64_t)blockIdx.x + 1) * per;   // a triple crosses the border before `end`
-        return end < total ? (int)end : -1;
-    });
-    const int64_t endl = ((int64_t)blockIdx.x + 1) * line.per;
-    if (line.whole || endl >= line.total) return;
-    const int end = (int)endl;
-    const KaFound f = line_sm.at[0];
-    const int nu = ka_units(a, f.len);
-    const int hs = (end - f.before) / (nu + a.weight);
-    const int p0 = f.before + hs * (nu + a.weight) + a.weight, p1 = p0 + nu;   // units of the triple at `end`
-    if (p0 >= end || p0 < end - line.per) return;          // none crosses, or it started before this range
-    const int first = blockIdx.x, last = (p1 - 1) / line.per;
-    const int head = hs / a.subs, row0 = (hs - head * a.subs) * ROWS;
-    const int row = blockIdx.y * KJ_ROWS + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;
+    const KaCross t = a.cross[blockIdx.x];
+    if (t.n < 0) return;
+    const int first = blockIdx.x, last = t.last, row0 = t.tile * ROWS;
+    const int row = blockIdx.y * KjCfg<HD, ROWS>::AT_ONCE + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;
     if (row >= ROWS || r >= a.R) return;
     // eight partials are read at once: a long triple waits for memory once per eight
     constexpr int BATCH = 8;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(HD / 4 * KJ_ROWS) kv4_attn_join_kernel(const K
         }
     }
     const float inv = __fdividef(a.v_pow2, L);
-    const int64_t at = ka_row(a, f.n, head, r, HD) + c;
+    const int64_t at = ka_row(a, t.n, t.head, r, HD) + c;
     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
         *reinterpret_cast<uint2*>(a.O + at) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));

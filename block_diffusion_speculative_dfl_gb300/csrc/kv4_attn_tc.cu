@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             vs.step();
             return true;
         };
+        if (issuer && lane == 0) a.cross[range] = KaCross{-1, 0, 0, 0};
         int x = x0;
         while (pos.enter(x, x1)) {
             const int head = pos.head, row0 = pos.tile * MM;
@@ -702,6 +703,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             tc_fence_before();
             __syncwarp();
             if (elect_one()) mbar_arrive(&bb.o_empty);
+            if (u0 == 0 && u1 < pos.nu && issuer && lane == 0)
+                a.cross[range] = KaCross{pos.n, head, pos.tile, (x + pos.nu - 1) / line.per};
             x += u1 - u0;
             pos.u = u1;
             if (u1 == pos.nu) pos.next_triple(a);
@@ -742,7 +745,7 @@ int kv4_attn_tc_weight() { return KT_WEIGHT; }
 
 size_t kv4_attn_tc_ws_bytes(int R, int hd) {
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * kv4_attn_tc_rows(R);
-    return al256(rows * hd * 4) + al256(rows * 8);
+    return al256(rows * hd * 4) + al256(rows * 8) + al256(sizeof(KaCross) * KT_PIPES * KT_SMS);
 }
 
 dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, cudaStream_t st) {
@@ -750,9 +753,10 @@ dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * mm;
     a.Opart = static_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(rows * hd * 4));
+    a.cross = reinterpret_cast<KaCross*>(reinterpret_cast<uint8_t*>(a.ml) + al256(rows * 8));
     const int grid = kt_grid(units);
     const DevErr err = dev_err(ctx);
-    auto run = [&](auto kern, auto join, int smem, int slot) -> dfl_status {
+    auto run = [&](auto kern, auto join, int smem, int slot, int at_once) -> dfl_status {
         if (!ctx->kv4_attr_set[slot]) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
                 return DFL_ERR_CUDA;
@@ -764,13 +768,17 @@ dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void
             if (rc != DFL_OK) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
-        return launch_pdl(join, dim3(KT_PIPES * grid, mm / KJ_ROWS), hd / 4 * KJ_ROWS, 0, st, a, err);
+        return launch_pdl(join, dim3(KT_PIPES * grid, mm / at_once), hd / 4 * at_once, 0, st, a, err);
     };
     if (hd == 128)
-        return mm == 64 ? run(kv4_attn_tc_kernel<128, 64>, kv4_attn_join_kernel<128, 64>, KtCfg<128, 64>::SMEM, 4)
-                        : run(kv4_attn_tc_kernel<128, 128>, kv4_attn_join_kernel<128, 128>, KtCfg<128, 128>::SMEM, 5);
-    return mm == 64 ? run(kv4_attn_tc_kernel<64, 64>, kv4_attn_join_kernel<64, 64>, KtCfg<64, 64>::SMEM, 6)
-                    : run(kv4_attn_tc_kernel<64, 128>, kv4_attn_join_kernel<64, 128>, KtCfg<64, 128>::SMEM, 7);
+        return mm == 64 ? run(kv4_attn_tc_kernel<128, 64>, kv4_attn_join_kernel<128, 64>, KtCfg<128, 64>::SMEM, 4,
+                              KjCfg<128, 64>::AT_ONCE)
+                        : run(kv4_attn_tc_kernel<128, 128>, kv4_attn_join_kernel<128, 128>, KtCfg<128, 128>::SMEM, 5,
+                              KjCfg<128, 128>::AT_ONCE);
+    return mm == 64 ? run(kv4_attn_tc_kernel<64, 64>, kv4_attn_join_kernel<64, 64>, KtCfg<64, 64>::SMEM, 6,
+                              KjCfg<64, 64>::AT_ONCE)
+                    : run(kv4_attn_tc_kernel<64, 128>, kv4_attn_join_kernel<64, 128>, KtCfg<64, 128>::SMEM, 7,
+                              KjCfg<64, 128>::AT_ONCE);
 }
 
 }  // namespace dfl
