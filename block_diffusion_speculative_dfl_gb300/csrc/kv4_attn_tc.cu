@@ -2,9 +2,9 @@
 // on the 5th-generation tensor cores.  The same sum and the same line of work
 // units as kv4_attn.cu, with up to 128 rows to a triple, where products and
 // exponentials, not bytes, are most of the work.  A block of 16 at 4 query heads
-// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 58 us, 280 TFLOP/s
+// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 57 us, 290 TFLOP/s
 // of products and 1.5 TB/s of cache; 64 rows of a head of 64 over 33,333 to
-// 100,001 tokens: 92 us.
+// 100,001 tokens: 90 us.
 //
 // One CTA per SM, two pipelines of eight warps, each with a range of the line of
 // its own, so that one pipeline's products run under the other's exponentials:
@@ -724,9 +724,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     }
 }
 
-// See KaLine.  A seam of 8 units of 128 keys: the block of 16 above takes 67 us
-// as whole triples and 70 cut (before the expansion was made faster); a weight
-// of 1, 2 or 3 gives the same times with long triples.
+// See KaLine.  The block of 16 above takes 57 us as whole triples and 60 cut,
+// with twice the query heads 79 and 88.  Weights of 1 and 3 give the same times.
 constexpr int KT_SEAM = 8;
 constexpr int KT_WEIGHT = 1;
 constexpr int KT_SMS = 152;   // SMs of a GB300
