@@ -828,7 +828,8 @@ dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const 
         if (p.layers < a->D || p.Hkv != a->Hkv || p.hd != a->hd || paged->pages.N != a->N) return DFL_ERR_INVALID_ARG;
         if ((int64_t)paged->pages.max_pages * p.page > a->C) return DFL_ERR_INVALID_ARG;
         if (!aligned4(paged->n_new) || !aligned4(paged->start)) return DFL_ERR_MISALIGNED;
-        if (a->B > 64) return DFL_ERR_UNSUPPORTED_SHAPE;
+        if (!pages_fit(paged->pages)) return DFL_ERR_UNSUPPORTED_SHAPE;
+        if ((rc = kv4_attn_check(p, paged->pages, a->B, a->Hq)) != DFL_OK) return rc;
         return step_bf16_shape(a);
     }
     return DFL_OK;

@@ -41,7 +41,7 @@ dfl_status pages_check(const dfl_kv4_pool* pool, const dfl_pages* pg, const void
     if (!pg || !pg->ref || !ws) return DFL_ERR_INVALID_ARG;
     const dfl_status rc = kv4_check(pool, 0, pg);
     if (rc != DFL_OK) return rc;
-    if ((int64_t)pg->N * pg->max_pages >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;   // page counts are summed in 32 bits
+    if (!pages_fit(*pg)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(ws)) return DFL_ERR_MISALIGNED;
     return ws_bytes < need ? DFL_ERR_WORKSPACE : DFL_OK;
 }
@@ -84,8 +84,7 @@ extern "C" dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, cons
     dfl_status rc = kv4_check(pool, layer, pages);
     if (rc != DFL_OK) return rc;
     if (Hq % pool->Hkv != 0) return DFL_ERR_INVALID_ARG;
-    if (B > 64 || (int64_t)B * (Hq / pool->Hkv) > KV4_MAX_HEAD_ROWS || !rows_fit((int64_t)pages->N * B))
-        return DFL_ERR_UNSUPPORTED_SHAPE;
+    if ((rc = kv4_attn_check(*pool, *pages, B, Hq)) != DFL_OK) return rc;
     const void* ptrs[] = {Q, Kb, Vb, O, ws};
     for (const void* p : ptrs) if (!aligned16(p)) return DFL_ERR_MISALIGNED;
     if (ws_bytes < kv4_attn_ws_bytes(pages->N, B, Hq, pool->Hkv, pool->hd)) return DFL_ERR_WORKSPACE;

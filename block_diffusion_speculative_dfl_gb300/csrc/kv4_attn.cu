@@ -535,9 +535,27 @@ int ka_groups(int nt) { return nt == 1 ? KaCfg<128, 1>::GROUPS : KaCfg<128, 2>::
 // CTAs of the launch: one per SM, fewer when there are fewer units.
 int ka_grid(int64_t units) { return (int)std::min<int64_t>(units, KA_SMS); }
 
+// Rows of a triple, row tiles of a K/V head, keys of a unit, places of a triple.
+int ka_rows(int R) { return R > KA_MAX_ROWS ? kv4_attn_tc_rows(R) : 8 * ka_nt(R); }
+int ka_subs(int R) { return (R + ka_rows(R) - 1) / ka_rows(R); }
+int ka_unit_log2(int R, int hd) { return R > KA_MAX_ROWS ? kv4_attn_tc_unit_log2(R, hd) : 6; }   // KA_UNIT
+int ka_weight(int R) { return R > KA_MAX_ROWS ? kv4_attn_tc_weight() : KA_WEIGHT; }
+int64_t ka_most_units(const dfl_kv4_pool& pool, const dfl_pages& pg, int R) {
+    return ((int64_t)pg.max_pages * pool.page >> ka_unit_log2(R, pool.hd)) + 2 + ka_weight(R);
+}
+
 inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 }  // namespace
+
+dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq) {
+    const int G = Hq / pool.Hkv;
+    if (B > 64 || (int64_t)B * G > KV4_MAX_HEAD_ROWS || !rows_fit((int64_t)pg.N * B)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    const int R = B * G;
+    const int64_t triples = (int64_t)pool.Hkv * ka_subs(R) * pg.N;
+    if (triples >= (int64_t)1 << 31 || triples * ka_most_units(pool, pg, R) >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
+    return DFL_OK;
+}
 
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
     if (N <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
@@ -552,13 +570,12 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
                         const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st) {
     const int G = Hq / pool.Hkv, R = B * G, nt = ka_nt(R);
     const bool tc = R > KA_MAX_ROWS;
-    const int rows = tc ? kv4_attn_tc_rows(R) : 8 * nt;
+    const int rows = ka_rows(R);
     KaArgs a{};
     a.slab = kv4_slab(pool, layer);
     a.table = pg.table; a.len = pg.len; a.max_pages = pg.max_pages;
     a.N = pg.N; a.B = B; a.Hq = Hq; a.G = G; a.R = R;
-    a.subs = (R + rows - 1) / rows;
-    if ((int64_t)pg.N * pool.Hkv * a.subs >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
+    a.subs = ka_subs(R);
     a.HS = pool.Hkv * a.subs;
     a.g_inv = (((uint64_t)1 << 40) + G - 1) / G;
     a.cells_inv = (((uint64_t)1 << 36) + a.slab.cells - 1) / a.slab.cells;
@@ -569,12 +586,11 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.scale_log2 = 1.4426950408889634f / sqrtf((float)pool.hd);
     a.k_pow2 = kv4_exp2i(pool.k_exp); a.k_inv = kv4_exp2i(-pool.k_exp);
     a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
-    a.unit_log2 = tc ? kv4_attn_tc_unit_log2(R, pool.hd) : 6;   // KA_UNIT
-    a.weight = tc ? kv4_attn_tc_weight() : KA_WEIGHT;
+    a.unit_log2 = ka_unit_log2(R, pool.hd);
+    a.weight = ka_weight(R);
     a.seam = tc ? kv4_attn_tc_seam() : KA_SEAM;
     static_assert(KA_UNIT == 64, "unit_log2");
-    const int64_t units = (((int64_t)pg.max_pages * pool.page >> a.unit_log2) + 2 + a.weight) * pg.N * a.HS;
-    if (units >= ((int64_t)1 << 31)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    const int64_t units = ka_most_units(pool, pg, R) * pg.N * a.HS;   // < 2^31: kv4_attn_check
     if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, st);
     const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * rows;
     a.Opart = static_cast<float*>(ws);

@@ -20,6 +20,9 @@ inline Kv4Slab kv4_slab(const dfl_kv4_pool& p, int layer) {
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Page counts are summed over sequences in 32 bits.
+inline bool pages_fit(const dfl_pages& pg) { return (int64_t)pg.N * pg.max_pages < (int64_t)1 << 31; }
+
 // Host-side checks of a pool, a layer of it and (nullable) its page tables.
 dfl_status kv4_check(const dfl_kv4_pool* pool, int layer, const dfl_pages* pg);
 
@@ -32,6 +35,8 @@ dfl_status kv4_read_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
 
 // Attention over the cache and the block's own keys (kv4_attn.cu).
 constexpr int KV4_MAX_HEAD_ROWS = 65536;   // query rows of a K/V head: B * Hq / Hkv
+// kv4_attn_check: the sizes that attention takes beyond kv4_check's.
+dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq);
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd);
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
                         const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st);

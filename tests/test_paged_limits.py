@@ -40,3 +40,11 @@ def test_heads_of_a_pool():
     p = dfl.Kv4Pool(FAKE, 1 << 50, 1, 1, 16, 1 << 25, 64, 0, 0)
     pages = dfl.Pages(FAKE, FAKE, FAKE, 2, 4)
     assert dfl.load().dfl_kv4_append(C.byref(p), 0, C.byref(pages), FAKE, FAKE, 1, FAKE, FAKE, None) == SHAPE
+
+
+@pytest.mark.parametrize("N,max_pages,rc", [(1000, 1 << 15, WORKSPACE), (1 << 15, 1 << 15, SHAPE), (1 << 25, 1, WORKSPACE),
+                                            (1 << 29, 1, SHAPE)])
+def test_units_of_work(N, max_pages, rc):
+    pages = dfl.Pages(FAKE, FAKE, FAKE, N, max_pages)
+    got = dfl.load().dfl_kv4_attn(C.byref(pool(Hkv=8)), 0, C.byref(pages), FAKE, FAKE, FAKE, 1, 8, FAKE, FAKE, 0, None)
+    assert got == rc
