@@ -98,6 +98,13 @@ __device__ __forceinline__ uint32_t hmul2u(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Pairwise maximum of two 16-bit unsigned numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);

@@ -59,13 +59,6 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Pairwise maximum of two 16-bit unsigned numbers.
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 // Eight of the block's own bf16 elements in units of the pool's power of two
 // (inv: its inverse), as fp16.  bf16's 8 bits survive from 2^-14 of the unit
 // up; finite values past fp16's range become its largest, as the cache's
