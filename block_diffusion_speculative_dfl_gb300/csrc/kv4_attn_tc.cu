@@ -56,9 +56,11 @@ struct KtCfg {
     static constexpr int TILE = KB * TKB;
     static constexpr int Q = KB * QKB;
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
-    // slots per pipeline: K or V codes of an expander's share of a unit, K and V tiles
-    static constexpr int RST = HD == 128 ? (KU == 128 ? 3 : 6) : 4, ST = HD == 64 ? 2 : 1;
-    static constexpr int SLOT = KU / 4 / KV4_CELL_TOKENS * CELL / 2;
+    // slots per pipeline: codes of an expander's share of a unit (K and V as one copy where a few of them fit, else one
+    // after the other), K and V tiles
+    static constexpr int PARTS = HD == 64 ? 1 : 2;
+    static constexpr int RST = HD == 64 || KU == 128 ? 3 : 6, ST = HD == 64 ? 2 : 1;
+    static constexpr int SLOT = KU / 4 / KV4_CELL_TOKENS * CELL / PARTS;
     static constexpr int PIPE = Q + 2 * ST * TILE + RST * 4 * SLOT;
     static constexpr int S_COL = 0, O_COL = 128, COLS = 256;
     static constexpr int SMEM = 1024 + KT_PIPES * PIPE;
@@ -236,11 +238,12 @@ __device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t 
 }
 
 // Bulk copies of the half cells that one expander warp needs, ahead of their use.
-// A warp's share of a unit is KU / 4 keys; its K half cells are one ring slot
-// and one step, its V half cells the next.  Steps are numbered along a sequence.
-template <int HD, int KU, int RST>
+// A warp's share of a unit is KU / 4 keys; its cells are one ring slot and one
+// step (PARTS = 1), or its K half cells are and its V half cells the next (2).
+// Steps are numbered along a sequence.
+template <int HD, int KU, int RST, int PARTS>
 struct KtFeed {
-    static constexpr int HALF = Kv4Cell<HD>::BYTES / 2, SHARE = KU / 4, NC = SHARE / KV4_CELL_TOKENS;
+    static constexpr int PART = Kv4Cell<HD>::BYTES / PARTS, SHARE = KU / 4, NC = SHARE / KV4_CELL_TOKENS;
     static constexpr int WIN = 32 / NC;   // units whose cells the lanes hold
     const KaArgs& a;
     const DevErr& err;
@@ -268,28 +271,28 @@ struct KtFeed {
         while (st == end) {
             if (!pos.enter(x, x1)) return false;
             const int u1 = min(pos.nu, pos.u + (x1 - x));
-            st = 2 * pos.u;
+            st = PARTS * pos.u;
             len = pos.len; n = pos.n; head = pos.head;
-            end = max(st, 2 * min(u1, (len - w * SHARE + KU - 1) / KU));   // units with a token of this warp's
+            end = max(st, PARTS * min(u1, (len - w * SHARE + KU - 1) / KU));   // units with a token of this warp's
             x += u1 - pos.u;
             if (u1 == pos.nu) pos.next_triple(a);
-            win = (st >> 1) - WIN;
+            win = st / PARTS - WIN;
         }
         return true;
     }
     // That step; one slot is free.
     __device__ __forceinline__ void produce() {
-        const int u = st >> 1;
+        const int u = st / PARTS;
         if (u == win + WIN) window(u);
         const int c0 = __shfl_sync(0xFFFFFFFFu, cells, NC * (u - win));
         const int c1 = NC == 2 ? __shfl_sync(0xFFFFFFFFu, cells, NC * (u - win) + 1) : 0;
         const bool more_than_one = NC == 2 && u * KU + w * SHARE + KV4_CELL_TOKENS < len;
         if (elect_one()) {
-            uint8_t* d = ring + slot * NC * HALF;
-            const uint8_t* base = a.slab.data + (st & 1) * HALF;
-            mbar_arrive_expect_tx(&full[slot], more_than_one ? 2 * HALF : HALF);
-            bulk_g2s(d, base + (int64_t)c0 * (2 * HALF), HALF, &full[slot]);
-            if (more_than_one) bulk_g2s(d + HALF, base + (int64_t)c1 * (2 * HALF), HALF, &full[slot]);
+            uint8_t* d = ring + slot * NC * PART;
+            const uint8_t* base = a.slab.data + st % PARTS * PART;
+            mbar_arrive_expect_tx(&full[slot], more_than_one ? 2 * PART : PART);
+            bulk_g2s(d, base + (int64_t)c0 * (PARTS * PART), PART, &full[slot]);
+            if (more_than_one) bulk_g2s(d + PART, base + (int64_t)c1 * (PARTS * PART), PART, &full[slot]);
         }
         __syncwarp();
         slot = slot + 1 == RST ? 0 : slot + 1;
@@ -300,12 +303,13 @@ struct KtFeed {
 
 // One expander warp: a quarter of the keys of the K tile, then of the V tile, of
 // all units of a range.
-template <int HD, int KU, int RST, int ST>
+template <int HD, int KU, int RST, int PARTS, int ST>
 __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, volatile int* abort, int w, int lane,
                                             uint8_t* ring, uint64_t* raw_full, uint32_t tiles, int tile_bytes,
                                             uint64_t (*t_full)[ST], uint64_t (*t_empty)[ST], KaPos pos, int x0, int x1) {
     constexpr int HALF = Kv4Cell<HD>::BYTES / 2;
-    using Feed = KtFeed<HD, KU, RST>;
+    using Feed = KtFeed<HD, KU, RST, PARTS>;
+    constexpr int PART = Feed::PART;
     constexpr int SHARE = Feed::SHARE, NC = Feed::NC;
     Feed feed(a, err, ring, raw_full, w, lane, pos, x0, x1);
     KtRing<RST> r;
@@ -330,19 +334,20 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         const int left = (own ? a.B : pos.len - u * KU) - share;   // keys of the unit from this warp's first on
         #pragma unroll 1
         for (int half = 0; half < 2; ++half) {   // K, V
-            #pragma unroll 1
-            while (feed.issued < taken + RST && feed.more()) feed.produce();
+            if (PARTS == 2 || half == 0)
+                #pragma unroll 1
+                while (feed.issued < taken + RST && feed.more()) feed.produce();
             const bool cell = !own && left > 0;
-            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && (!cell || kt_wait(&raw_full[r.i], r.ph, err, abort));
+            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && (!cell || (PARTS == 1 && half) || kt_wait(&raw_full[r.i], r.ph, err, abort));
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
-            const uint32_t src = smem_u32(ring) + r.i * NC * HALF;
+            const uint32_t src = smem_u32(ring) + r.i * NC * PART + (PARTS == 1 ? half * HALF : 0);
             #pragma unroll 1
             for (int j = 0; j < NC; ++j) {   // 16 tokens at a time
                 const int lj = left - j * KV4_CELL_TOKENS;
                 if (!own && lj > 0) {
-                    if (half) KtExpandV<HD, KU>::run(src + j * HALF, t + j * 16 * 128, lane, lj);
-                    else KtExpandK<HD, KU>::run(src + j * HALF, t + j * 16 * 128, lane);
+                    if (half) KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, lj);
+                    else KtExpandK<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane);
                 } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
                     const int64_t at = ((int64_t)(pos.n * a.B + share + j * 16) * a.slab.Hkv + pos.head) * HD;
                     kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj,
@@ -352,7 +357,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
             fence_proxy_async_smem();
             __syncwarp();   // the slot has been read, the rows are written by every lane
             if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
-            if (cell) { ++taken; r.step(); }
+            if (cell && (PARTS == 2 || half)) { ++taken; r.step(); }
         }
         if (!ok) break;
         ts.step();
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 
     if (warp >= 8) {
         const int w = warp & 3;
-        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::ST>(a, err, abort, w, lane, sR + w * Cfg::RST * Cfg::SLOT, bb.raw_full[w], smem_u32(sK),
+        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::PARTS, Cfg::ST>(a, err, abort, w, lane, sR + w * Cfg::RST * Cfg::SLOT, bb.raw_full[w], smem_u32(sK),
                                                    Cfg::TILE, bb.t_full, bb.t_empty, pos, x0, x1);
     } else {
         // ------------------------------------------------------------- softmax
