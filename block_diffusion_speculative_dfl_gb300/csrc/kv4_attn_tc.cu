@@ -58,8 +58,8 @@ struct KtCfg {
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
     // slots per pipeline: codes of an expander's share of a unit (K and V as one copy where a few of them fit, else one
     // after the other), K and V tiles
-    static constexpr int PARTS = HD == 64 ? 1 : 2;
-    static constexpr int RST = HD == 64 || KU == 128 ? 3 : 6, ST = HD == 64 ? 2 : 1;
+    static constexpr int PARTS = HD == 64 || KU == 64 ? 1 : 2;
+    static constexpr int RST = 3, ST = HD == 64 ? 2 : 1;
     static constexpr int SLOT = KU / 4 / KV4_CELL_TOKENS * CELL / PARTS;
     static constexpr int PIPE = Q + 2 * ST * TILE + RST * 4 * SLOT;
     static constexpr int S_COL = 0, O_COL = 128, COLS = 256;
