@@ -195,6 +195,13 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
             #pragma unroll
             for (int i = 0; i < 4; ++i) w[4 * b + i] = lds32(codes + (4 * i + RPL * b) * Cell::ROW);
         }
+        if (left < KV4_CELL_TOKENS) {   // scale bytes of absent tokens
+            #pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int held = min(max((left - RPL * b - h + 3) >> 2, 0), 4);
+                sw[b] &= held == 4 ? 0xFFFFFFFFu : (1u << 8 * held) - 1;
+            }
+        }
         #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int c = HD == 128 && b ? pos ^ 8 : pos;
@@ -203,8 +210,7 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
             #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 4 * i + RPL * b;
-                uint32_t s = __byte_perm(sp[i >> 1], sp[i >> 1], i & 1 ? 0x3232 : 0x1010);
-                if (r + h >= left) s = 0;
+                const uint32_t s = __byte_perm(sp[i >> 1], sp[i >> 1], i & 1 ? 0x3232 : 0x1010);
                 sts128((at ^ ((r & 7) << 4)) + r * 128, kt_expand(w[4 * b + i], s));
             }
         }
@@ -332,6 +338,24 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         const bool own = u == pos.nu - 1;
         const int share = w * SHARE;
         const int left = (own ? a.B : pos.len - u * KU) - share;   // keys of the unit from this warp's first on
+        auto turn = [&](int half, auto&& expand) {
+            if (PARTS == 2 || half == 0)
+                if (feed.issued < taken + RST && feed.more()) feed.produce();
+            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && ((PARTS == 1 && half) || kt_wait(&raw_full[r.i], r.ph, err, abort));
+            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; return; }
+            const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
+            const uint32_t src = smem_u32(ring) + r.i * NC * PART + (PARTS == 1 ? half * HALF : 0);
+            #pragma unroll
+            for (int j = 0; j < NC; ++j) expand(src + j * PART, t + j * 16 * 128);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
+            if (PARTS == 2 || half) { ++taken; r.step(); }
+        };
+        if (!own && left >= SHARE && feed.issued > taken + 1) {
+            turn(0, [&](uint32_t src, uint32_t t) { KtExpandK<HD, KU>::run(src, t, lane); });
+            if (ok) turn(1, [&](uint32_t src, uint32_t t) { KtExpandV<HD, KU>::run(src, t, lane, KV4_CELL_TOKENS); });
+        } else
         #pragma unroll 1
         for (int half = 0; half < 2; ++half) {   // K, V
             if (PARTS == 2 || half == 0)
