@@ -609,39 +609,45 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                         }
                         tmem_st_wait();
                     }
-                    float mt = -INFINITY;
-                    #pragma unroll 1
-                    for (int k0 = 0; k0 < KPT; k0 += 32) {
-                        float s[32];
-                        if constexpr (HALF) tmem_ld32_hx2<KPT>(s_at + k0, s);
-                        else tmem_ld32(s_at + k0, s);
-                        float m4[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
-                        #pragma unroll
-                        for (int j = 0; j < 32; j += 2) m4[(j >> 1) & 3] = max3(m4[(j >> 1) & 3], s[j], s[j + 1]);
-                        mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-                    }
-                    if constexpr (HALF) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 16));
-                    mt *= mult;   // mult > 0: the maximum commutes
-                    const bool need = mt > m + KA_LAZY;
-                    if (__any_sync(0xFFFFFFFFu, need)) {
-                        const float mn = need ? mt : m, al = mn == m ? 1.f : ex2_ftz(m - mn);
-                        if (u > u0) {
-                            #pragma unroll 1
-                            for (int c = 0; c < OPT; c += 32) {
-                                float o[32];
-                                if constexpr (HALF) tmem_ld32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
-                                else tmem_ld32(my + Cfg::O_COL + c, o);
-                                #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] *= al;
-                                if constexpr (HALF) tmem_st32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
-                                else tmem_st32(my + Cfg::O_COL + c, o);
-                            }
+                    auto grow = [&] {   // the maximum; O is rescaled only where it grows by more than 2^8
+                        float mt = -INFINITY;
+                        #pragma unroll 1
+                        for (int k0 = 0; k0 < KPT; k0 += 32) {
+                            float s[32];
+                            if constexpr (HALF) tmem_ld32_hx2<KPT>(s_at + k0, s);
+                            else tmem_ld32(s_at + k0, s);
+                            float m4[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
+                            #pragma unroll
+                            for (int j = 0; j < 32; j += 2) m4[(j >> 1) & 3] = max3(m4[(j >> 1) & 3], s[j], s[j + 1]);
+                            mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                         }
-                        l *= al;
-                        m = mn;
-                    }
-                    const float2 off2 = make_float2(KA_LIFT - m, KA_LIFT - m), mult2 = make_float2(mult, mult);
-                    float2 l2[2] = {};
+                        if constexpr (HALF) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, 16));
+                        mt *= mult;   // mult > 0: the maximum commutes
+                        const bool need = mt > m + KA_LAZY;
+                        if (__any_sync(0xFFFFFFFFu, need)) {
+                            const float mn = need ? mt : m, al = mn == m ? 1.f : ex2_ftz(m - mn);
+                            if (u > u0) {
+                                #pragma unroll 1
+                                for (int c = 0; c < OPT; c += 32) {
+                                    float o[32];
+                                    if constexpr (HALF) tmem_ld32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
+                                    else tmem_ld32(my + Cfg::O_COL + c, o);
+                                    #pragma unroll
+                                    for (int j = 0; j < 32; ++j) o[j] *= al;
+                                    if constexpr (HALF) tmem_st32_hx2<HD / 2>(my + Cfg::O_COL + c, o);
+                                    else tmem_st32(my + Cfg::O_COL + c, o);
+                                }
+                            }
+                            l *= al;
+                            m = mn;
+                        }
+                    };
+                    float2 off2, l2[2];
+                    const float2 mult2 = make_float2(mult, mult);
+                    auto begin = [&] {
+                        off2 = make_float2(KA_LIFT - m, KA_LIFT - m);
+                        l2[0] = l2[1] = make_float2(0.f, 0.f);
+                    };
                     auto weigh16 = [&](int k0, uint32_t* pk) {   // weights of 16 of this thread's keys, two per word
                         float s[16];
                         if constexpr (HALF) tmem_ld16_hx2<KPT>(s_at + k0, s);
@@ -655,12 +661,24 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                             pk[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                     };
+                    auto sum = [&] { return (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y); };
                     // P, two keys per column, over the first half of S's columns
                     if constexpr (HALF) {   // both halves of a row share its columns: all of S is read first
+                        // The weights by the maximum that is known: they stand when no thread's sum shows one past
+                        // 2^15 (2^8 above the maximum); else, and at first, by the unit's own maximum.  With heads of
+                        // 128 the look at the maximum hides under the expansion (with it the block of 16 takes 51.7 us,
+                        // without 52.7); with heads of 64 it does not (64 rows over long contexts 81 and 74.5 us).
                         uint32_t pk[KPT / 16][8];
-                        #pragma unroll
-                        for (int g = 0; g < KPT / 16; ++g) weigh16(16 * g, pk[g]);
-                        __syncwarp();
+                        bool known = HD == 64 && u > u0;
+                        #pragma unroll 1
+                        while (true) {
+                            if (!known) grow();
+                            begin();
+                            #pragma unroll
+                            for (int g = 0; g < KPT / 16; ++g) weigh16(16 * g, pk[g]);
+                            if (!known || !__any_sync(0xFFFFFFFFu, !(sum() <= 32768.f))) break;
+                            known = false;
+                        }
                         #pragma unroll
                         for (int g = 0; g < KPT / 16; g += 2) {
                             uint32_t v[16];
@@ -669,6 +687,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                             tmem_st16u_hx2<KPT / 2>(s_at + 8 * g, v);
                         }
                     } else {
+                        grow();
+                        begin();
                         #pragma unroll 1
                         for (int k0 = 0; k0 < KPT; k0 += 16) {   // over columns already read
                             uint32_t pk[8];
@@ -676,7 +696,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                             tmem_st8u(s_at + k0 / 2, pk);
                         }
                     }
-                    l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+                    l += sum();
                     tmem_st_wait();
                 }
                 tc_fence_before();

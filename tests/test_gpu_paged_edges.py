@@ -82,6 +82,26 @@ def test_attention_over_cut_and_uncut_lines(B, Hq, Hkv, hd, lens):
     check(c, *run_attn(rng, c, lens, B, Hq), lens, which=which)
 
 
+@pytest.mark.parametrize("B,Hq", [(16, 4), (16, 8)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_maxima_that_grow_fall_and_jump(B, Hq, hd):
+    # keys sorted by their score, rows that see them rise and fall by much or little, and one key far above the rest
+    rng = np.random.default_rng(hd + Hq)
+    T, lens = 1500, [1500, 700]
+    c = make_cache(rng, 2, lens, 16, 1, hd)
+    K = torch.zeros((2, T, 1, hd), dtype=torch.bfloat16, device="cuda")
+    K[0, :, 0, 0] = torch.linspace(-6, 6, T).to(torch.bfloat16).cuda()
+    K[1, :, 0, 0] = (torch.rand(T, device="cuda") * 0.2).to(torch.bfloat16)
+    K[1, 333, 0, 0], K[1, 600, 0, 0] = 6.0, -6.0
+    V = bf16(rng, (2, T, 1, hd))
+    c.append(0, K, V, i32([0, 0]), i32(lens))
+    Q = torch.zeros((2, B, Hq, hd), dtype=torch.bfloat16, device="cuda")
+    Q[..., 0] = torch.tensor([200.0, -200.0, 30.0, -30.0, 6.0, -6.0, 1.0, 0.0], device="cuda").repeat(B * Hq // 8).view(B, Hq)
+    Kb, Vb = bf16(rng, (2, B, 1, hd)), bf16(rng, (2, B, 1, hd))
+    O = c.attn(0, Q, Kb, Vb)
+    check(c, host(K).astype(np.float64), host(V).astype(np.float64), Q, Kb, Vb, O, lens)
+
+
 @pytest.mark.parametrize("B,Hq", [(3, 2), (16, 8)])
 @pytest.mark.parametrize("hd", [64, 128])
 def test_own_rows_past_fp16_and_below_it(B, Hq, hd):
