@@ -521,7 +521,7 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 // Row tiles of 8 query rows when a group has at most 8, of 16 up to 16: a wider
 // tile expands each key for more rows at once.  More rows go to the
 // tensor-memory kernel: 32 sequences of 2,048 tokens with 16 rows to a head take
-// 39 us here and 58 there, with 32 rows 64 and 56.
+// 39 us here and 52 there, with 32 rows 64 and 52.
 // See KaLine.  The weight: a triple costs some 4.5 us beside 1.1 us per unit
 // (the batch above 107, 102 and 103 us with weights 2, 4 and 6).
 constexpr int KA_SEAM = 8;

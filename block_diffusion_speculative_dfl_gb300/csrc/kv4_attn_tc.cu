@@ -2,9 +2,9 @@
 // on the 5th-generation tensor cores.  The same sum and the same line of work
 // units as kv4_attn.cu, with up to 128 rows to a triple, where products and
 // exponentials, not bytes, are most of the work.  A block of 16 at 4 query heads
-// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 57 us, 290 TFLOP/s
-// of products and 1.5 TB/s of cache; 64 rows of a head of 64 over 33,333 to
-// 100,001 tokens: 90 us.
+// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 52 us, 310 TFLOP/s
+// of products and 1.6 TB/s of cache; 64 rows of a head of 64 over 33,333 to
+// 100,001 tokens: 75 us.
 //
 // One CTA per SM, two pipelines of eight warps, each with a range of the line of
 // its own, so that one pipeline's products run under the other's exponentials:
@@ -22,16 +22,18 @@
 // fifth place on its scheduler and with it 32 registers from every thread.
 //
 // What bounds it: how fast one warp issues, about one instruction in 4.7 clocks
-// with four warps to a scheduler (dependent instructions, branches, fetches).
-// Per unit of 128 keys and 64 rows (hd = 128) a pipeline's clocks are
-//   expanders  2 x 1,150 of expansion, 1,100 of copies ahead, 1,000 of waits
-//              and arrivals: 4,500, the longest turn;
-//   products   S 900 to its commit, softmax 1,450, P V 1,000, its end 250, the
-//              next S 380 to be seen: 4,000, hidden under it.
-// At hd = 64 the two trade places.  Hence units of 128 keys where shared and
-// tensor memory allow (64 at hd = 128 with 128 rows), and four expanders on K,
-// then on V: two on each waited for their one tile's product in turn (64-row
-// heads of 64 over long contexts 98 against 92 us).
+// with four warps to a scheduler (dependent instructions, branches, fetches), so
+// control code counts: the expanders' full units have a path of their own (the
+// block of 16 above 57 us without).  Clocks of a pipeline per unit of 128 keys and
+// 64 rows:
+//   hd = 128  expanders 2 x 1,000 of expansion, 950 of copies ahead, 1,100 of
+//             waits and arrivals: 4,100, the longest turn; S 900 to its commit,
+//             450 until it is seen, softmax 1,500, P V 900, its end 260;
+//   hd = 64   the products' chain, 2,900: S, 500, softmax 1,100, P V 640, 190;
+//             the expanders wait for it.
+// Hence units of 128 keys where shared and tensor memory allow (64 at hd = 128
+// with 128 rows), and four expanders on K, then on V: two on each waited for
+// their one tile's product in turn (64-row heads of 64 98 against 92 us then).
 #include "internal.h"
 #include "kv4_attn.cuh"
 #include "paged.h"
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     }
 }
 
-// See KaLine.  The block of 16 above takes 57 us as whole triples and 60 cut,
+// See KaLine.  The block of 16 above took 57 us as whole triples and 60 cut,
 // with twice the query heads 79 and 88.  Weights of 1 and 3 give the same times.
 constexpr int KT_SEAM = 8;
 constexpr int KT_WEIGHT = 1;
