@@ -17,7 +17,7 @@
 // A range belongs to a group of four warps; warp w takes tokens 16w .. 16w + 15
 // (one cell) of every unit with its own running maximum, sum and O, so the
 // warps meet only at the end of a triple.  One CTA per SM holds four such groups
-// (three with 16 rows): as CTAs of their own the hardware put five on one SM
+// (three with 16 rows of 128): as CTAs of their own the hardware put five on one SM
 // and three on another, and all waited for the five.  Each warp keeps a ring of
 // cells in flight (one bulk copy of 18 hd bytes each, K, V and scales together)
 // and expands codes in registers straight into operand fragments:
@@ -53,7 +53,7 @@ namespace {
 constexpr int KA_UNIT = 64;        // keys per unit
 constexpr int KA_WARPS = 4;        // of a group: one cell of 16 keys per warp and unit
 constexpr int KA_THREADS = KA_WARPS * 32;
-constexpr int KA_SLOTS = 4;        // cells in flight per warp
+constexpr int KA_SLOTS = 3;        // cells in flight per warp
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -74,12 +74,13 @@ struct KaCfg {
     static constexpr int MT = HD / 16;                // 16-dim tiles of O^T
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
     static constexpr int PITCH = HD + 4;              // floats per row of the warps' O in shared memory
-    static constexpr int GROUPS = NT == 1 ? 4 : 3;    // per CTA (registers)
+    static constexpr int GROUPS = HD == 128 && NT == 2 ? 3 : 4;   // per CTA (registers)
     static constexpr int THREADS = GROUPS * KA_THREADS;
     static constexpr int RING = KA_WARPS * KA_SLOTS * CELL;
-    static constexpr int MERGE = KA_WARPS * ROWS * PITCH * 4;
+    static constexpr int MERGE = KA_WARPS * 8 * PITCH * 4;   // of one 8-row tile
+    static constexpr int QS = NT == 1 ? 0 : ROWS * HD * 2;   // Q of two tiles is read from here: registers (see below)
     static constexpr int ML = KA_WARPS * ROWS * 8;
-    static constexpr int GROUP = (RING + MERGE + ML + KA_WARPS * KA_SLOTS * 8 + 127) / 128 * 128;
+    static constexpr int GROUP = (RING + MERGE + QS + ML + KA_WARPS * KA_SLOTS * 8 + 127) / 128 * 128;
     static constexpr int SMEM = GROUPS * GROUP;
     static_assert(SMEM <= 226 * 1024, "shared memory");
 };
@@ -201,8 +202,9 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
     uint8_t* sm = smem + group * Cfg::GROUP;
     uint8_t* ring = sm + warp * KA_SLOTS * Cfg::CELL;
     float* merge = reinterpret_cast<float*>(sm + Cfg::RING);
-    float2* mlsm = reinterpret_cast<float2*>(sm + Cfg::RING + Cfg::MERGE);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + Cfg::RING + Cfg::MERGE + Cfg::ML) + warp * KA_SLOTS;
+    uint4* qs = reinterpret_cast<uint4*>(sm + Cfg::RING + Cfg::MERGE);
+    float2* mlsm = reinterpret_cast<float2*>(sm + Cfg::RING + Cfg::MERGE + Cfg::QS);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + Cfg::RING + Cfg::MERGE + Cfg::QS + Cfg::ML) + warp * KA_SLOTS;
     if (lane == 0) {
         for (int i = 0; i < KA_SLOTS; ++i) mbar_init(&full[i], 1);
         fence_barrier_init();
@@ -239,32 +241,48 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
         const int head = pos.head, row0 = pos.tile * Cfg::ROWS;
         const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
         // ---- Q of this triple: lane (g, t) holds row g's quarter t of each 8-row tile
-        uint32_t q[NT][2 * Cfg::KSTEPS];
+        uint32_t q1[2 * Cfg::KSTEPS];   // (NT = 1)
         float mult[NT][2];   // rows 2t, 2t + 1: score of fp16 operands -> log2 units
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = row0 + nt * 8 + g;
+            uint32_t q[2 * Cfg::KSTEPS];
             uint32_t mx = 0;
             const uint4* src = reinterpret_cast<const uint4*>(
                 a.Q + ka_row(a, pos.n, head, r, HD) + t * (HD / 4));
             #pragma unroll
             for (int i = 0; i < HD / 32; ++i) {
                 const uint4 w = r < a.R ? src[i] : make_uint4(0, 0, 0, 0);
-                q[nt][4 * i] = w.x; q[nt][4 * i + 1] = w.y; q[nt][4 * i + 2] = w.z; q[nt][4 * i + 3] = w.w;
+                q[4 * i] = w.x; q[4 * i + 1] = w.y; q[4 * i + 2] = w.z; q[4 * i + 3] = w.w;
             }
             #pragma unroll
-            for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) mx = max(mx, max(q[nt][i] & 0x7FFFu, (q[nt][i] >> 16) & 0x7FFFu));
+            for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) mx = max(mx, max(q[i] & 0x7FFFu, (q[i] >> 16) & 0x7FFFu));
             mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
             int e = (int)(mx >> 7);                       // biased exponent of the row's largest element
             e = (e == 0 || e >= 254) ? 127 : e;           // zero, subnormal, huge or not finite: as it is
             const float down = __int_as_float((254 - e) << 23);
             #pragma unroll
-            for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) q[nt][i] = pack_half(bf16lo(q[nt][i]) * down, bf16hi(q[nt][i]) * down);
+            for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) q[i] = pack_half(bf16lo(q[i]) * down, bf16hi(q[i]) * down);
+            if constexpr (NT == 1) {
+                #pragma unroll
+                for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) q1[i] = q[i];
+            } else if (warp == nt) {   // a warp per tile writes it for all
+                #pragma unroll
+                for (int i = 0; i < HD / 32; ++i) qs[(nt * (HD / 32) + i) * 32 + lane] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+            }
             const float up = __int_as_float(e << 23) * a.scale_log2 * a.k_pow2;
             mult[nt][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * t);       // lane of row 2t
             mult[nt][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * t + 4);   // lane of row 2t + 1
         }
+        // Two tiles' Q would take 32 registers beside 64 of O (hd = 128): spilled, 16 rows over the single-token
+        // batch's lengths take 150 us, read from shared memory 136.
+        if constexpr (NT > 1) group_sync(group);
+        // words 4i .. 4i + 3 of this lane's quarter of its row of tile nt
+        auto q_words = [&](int nt, int i) {
+            if constexpr (NT == 1) return make_uint4(q1[4 * i], q1[4 * i + 1], q1[4 * i + 2], q1[4 * i + 3]);
+            else return qs[(nt * (HD / 32) + i) * 32 + lane];
+        };
         KaAcc<HD, NT> acc;
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -328,7 +346,10 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t af[4] = {h0[2 * j], h1[2 * j], h0[2 * j + 1], h1[2 * j + 1]};
                         #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], af, q[nt][4 * w + 2 * j], q[nt][4 * w + 2 * j + 1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 qw = q_words(nt, w);
+                            mma_f16(s[nt], af, j ? qw.z : qw.x, j ? qw.w : qw.y);
+                        }
                     }
                 }
             }
@@ -419,8 +440,9 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
                 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(s[nt], f0, q[nt][4 * i], q[nt][4 * i + 1]);
-                    mma_f16(s[nt], f1, q[nt][4 * i + 2], q[nt][4 * i + 3]);
+                    const uint4 qw = q_words(nt, i);
+                    mma_f16(s[nt], f0, qw.x, qw.y);
+                    mma_f16(s[nt], f1, qw.z, qw.w);
                 }
             }
             #pragma unroll
@@ -455,7 +477,8 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
         }
         // ---- the warps' parts of this triple
         #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {   // a tile at a time: shared memory
+            if (nt > 0) group_sync(group);
             #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float l = acc.l[nt][r];
@@ -463,19 +486,18 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
                 const int row = nt * 8 + 2 * t + r;
                 if (g == 0) mlsm[warp * Cfg::ROWS + row] = make_float2(acc.m[nt][r], l);
-                float* dst = merge + (warp * Cfg::ROWS + row) * Cfg::PITCH + g * (HD / 8);
+                float* dst = merge + (warp * 8 + 2 * t + r) * Cfg::PITCH + g * (HD / 8);
                 #pragma unroll
                 for (int i = 0; i < Cfg::MT; i += 2)
                     *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc.o[nt][i][r], acc.o[nt][i][r + 2],
                                                                           acc.o[nt][i + 1][r], acc.o[nt][i + 1][r + 2]);
             }
-        group_sync(group);
-        {
+            group_sync(group);
             const bool whole = u0 == 0 && u1 == pos.nu;
             const int part = 2 * range + (u0 == 0 ? 1 : 0);
             constexpr int TPR = HD / 4;   // threads per row
             #pragma unroll 1
-            for (int row = tid / TPR; row < Cfg::ROWS; row += KA_THREADS / TPR) {
+            for (int row = nt * 8 + tid / TPR; row < nt * 8 + 8; row += KA_THREADS / TPR) {
                 const int r = row0 + row, c = (tid % TPR) * 4;
                 if (r >= a.R) break;
                 float2 ml[KA_WARPS];
@@ -486,7 +508,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 #pragma unroll
                 for (int w = 0; w < KA_WARPS; ++w) {
                     const float f = ml[w].x == -INFINITY ? 0.f : ex2_ftz(ml[w].x - M);
-                    const float4 v = *reinterpret_cast<const float4*>(merge + (w * Cfg::ROWS + row) * Cfg::PITCH + c);
+                    const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row - nt * 8) * Cfg::PITCH + c);
                     L += f * ml[w].y;
                     o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                 }
@@ -521,7 +543,7 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 // Row tiles of 8 query rows when a group has at most 8, of 16 up to 16: a wider
 // tile expands each key for more rows at once.  More rows go to the
 // tensor-memory kernel: 32 sequences of 2,048 tokens with 16 rows to a head take
-// 39 us here and 52 there, with 32 rows 64 and 52.
+// 37 us here and 52 there, with 32 rows 64 and 52.
 // See KaLine.  The weight: a triple costs some 4.5 us beside 1.1 us per unit
 // (the batch above 107, 102 and 103 us with weights 2, 4 and 6).
 constexpr int KA_SEAM = 8;
@@ -530,7 +552,7 @@ constexpr int KJ_ROWS = KjCfg<128, 8>::AT_ONCE;
 constexpr int KA_MAX_ROWS = 16;
 int ka_nt(int R) { return R <= 8 ? 1 : 2; }
 
-int ka_groups(int nt) { return nt == 1 ? KaCfg<128, 1>::GROUPS : KaCfg<128, 2>::GROUPS; }
+int ka_groups(int hd, int nt) { return hd == 128 && nt == 2 ? KaCfg<128, 2>::GROUPS : KaCfg<128, 1>::GROUPS; }
 
 // CTAs of the launch: one per SM, fewer when there are fewer units.
 int ka_grid(int64_t units) { return (int)std::min<int64_t>(units, KA_SMS); }
@@ -562,8 +584,8 @@ size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
     if ((int64_t)B * (Hq / Hkv) > KV4_MAX_HEAD_ROWS) return 0;
     const int R = B * (Hq / Hkv), nt = ka_nt(R);
     if (R > KA_MAX_ROWS) return kv4_attn_tc_ws_bytes(R, hd);
-    const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * 8 * nt;
-    return al256(parts * hd * 4) + al256(parts * 8) + al256(sizeof(KaCross) * KA_SMS * ka_groups(nt));
+    const size_t parts = 2 * (size_t)KA_SMS * ka_groups(hd, nt) * 8 * nt;
+    return al256(parts * hd * 4) + al256(parts * 8) + al256(sizeof(KaCross) * KA_SMS * ka_groups(hd, nt));
 }
 
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
@@ -592,11 +614,11 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     static_assert(KA_UNIT == 64, "unit_log2");
     const int64_t units = ka_most_units(pool, pg, R) * pg.N * a.HS;   // < 2^31: kv4_attn_check
     if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, st);
-    const size_t parts = 2 * (size_t)KA_SMS * ka_groups(nt) * rows;
+    const size_t parts = 2 * (size_t)KA_SMS * ka_groups(pool.hd, nt) * rows;
     a.Opart = static_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
     a.cross = reinterpret_cast<KaCross*>(reinterpret_cast<uint8_t*>(a.ml) + al256(parts * 8));
-    const int grid = ka_grid(units), groups = ka_groups(nt);
+    const int grid = ka_grid(units), groups = ka_groups(pool.hd, nt);
     const DevErr err = dev_err(ctx);
     auto run = [&](auto kern, auto join, int smem, int slot) -> dfl_status {
         if (!ctx->kv4_attr_set[slot]) {
