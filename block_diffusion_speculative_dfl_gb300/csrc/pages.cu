@@ -10,6 +10,13 @@
 // bytes (pages copied or moved in every layer, table entries) are the second
 // kernel's, spread over all SMs in 16-KB pieces; it finds its list on the
 // device, so neither call reads anything back to the host.
+//
+// Measured (replayed): 256 forked sequences that copy their last page in 7 layers
+// (256 MB read and written) 37 us, 8 of them the plan; moving the scattered half
+// of a pool of 7 layers (525 MB) 95 us, 9 of them the plan, the moves at 90 % of
+// a plain copy's rate; reordering 512 rows of 1,024 pages 11-12 us.  Copies go
+// through registers: rings of bulk copies through shared memory moved the pool in
+// 98 to 101 us.
 #include "internal.h"
 #include "paged.h"
 
