@@ -260,6 +260,31 @@ def test_page_operations_write_only_theirs(N, page, num_pages, max_pages):
         same()
 
 
+@pytest.mark.parametrize("N,Hkv,layers", [(1, 1, 1), (6, 2, 3), (28, 2, 2), (29, 2, 2), (200, 1, 1)])
+def test_shared_last_pages_are_copied(N, Hkv, layers):
+    # pages of 4,608 bytes with two heads: 28 sequences in two layers are the most that the planning block copies itself
+    rng = np.random.default_rng(N)
+    page, num = 32, 4 * N + 5
+    c = dfl.PagedCache(layers, num, page, Hkv, 64, N, 3)
+    c.data.random_(0, 256)
+    b = ko.PageBook(host(c.table), host(c.len), host(c.ref), page)
+    data = c.data.clone()
+    first = np.zeros(N, int)
+    first[0] = 40
+    for new in (first, None, rng.integers(0, 20, N), rng.integers(0, 20, N)):
+        if new is None:   # everyone forks sequence 0
+            c.remap(i32(np.zeros(N)))
+            b.remap(np.zeros(N, int))
+            continue
+        new = np.minimum(new, 96 - b.len)
+        start, copies = b.reserve(new)
+        assert np.array_equal(host(c.reserve(i32(new))), start)
+        for s, d in copies:
+            data[:, d] = data[:, s]
+        assert torch.equal(c.data, data)
+        assert np.array_equal(host(c.table), b.table) and np.array_equal(host(c.ref), b.ref)
+
+
 @pytest.mark.parametrize("N,max_pages", [(1, 1), (3, 7), (9, 33), (4096, 1), (8, 512), (8, 513), (700, 600)])
 def test_remap_of_tables_of_every_size(N, max_pages):
     # up to 4,096 entries are one block's
