@@ -10,6 +10,7 @@ another, and so do two graphs captured from it.
 from __future__ import annotations
 
 import ctypes as C
+from contextlib import nullcontext
 
 import torch
 
@@ -66,6 +67,15 @@ class PagedCache:
             return torch._C._cuda_getCurrentRawStream(self._index)
         return _lib._stream(stream)
 
+    def _on(self, stream):
+        """Allocations under it belong to the stream that the call launches on."""
+        if stream is None:
+            return nullcontext()
+        if isinstance(stream, int):   # (ExternalStream takes no null handle)
+            stream = (torch.cuda.ExternalStream(stream, device=self._index) if stream else
+                      torch.cuda.default_stream(self._index))
+        return torch.cuda.stream(stream)
+
     def _i32(self, x, what):
         if x.dtype is not torch.int32 or not x.is_contiguous() or x.get_device() != self._index or x.numel() != self.N:
             raise ValueError(f"{what} must be a contiguous int32 tensor of {self.N} elements on {self.book.device}")
@@ -102,19 +112,22 @@ class PagedCache:
     def attn(self, layer, Q, Kb, Vb, out=None, stream=None):
         """Block attention over each sequence's cached tokens and the block's own rows.
 
-        Q bf16 [N, B, Hq, hd], Kb, Vb bf16 [N, B, Hkv, hd]; returns O bf16 [N, B, Hq, hd].
+        Q bf16 [N, B, Hq, hd], Kb, Vb bf16 [N, B, Hkv, hd]; returns O bf16 [N, B, Hq, hd], allocated on the stream of
+        the call unless ``out`` is given.
         """
         q, B = self._rows(Q, "Q")
         Hq = Q.shape[2]
         k, _ = self._rows(Kb, "Kb", self.Hkv, B)
         v, _ = self._rows(Vb, "Vb", self.Hkv, B)
         if out is None:
-            out = torch.empty_like(Q)
+            with self._on(stream):
+                out = torch.empty_like(Q)
         o, _ = self._rows(out, "out", Hq, B)
         ws = self._attn_ws.get((B, Hq))
         if ws is None:
             need = _lib.workspace_size(_lib.DFL_OP_KV4_ATTN, N=self.N, B=B, Hq=Hq, Hkv=self.Hkv, hd=self.hd)
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.book.device)
+            with self._on(stream):
+                ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.book.device)
             ws = self._attn_ws[(B, Hq)] = (ws, ws.data_ptr(), ws.numel())
         rc = self._lib.dfl_kv4_attn(self._pool, layer, self._pages, q, k, v, B, Hq, o, ws[1], ws[2], self._st(stream))
         if rc:
