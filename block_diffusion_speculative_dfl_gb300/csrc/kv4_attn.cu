@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
             for (int i = 0; i < Cfg::MT; ++i)
                 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc.o[nt][i][c] = 0.f;
-            acc.m[nt][0] = acc.m[nt][1] = -INFINITY;
+            acc.m[nt][0] = acc.m[nt][1] = KA_NONE;
             acc.l[nt][0] = acc.l[nt][1] = 0.f;
         }
         // ---- context cells
@@ -501,13 +501,13 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 const int r = row0 + row, c = (tid % TPR) * 4;
                 if (r >= a.R) break;
                 float2 ml[KA_WARPS];
-                float M = -INFINITY, L = 0.f;
+                float M = KA_NONE, L = 0.f;
                 #pragma unroll
                 for (int w = 0; w < KA_WARPS; ++w) { ml[w] = mlsm[w * Cfg::ROWS + row]; M = fmaxf(M, ml[w].x); }
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                 #pragma unroll
                 for (int w = 0; w < KA_WARPS; ++w) {
-                    const float f = ml[w].x == -INFINITY ? 0.f : ex2_ftz(ml[w].x - M);
+                    const float f = ex2_ftz(ml[w].x - M);
                     const float4 v = *reinterpret_cast<const float4*>(merge + (w * 8 + row - nt * 8) * Cfg::PITCH + c);
                     L += f * ml[w].y;
                     o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;

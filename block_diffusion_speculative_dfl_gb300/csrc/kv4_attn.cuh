@@ -49,6 +49,10 @@ namespace {
 
 constexpr float KA_LAZY = 8.f;     // rescale when a maximum grows by more (log2)
 constexpr float KA_LIFT = 7.f;     // P is 2^7 above its nominal value
+// The running maximum before the first key: no finite score is below it.  A key
+// whose score is -inf has the weight 2^(-inf - m) = 0 with it; with -inf in its
+// place, keys that are all of that kind had weights of -inf + inf.
+constexpr float KA_NONE = -3.402823466e38f;
 
 // One lane of a converged warp.  What it issues (copies, products) has operands
 // the compiler knows to be uniform, at half the clocks of a lane in a divergent
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
     if (row >= ROWS || r >= a.R) return;
     // eight partials are read at once: a long triple waits for memory once per eight
     constexpr int BATCH = 8;
-    float M = -INFINITY, L = 0.f;
+    float M = KA_NONE, L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     #pragma unroll 1
     for (int j0 = first; j0 <= last; j0 += BATCH) {
@@ -264,12 +268,12 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
         }
         #pragma unroll
         for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, ml[i].x);
-        const float old = M == -INFINITY ? 0.f : ex2_ftz(M - mn);
+        const float old = ex2_ftz(M - mn);
         M = mn;
         L *= old; o.x *= old; o.y *= old; o.z *= old; o.w *= old;
         #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-            const float f = ml[i].x == -INFINITY || j0 + i > last ? 0.f : ex2_ftz(ml[i].x - M);
+            const float f = j0 + i > last ? 0.f : ex2_ftz(ml[i].x - M);
             L += f * ml[i].y;
             o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
         }

@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                     if (!HALF && HD == 128) prefetch_l2(p + HD / 2);
                 }
             }
-            float m = -INFINITY, l = 0.f;
+            float m = KA_NONE, l = 0.f;
             for (int u = u0; u < u1; ++u) {
                 ok = kt_wait(&bb.s_full, unit & 1, err, abort);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
