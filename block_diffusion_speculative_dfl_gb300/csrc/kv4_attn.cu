@@ -182,7 +182,7 @@ __device__ __forceinline__ void ka_softmax(KaAcc<HD, NT>& acc, float (&s)[NT][4]
     for (int nt = 0; nt < NT; ++nt) {
         #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const float off = KA_LIFT - acc.m[nt][r];
+            const float off = __fsub_rd(KA_LIFT, acc.m[nt][r]);
             s[nt][r] = ex2_ftz(s[nt][r] + off);
             s[nt][r + 2] = ex2_ftz(s[nt][r + 2] + off);
             acc.l[nt][r] += s[nt][r] + s[nt][r + 2];
@@ -354,10 +354,9 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 }
             }
             #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] *= mult[nt][0]; s[nt][1] *= mult[nt][1];
-                s[nt][2] *= mult[nt][0]; s[nt][3] *= mult[nt][1];
-            }
+            for (int nt = 0; nt < NT; ++nt)
+                #pragma unroll
+                for (int c = 0; c < 4; ++c) s[nt][c] = __fmul_rn(s[nt][c], mult[nt][c & 1]);   // rounded before 7 - m is added
             if (left < KV4_CELL_TOKENS) {   // the cell's last tokens do not exist
                 const bool v0 = Cell::token(g) < left, v1 = Cell::token(g + 8) < left;
                 #pragma unroll
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[nt][c] = (c < 2 ? b0 : b1) < a.B ? s[nt][c] * mult[nt][c & 1] : -INFINITY;
+                for (int c = 0; c < 4; ++c) s[nt][c] = (c < 2 ? b0 : b1) < a.B ? __fmul_rn(s[nt][c], mult[nt][c & 1]) : -INFINITY;
             ka_softmax<HD, NT>(acc, s);
             uint32_t pb[NT][2];
             #pragma unroll

@@ -48,7 +48,9 @@ dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void
 namespace {
 
 constexpr float KA_LAZY = 8.f;     // rescale when a maximum grows by more (log2)
-constexpr float KA_LIFT = 7.f;     // P is 2^7 above its nominal value
+// P is 2^7 above its nominal value, so at most 2^15: below fp16's largest.
+// 7 - m is rounded down: at large m up, it would lift P past that.
+constexpr float KA_LIFT = 7.f;
 // The running maximum before the first key: no finite score is below it.  A key
 // whose score is -inf has the weight 2^(-inf - m) = 0 with it; with -inf in its
 // place, keys that are all of that kind had weights of -inf + inf.

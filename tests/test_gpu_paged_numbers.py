@@ -62,3 +62,59 @@ def test_rows_without_any_finite_score_are_nan_and_alone(B, Hq, hd):
     Kb[0, :, 0, 0] = -float("inf")
     O = host(c.attn(0, Q, Kb, Vb))
     assert np.isnan(O[0, :, :Hq]).all() and np.isfinite(O[0, :, Hq:]).all() and np.isfinite(O[1]).all()
+
+
+def _one_hot(c, K, V, Q, Kb, Vb, O, lens):
+    """Scores so far apart that every weight but the largest keys' is 0: the mean of their values, rounded once to bf16,
+    with the weights' fp16 rounding (2^-11) and fp32's in the sums."""
+    Kd, Vd = ko.kv4_values(K, 0), ko.kv4_values(V, 0)
+    q, kb, vb, O = (host(x).astype(np.float64) for x in (Q, Kb, Vb, O))
+    for n, l in enumerate(lens):
+        ref, Ac, Ab, _ = ko.paged_attn(q[n], Kd[n, :l], Vd[n, :l], kb[n], vb[n])
+        tol = 2.0 ** -8 * np.abs(ref) + (1.01 * 2.0 ** -11 + 2.0 ** -20) * (Ac + Ab) + 2.0 ** -25
+        err = np.abs(O[n] - ref)
+        assert (err <= tol).all(), (n, float(np.nanmax(err / tol)), bool(np.isnan(err).any()))
+
+
+@pytest.mark.parametrize("B,Hq,hd", ROWS)
+@pytest.mark.parametrize("power", [20, 23, 26, 29, 33, 40, 90])
+def test_scores_of_any_size_give_the_largest_keys_values(B, Hq, hd, power):
+    # one dimension carries scores: the codes' steps of 0.5 make gaps of 2^(power - 6) at least
+    rng = np.random.default_rng(power + hd + B)
+    lens = [700, 1500, 0]
+    c = make_cache(rng, 3, lens, 16, 1, hd)
+    K, V = torch.zeros((3, 1500, 1, hd)), bf16(rng, (3, 1500, 1, hd))
+    K[:, :, 0, 0] = torch.from_numpy(rng.choice([0.5, 1.0, 1.5, 2.0, 3.0, -1.0, -6.0], (3, 1500)))
+    K[:, :, 0, 1] = 6.0   # every token's scale is 1
+    K[0, 123, 0, 0], K[1, 1400, 0, 0], K[1, 77, 0, 0] = 4.0, 6.0, 6.0
+    K = K.to(torch.bfloat16).cuda()
+    c.append(0, K, V, i32([0] * 3), i32(lens))
+    Q = torch.zeros((3, B, Hq, hd), device="cuda")
+    Q[..., 0] = 2.0 ** power * (1 + torch.from_numpy(rng.random((3, B, Hq)).astype(np.float32)).cuda())
+    Q[:, :, 1::2] *= -1   # the lowest keys are the largest scores, or all scores are far below zero
+    Q = Q.to(torch.bfloat16)
+    Kb, Vb = torch.zeros((3, B, 1, hd), dtype=torch.bfloat16, device="cuda"), bf16(rng, (3, B, 1, hd))
+    Kb[:, :, 0, 0] = 1.0
+    O = c.attn(0, Q, Kb, Vb)
+    _one_hot(c, host(K).astype(np.float64), host(V).astype(np.float64), Q, Kb, Vb, O, lens)
+
+
+@pytest.mark.parametrize("B,Hq,hd", ROWS)
+def test_scores_one_fp32_step_apart_stay_in_the_values_hull(B, Hq, hd):
+    # tokens after the first 64 score higher by a few steps of fp32 at 2^25 to 2^29: whatever these weigh, no output leaves the values
+    rng = np.random.default_rng(hd + B)
+    for step, last in ((0.5, 250), (1.0, 250), (2.0, 700), (6.0, 700)):   # whole triples, cut ones
+        lens = [64, 128, last]
+        c = make_cache(rng, 3, lens, 16, 1, hd)
+        K, V = torch.zeros((3, 700, 1, hd)), bf16(rng, (3, 700, 1, hd))
+        K[:, :, 0, 0] = 1.0
+        K[:, 64:, 0, 16] = step * 2.0 ** -9   # another group, of the smallest scale
+        c.append(0, K.to(torch.bfloat16).cuda(), V, i32([0] * 3), i32(lens))
+        Kb, Vb = torch.zeros((3, B, 1, hd), dtype=torch.bfloat16, device="cuda"), bf16(rng, (3, B, 1, hd))
+        Kb[:, :, 0, 0] = 1.0
+        top = max(float(V.abs().max()), float(Vb.abs().max()))
+        for power in range(27, 33):
+            Q = torch.zeros((3, B, Hq, hd), dtype=torch.bfloat16, device="cuda")
+            Q[..., 0], Q[..., 16] = 2.0 ** power * 1.5, 2.0 ** (power - 14) * 1.5
+            O = c.attn(0, Q, Kb, Vb).float()
+            assert bool(torch.isfinite(O).all()) and float(O.abs().max()) <= top * (1 + 2.0 ** -7), (step, power)
