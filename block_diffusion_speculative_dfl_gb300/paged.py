@@ -10,7 +10,6 @@ another, and so do two graphs captured from it.
 from __future__ import annotations
 
 import ctypes as C
-from contextlib import nullcontext
 
 import torch
 
@@ -67,14 +66,15 @@ class PagedCache:
             return torch._C._cuda_getCurrentRawStream(self._index)
         return _lib._stream(stream)
 
-    def _on(self, stream):
-        """Allocations under it belong to the stream that the call launches on."""
+    def _alloc(self, stream, f, *args, **kw):
+        """f(*args, **kw) with its memory from the stream that the call launches on."""
         if stream is None:
-            return nullcontext()
+            return f(*args, **kw)
         if isinstance(stream, int):   # (ExternalStream takes no null handle)
             stream = (torch.cuda.ExternalStream(stream, device=self._index) if stream else
                       torch.cuda.default_stream(self._index))
-        return torch.cuda.stream(stream)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
 
     def _i32(self, x, what):
         if x.dtype is not torch.int32 or not x.is_contiguous() or x.get_device() != self._index or x.numel() != self.N:
@@ -120,14 +120,12 @@ class PagedCache:
         k, _ = self._rows(Kb, "Kb", self.Hkv, B)
         v, _ = self._rows(Vb, "Vb", self.Hkv, B)
         if out is None:
-            with self._on(stream):
-                out = torch.empty_like(Q)
+            out = torch.empty_like(Q) if stream is None else self._alloc(stream, torch.empty_like, Q)
         o, _ = self._rows(out, "out", Hq, B)
         ws = self._attn_ws.get((B, Hq))
         if ws is None:
             need = _lib.workspace_size(_lib.DFL_OP_KV4_ATTN, N=self.N, B=B, Hq=Hq, Hkv=self.Hkv, hd=self.hd)
-            with self._on(stream):
-                ws = torch.empty(max(need, 16), dtype=torch.uint8, device=self.book.device)
+            ws = self._alloc(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=self.book.device)
             ws = self._attn_ws[(B, Hq)] = (ws, ws.data_ptr(), ws.numel())
         rc = self._lib.dfl_kv4_attn(self._pool, layer, self._pages, q, k, v, B, Hq, o, ws[1], ws[2], self._st(stream))
         if rc:
