@@ -259,8 +259,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
             for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) mx = max(mx, max(q[i] & 0x7FFFu, (q[i] >> 16) & 0x7FFFu));
             mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
             mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-            int e = (int)(mx >> 7);                       // biased exponent of the row's largest element
-            e = (e == 0 || e >= 254) ? 127 : e;           // zero, subnormal, huge or not finite: as it is
+            const int e = ka_query_exp(mx);
             const float down = __int_as_float((254 - e) << 23);
             #pragma unroll
             for (int i = 0; i < 2 * Cfg::KSTEPS; ++i) q[i] = pack_half(bf16lo(q[i]) * down, bf16hi(q[i]) * down);
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 #pragma unroll
                 for (int i = 0; i < HD / 32; ++i) qs[(nt * (HD / 32) + i) * 32 + lane] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
             }
-            const float up = __int_as_float(e << 23) * a.scale_log2 * a.k_pow2;
+            const float up = ka_mult(a, __int_as_float(e << 23));
             mult[nt][0] = __shfl_sync(0xFFFFFFFFu, up, 8 * t);       // lane of row 2t
             mult[nt][1] = __shfl_sync(0xFFFFFFFFu, up, 8 * t + 4);   // lane of row 2t + 1
         }

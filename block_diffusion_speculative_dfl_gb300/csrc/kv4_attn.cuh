@@ -88,6 +88,21 @@ __device__ __forceinline__ uint4 block_half8(const uint4 v, float inv) {
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// Biased exponent of the power of two that takes a query row's largest element
+// (magnitude mx, a bf16) to [1, 2), or to below 4 at the top of the range, whose
+// inverse is to stay normal.  Rows of zeros and subnormals: as they are.
+__device__ __forceinline__ int ka_query_exp(uint32_t mx) {
+    const int e = (int)(mx >> 7);
+    return e == 0 ? 127 : min(e, 253);
+}
+
+// Score of fp16 operands -> log2 units, for a row that was divided by `up`.
+// Neither 0, which would take a masked score's -inf to NaN, nor infinite, which
+// would a 0.
+__device__ __forceinline__ float ka_mult(const KaArgs& a, float up) {
+    return fminf(fmaxf(up * a.scale_log2 * a.k_pow2, 1.175494351e-38f), 3.402823466e38f);
+}
+
 // Block row and head of query row r of a group: element offset of its Q and O.
 __device__ __forceinline__ int64_t ka_row(const KaArgs& a, int n, int head, int r, int hd) {
     const int b = (int)(((uint64_t)(uint32_t)r * a.g_inv) >> 40);   // r / G: r G < 2^40

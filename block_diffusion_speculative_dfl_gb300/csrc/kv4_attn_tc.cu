@@ -428,8 +428,7 @@ __device__ __forceinline__ void kt_load_q(const KaArgs& a, int n, int head, int 
             uint32_t mx = max(m2 & 0xFFFFu, m2 >> 16), q[4];
             #pragma unroll
             for (int o = 1; o < WPR; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            int e = (int)(mx >> 7);
-            e = (e == 0 || e >= 254) ? 127 : e;   // zero, subnormal, huge or not finite: as it is
+            const int e = ka_query_exp(mx);
             const float down = __int_as_float((254 - e) << 23);
             #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -580,7 +579,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             __syncwarp();
             if (elect_one()) mbar_arrive(&bb.q_full);
             if (issuer && !issue_s(true)) { ok = false; break; }
-            const float mult = q_up[pipe][row] * a.scale_log2 * a.k_pow2;
+            const float mult = ka_mult(a, q_up[pipe][row]);
             if (x + u1 - u0 < x1) {   // the next triple's Q on its way to L2
                 const bool wrap = pos.hs + 1 == a.HS;
                 const int hs = wrap ? 0 : pos.hs + 1, nn = pos.n + wrap;

@@ -118,3 +118,26 @@ def test_scores_one_fp32_step_apart_stay_in_the_values_hull(B, Hq, hd):
             Q[..., 0], Q[..., 16] = 2.0 ** power * 1.5, 2.0 ** (power - 14) * 1.5
             O = c.attn(0, Q, Kb, Vb).float()
             assert bool(torch.isfinite(O).all()) and float(O.abs().max()) <= top * (1 + 2.0 ** -7), (step, power)
+
+
+@pytest.mark.parametrize("B,Hq,hd", ROWS)
+@pytest.mark.parametrize("q,k_exp", [(1e-36, -60), (1e-38, 0), (1e-38, -30), (2e38, 0), (-3.3e38, -60), (1e38, 60), (0.0, 60)])
+def test_queries_at_the_ends_of_bf16(B, Hq, hd, q, k_exp):
+    # scores that are all equal (keys of 0), or closer than 2^-20: the mean of the values
+    rng = np.random.default_rng(hd + B)
+    lens = [300, 37, 1200]
+    c = make_cache(rng, 3, lens, 16, 1, hd, k_exp=k_exp)
+    tiny = abs(q) < 1e-30
+    K, V = bf16(rng, (3, 1200, 1, hd)) * (2.0 ** k_exp if tiny and q else 0), bf16(rng, (3, 1200, 1, hd))
+    c.append(0, K, V, i32([0] * 3), i32(lens))
+    Q = bf16(rng, (3, B, Hq, hd)) * q if tiny else torch.zeros((3, B, Hq, hd), dtype=torch.bfloat16, device="cuda")
+    if not tiny:
+        Q[..., 3] = q
+    Kb, Vb = torch.zeros((3, B, 1, hd), dtype=torch.bfloat16, device="cuda"), bf16(rng, (3, B, 1, hd))
+    O = host(c.attn(0, Q, Kb, Vb)).astype(np.float64)
+    Vd, vb = ko.kv4_values(host(V).astype(np.float64), 0), host(Vb).astype(np.float64)
+    for n, l in enumerate(lens):
+        v = np.concatenate([Vd[n, :l], vb[n]])[:, 0]
+        ref, mean_abs = v.mean(0), np.abs(v).mean(0)
+        tol = 2.0 ** -8 * np.abs(ref) + (1.01 * 2.0 ** -11 + 2.0 ** -18) * mean_abs + 2.0 ** -25
+        assert (np.abs(O[n] - ref) <= tol).all(), n
