@@ -121,8 +121,10 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
                 need = (l + m + a.page - 1) / a.page - have;
                 if (m > 0 && l % a.page != 0) {
                     const int t = a.table[(int64_t)n * a.max_pages + have - 1];
-                    if (t < 0 || t >= a.num_pages) record_error(err, DFL_ERR_INVALID_ARG);
-                    else if (a.ref[t] > 1) { tail = t; ++need; }
+                    if (t < 0 || t >= a.num_pages) {   // new tokens would share a page that is none
+                        record_error(err, DFL_ERR_INVALID_ARG);
+                        need = -1;
+                    } else if (a.ref[t] > 1) { tail = t; ++need; }
                 }
             }
         }

@@ -673,8 +673,9 @@ dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages
  *   the free ones is not served: start[n] = -1 and nothing of it changes.
  *   n_new   in, device int32 [N]; start out, device int32 [N]
  *   ws      dfl_workspace_size(DFL_OP_PAGES_RESERVE) bytes
- *   n_new[n] below 0 or past max_pages * page in all, or a length out of range:
- *   not served, DFL_ERR_INVALID_ARG in the device error word.
+ *   n_new[n] below 0 or past max_pages * page in all, a length out of range, or
+ *   new tokens behind a partly filled last page whose table entry is outside
+ *   0..num_pages-1: not served, DFL_ERR_INVALID_ARG in the device error word.
  *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE.
  */
 dfl_status dfl_pages_reserve(const dfl_kv4_pool* pool, const dfl_pages* pages, const int32_t* n_new,
