@@ -571,6 +571,7 @@ inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq) {
     const int G = Hq / pool.Hkv;
     if (B > 64 || (int64_t)B * G > KV4_MAX_HEAD_ROWS || !rows_fit((int64_t)pg.N * B)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if ((int64_t)pg.max_pages * pool.page > KV4_ATTN_TOKENS) return DFL_ERR_UNSUPPORTED_SHAPE;
     const int R = B * G;
     const int64_t triples = (int64_t)pool.Hkv * ka_subs(R) * pg.N;
     if (triples >= (int64_t)1 << 31 || triples * ka_most_units(pool, pg, R) >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;

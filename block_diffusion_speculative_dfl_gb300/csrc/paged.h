@@ -35,6 +35,9 @@ dfl_status kv4_read_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
 
 // Attention over the cache and the block's own keys (kv4_attn.cu).
 constexpr int KV4_MAX_HEAD_ROWS = 65536;   // query rows of a K/V head: B * Hq / Hkv
+// Tokens of a sequence that attention takes: its positions are 32-bit and are
+// looked up as much as 32 units of 128 ahead.
+constexpr int64_t KV4_ATTN_TOKENS = ((int64_t)1 << 31) - 8192;
 // kv4_attn_check: the sizes that attention takes beyond kv4_check's.
 dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq);
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd);

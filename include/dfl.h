@@ -657,7 +657,8 @@ dfl_status dfl_kv4_read(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages
  *   0..num_pages-1 as page 0, and either records DFL_ERR_INVALID_ARG in the
  *   device error word.
  *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (B above 64, more than 65,536
- *   query rows to a K/V head, hd, page, sizes), MISALIGNED, WORKSPACE.
+ *   query rows to a K/V head, max_pages * page above 2^31 - 8192, hd, page,
+ *   sizes), MISALIGNED, WORKSPACE.
  */
 dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
                         const void* Q, const void* Kb, const void* Vb, int32_t B, int32_t Hq, void* O,
