@@ -211,7 +211,7 @@ using namespace dfl;
 
 // ------------------------------------------------------------------ misc
 
-extern "C" const char* dfl_version(void) { return "dfl 0.1.0 (sm_103a)"; }
+extern "C" const char* dfl_version(void) { return "dfl 0.2.0 (sm_103a)"; }
 
 extern "C" const char* dfl_status_string(dfl_status s) {
     switch (s) {
@@ -230,10 +230,14 @@ extern "C" const char* dfl_status_string(dfl_status s) {
 
 extern "C" size_t dfl_workspace_size(dfl_op op, const dfl_shape* s) {
     if (!s || (s->dtype != DFL_F32 && s->dtype != DFL_BF16)) return 0;
-    // every size is a count: a negative one makes the shape invalid
+    // every size is a count: a negative one makes the shape invalid.  `pages`, the last field, came with the paged
+    // cache: it is read for its ops alone, a caller built before it passes a struct that ends at `fc`.
     for (int32_t v : {s->N, s->C, s->B, s->d, s->Hq, s->Hkv, s->hd, s->D, s->L, s->V, s->K, s->G, s->row0, s->F, s->R,
-                      s->fc, s->pages})
+                      s->fc})
         if (v < 0) return 0;
+    const bool paged = op == DFL_OP_PAGES_RESERVE || op == DFL_OP_PAGES_REMAP || op == DFL_OP_PAGES_COMPACT ||
+                       op == DFL_OP_DRAFT_STEP_PAGED;
+    if (paged && s->pages < 0) return 0;
     switch (op) {
         case DFL_OP_DUAL_KV_PROJ: return ws_dual_kv_proj(s->N, s->B, s->d, s->dtype);
         case DFL_OP_BLOCK_ATTN: return ws_block_attn(s->N, s->C, s->B, s->Hq, s->Hkv, s->hd, s->dtype, false, s->d);

@@ -92,7 +92,7 @@ typedef struct dfl_shape {
                          fusion (dfl_fc_fuse) instead of per-layer mixtures */
     int32_t pages;        /* pages of the pool (DFL_OP_PAGES_RESERVE, DFL_OP_PAGES_COMPACT,
                              DFL_OP_DRAFT_STEP_PAGED) or entries of a sequence's page table
-                             (DFL_OP_PAGES_REMAP) */
+                             (DFL_OP_PAGES_REMAP); read for these ops only (since 0.2.0) */
 } dfl_shape;
 
 typedef enum dfl_op {

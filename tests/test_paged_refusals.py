@@ -19,3 +19,31 @@ def test_positions_of_attention_keep_to_32_bits(page, max_pages, rc, B, Hq):
     pages = dfl.Pages(FAKE, FAKE, FAKE, 1, max_pages)
     got = dfl.load().dfl_kv4_attn(C.byref(pool), 0, C.byref(pages), FAKE, FAKE, FAKE, B, Hq, FAKE, FAKE, 0, None)
     assert got == rc
+
+
+def test_shapes_of_before_the_paged_cache_end_before_its_field():
+    # the old struct lies at the end of a mapping; behind it an unreadable page of memory
+    import mmap
+    libc, old = C.CDLL(None, use_errno=True), dfl._lib.Shape.pages.offset
+    libc.mprotect.argtypes = [C.c_void_p, C.c_size_t, C.c_int]
+    m = mmap.mmap(-1, 2 * mmap.PAGESIZE)
+    base = C.addressof(C.c_char.from_buffer(m))
+    sizes = dict(N=2, C=64, B=16, d=256, Hq=4, Hkv=2, hd=64, D=2, L=3, V=1000, K=4, G=15, row0=1, dtype=1, F=512, R=8)
+    s = dfl._lib.Shape(**sizes)
+    C.memmove(base + mmap.PAGESIZE - old, C.addressof(s), old)
+    f = dfl.load().dfl_workspace_size
+    at = C.cast(base + mmap.PAGESIZE - old, C.POINTER(dfl._lib.Shape))
+    try:
+        assert libc.mprotect(base + mmap.PAGESIZE, mmap.PAGESIZE, 0) == 0
+        got = [f(op, at) for op in list(range(1, 14))]
+    finally:
+        libc.mprotect(base + mmap.PAGESIZE, mmap.PAGESIZE, mmap.PROT_READ | mmap.PROT_WRITE)
+    assert got == [dfl.workspace_size(op, **sizes) for op in range(1, 14)] and all(got)
+
+
+@pytest.mark.parametrize("op", range(1, 18))
+def test_a_negative_count_of_pages_matters_to_its_ops_only(op):
+    sizes = dict(N=2, C=64, B=16, d=256, Hq=4, Hkv=2, hd=64, D=2, L=3, V=1000, K=4, G=15, row0=1, dtype=1, F=512, R=8)
+    paged = op in (dfl.DFL_OP_PAGES_RESERVE, dfl.DFL_OP_PAGES_REMAP, dfl.DFL_OP_PAGES_COMPACT, dfl.DFL_OP_DRAFT_STEP_PAGED)
+    assert (dfl.workspace_size(op, pages=-1, **sizes) == 0) == paged
+    assert dfl.workspace_size(op, pages=9, **sizes) > 0
