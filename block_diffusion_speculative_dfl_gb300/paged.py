@@ -58,6 +58,7 @@ class PagedCache:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
         self._start, self._map, self._live, self._ws = (_lib.ptr(x) for x in (self.start, self.map, self.live, self.ws))
         self._attn_ws = {}   # (B, Hq) -> scratch, its address and size
+        self._scratch = {}   # bytes -> the same: the sizes are a few, whatever B and Hq
 
     def _st(self, stream):
         if torch.cuda.current_device() != self._index:
@@ -125,8 +126,11 @@ class PagedCache:
         ws = self._attn_ws.get((B, Hq))
         if ws is None:
             need = _lib.workspace_size(_lib.DFL_OP_KV4_ATTN, N=self.N, B=B, Hq=Hq, Hkv=self.Hkv, hd=self.hd)
-            ws = self._alloc(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=self.book.device)
-            ws = self._attn_ws[(B, Hq)] = (ws, ws.data_ptr(), ws.numel())
+            ws = self._scratch.get(need)
+            if ws is None:
+                ws = self._alloc(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=self.book.device)
+                ws = self._scratch[need] = (ws, ws.data_ptr(), ws.numel())
+            self._attn_ws[(B, Hq)] = ws
         rc = self._lib.dfl_kv4_attn(self._pool, layer, self._pages, q, k, v, B, Hq, o, ws[1], ws[2], self._st(stream))
         if rc:
             _lib._check("dfl_kv4_attn", rc)

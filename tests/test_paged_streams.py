@@ -72,3 +72,16 @@ def test_blocks_of_a_call_on_a_side_stream(by_handle):
     assert len(own) == 2 and found == [s.cuda_stream] * 2
     assert not bool(out.any())
     assert dfl.dfl_get_device_error() == 0
+
+
+def test_scratch_does_not_grow_with_the_number_of_shapes(cpu_cache):
+    c, log = cpu_cache
+    for B in range(1, 65):
+        for Hq in (2, 4, 8):
+            Q, K = torch.zeros((2, B, Hq, 64), dtype=torch.bfloat16), torch.zeros((2, B, 2, 64), dtype=torch.bfloat16)
+            c.attn(0, Q, K, K, out=torch.zeros_like(Q))
+    held = {ws.data_ptr(): ws.numel() for ws, _, _ in c._attn_ws.values()}
+    # a size for up to 8, 16, 64 and more query rows to a K/V head
+    assert len(held) == 4 and sum(held.values()) <= 64 << 20
+    for (B, Hq), (ws, at, size) in c._attn_ws.items():
+        assert size >= dfl.workspace_size(dfl.DFL_OP_KV4_ATTN, N=2, B=B, Hq=Hq, Hkv=2, hd=64) and at == ws.data_ptr()
