@@ -28,10 +28,17 @@ constexpr int PG_PLAN = 1024;        // threads of a planning block
 constexpr int PG_PASS = PG_PLAN * 32;  // pages per pass
 constexpr int PG_FEW = 4096;         // free pages that are handed out from shared memory
 // At most this many bytes to copy (every sequence's last page in every layer) are
-// copied by the planning block: 8 sequences' pages of 4.6 KB are reserved in 8.3
-// us instead of 9.3 (replayed), and the call takes the host 3.8 instead of 5.3.
-// More than an SM copies in a launch's 2 us goes to a kernel of its own.
-constexpr int64_t PG_HERE = 256 * 1024;
+// copied by the planning block, PG_WORDS 16-byte words a thread, all read before
+// the first is written; more go to a kernel of its own.  Here and there, us
+// replayed, and issued one after another (which the host bounds):
+//   nothing shared, any size          2.9  6.5 |  3.8  8.6
+//   all copied, 16 pages of 1,152 B   5.5  6.3 |  6.2  8.8
+//               28 pages of 2,304 B   6.4  7.0 |  5.6  8.2
+//               56 pages of 2,304 B   9.1  9.3 |  6.3  8.6
+//              224 pages of 1,152 B  16.3 15.8 |  9.5  9.5
+// Copied page by page here, the last two took 19.8 and 62.9: a round trip each.
+constexpr int PG_WORDS = 4;
+constexpr int64_t PG_HERE = PG_PLAN * PG_WORDS * 16;
 constexpr int PG_PIECE = 16384;      // bytes a block copies at a time
 constexpr int PG_THREADS = 256;
 
@@ -183,14 +190,22 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
         if (threadIdx.x == 0) *p.cow.count = cows;
         return;
     }
-    const int n16 = (int)(here.page_bytes / 16), all = cows * here.layers;
-    for (int k = 0; k < all; ++k) {
-        const int c = k / here.layers;
-        uint8_t* layer = here.data + (k - c * here.layers) * here.layer_stride;
-        const uint4* s = reinterpret_cast<const uint4*>(layer + p.cow.src[c] * here.page_bytes);
-        uint4* t = reinterpret_cast<uint4*>(layer + p.cow.dst[c] * here.page_bytes);
-        for (int i = threadIdx.x; i < n16; i += PG_PLAN) t[i] = s[i];
+    // one index over (copied page, layer, 16 bytes)
+    const uint32_t n16 = (uint32_t)(here.page_bytes / 16), all = (uint32_t)cows * here.layers * n16;   // <= PG_HERE / 16
+    uint4 v[PG_WORDS];
+    uint4* to[PG_WORDS];
+    #pragma unroll
+    for (int j = 0; j < PG_WORDS; ++j) {
+        const uint32_t i = threadIdx.x + j * PG_PLAN;
+        if (i >= all) continue;
+        const uint32_t pl = i / n16, c = pl / here.layers;
+        uint8_t* layer = here.data + (int64_t)(pl - c * here.layers) * here.layer_stride + (i - pl * n16) * 16;
+        v[j] = *reinterpret_cast<const uint4*>(layer + p.cow.src[c] * here.page_bytes);
+        to[j] = reinterpret_cast<uint4*>(layer + p.cow.dst[c] * here.page_bytes);
     }
+    #pragma unroll
+    for (int j = 0; j < PG_WORDS; ++j)
+        if (threadIdx.x + j * PG_PLAN < all) *to[j] = v[j];
 }
 
 // Copies whole pages src[k] -> dst[k] of every layer, in pieces.
