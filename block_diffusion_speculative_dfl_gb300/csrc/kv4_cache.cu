@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(KR_THREADS, 5) kv4_append_kernel(const Kv4Rows
         int tok;
         uint8_t* cell = row_cell<HD>(a, t, err, tok);
         if (!cell) return;
-        if (!DFL_IN_BOUNDS(err.word, cell - a.slab.data,
+        if (!DFL_IN_BOUNDS(err.word, cell - a.slab.data + Cell::BYTES - 1,
                            (int64_t)a.slab.num_pages * a.slab.Hkv * a.slab.cells * Cell::BYTES))
             return;
         uint2 c;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(KR_THREADS, 5) kv4_read_kernel(const Kv4Rows a
     kv4_each<HD>(a, err, [&](const Kv4Item& t) {
         int tok;
         const uint8_t* cell = row_cell<HD>(a, t, err, tok);
-        if (!cell) return;
+        if (!cell || !DFL_IN_BOUNDS(err.word, t.at, (int64_t)a.N * a.R * a.width)) return;
         const uint2 kc = *reinterpret_cast<const uint2*>(cell + Cell::k_code(tok, t.group));
         const uint2 vc = *reinterpret_cast<const uint2*>(cell + Cell::v_code(tok, t.group));
         uint4 lo, hi;

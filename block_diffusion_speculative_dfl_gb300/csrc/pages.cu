@@ -55,7 +55,9 @@ PgArgs pg_args(const dfl_kv4_pool& pool, const dfl_pages& pg) {
     return PgArgs{pg.table, pg.len, pg.ref, pg.N, pg.max_pages, pool.num_pages, pool.page};
 }
 
-// Where the second kernel finds the pages to copy.
+// Where the second kernel finds the pages to copy.  (The bounds-checked build
+// checks what goes through these lists and through the free list: the page
+// numbers, and the entries' own places.)
 struct PgMoves {
     int32_t* count;   // [1]
     int32_t* src;     // [<= capacity]
@@ -149,7 +151,8 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
         uint32_t f = ~u & low_bits(valid_count(a.num_pages, first));
         int sum;
         int k = found + block_exscan<PG_PLAN>(__popc(f), red, &sum);
-        for (; f && k < asked; f &= f - 1) free_[k++] = first + __ffs(f) - 1;
+        for (; f && k < asked; f &= f - 1, ++k)
+            if (DFL_IN_BOUNDS(err.word, k, asked <= PG_FEW ? PG_FEW : a.num_pages)) free_[k] = first + __ffs(f) - 1;
         found += sum;
     }
     __syncthreads();   // the lists are read by other threads (and the counts are written) from here on
@@ -164,8 +167,10 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
         const bool served = n < a.N && (need == 0 || (need > 0 && off + need <= found));
         if (served && tail >= 0) {
             const int c = atomicAdd(&cows, 1);   // the order of copies does not matter
-            p.cow.src[c] = tail;
-            p.cow.dst[c] = free_[off];
+            if (DFL_IN_BOUNDS(err.word, c, a.N)) {
+                p.cow.src[c] = tail;
+                p.cow.dst[c] = free_[off];
+            }
             atomicSub(&a.ref[tail], 1);
         }
         if (n < a.N) {
@@ -177,9 +182,11 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
         for (uint32_t who = __ballot_sync(0xFFFFFFFFu, served && need > 0); who; who &= who - 1) {
             const int j = __ffs(who) - 1;
             const int nj = __shfl_sync(0xFFFFFFFFu, need, j), oj = __shfl_sync(0xFFFFFFFFu, off, j);
-            int32_t* row = a.table + (int64_t)(n - lane + j) * a.max_pages + __shfl_sync(0xFFFFFFFFu, first, j);
+            const int fj = __shfl_sync(0xFFFFFFFFu, first, j);
+            int32_t* row = a.table + (int64_t)(n - lane + j) * a.max_pages + fj;
             for (int k = lane; k < nj; k += 32) {
                 const int f = free_[oj + k];
+                if (!DFL_IN_BOUNDS(err.word, fj + k, a.max_pages) || !DFL_IN_BOUNDS(err.word, f, a.num_pages)) continue;
                 row[k] = f;
                 a.ref[f] = 1;
             }
@@ -200,25 +207,30 @@ __global__ void __launch_bounds__(PG_PLAN) pages_reserve_plan_kernel(const PgArg
         if (i >= all) continue;
         const uint32_t pl = i / n16, c = pl / here.layers;
         uint8_t* layer = here.data + (int64_t)(pl - c * here.layers) * here.layer_stride + (i - pl * n16) * 16;
-        v[j] = *reinterpret_cast<const uint4*>(layer + p.cow.src[c] * here.page_bytes);
-        to[j] = reinterpret_cast<uint4*>(layer + p.cow.dst[c] * here.page_bytes);
+        const int src = p.cow.src[c], dst = p.cow.dst[c];
+        to[j] = nullptr;
+        if (!DFL_IN_BOUNDS(err.word, src, a.num_pages) || !DFL_IN_BOUNDS(err.word, dst, a.num_pages)) continue;
+        v[j] = *reinterpret_cast<const uint4*>(layer + src * here.page_bytes);
+        to[j] = reinterpret_cast<uint4*>(layer + dst * here.page_bytes);
     }
     #pragma unroll
     for (int j = 0; j < PG_WORDS; ++j)
-        if (threadIdx.x + j * PG_PLAN < all) *to[j] = v[j];
+        if (threadIdx.x + j * PG_PLAN < all && to[j]) *to[j] = v[j];
 }
 
 // Copies whole pages src[k] -> dst[k] of every layer, in pieces.
 __device__ __forceinline__ void copy_pages(const PgMoves& mv, uint8_t* data, int64_t layer_stride, int layers,
-                                           int64_t page_bytes) {
+                                           int64_t page_bytes, int num_pages, const DevErr& err) {
     const int64_t pieces = (page_bytes + PG_PIECE - 1) / PG_PIECE;
     const int64_t items = (int64_t)*mv.count * layers * pieces;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int64_t pl = it / pieces;
         const int64_t at = (it - pl * pieces) * PG_PIECE;
         const int k = (int)(pl / layers), layer = (int)(pl - (int64_t)k * layers);
-        const uint8_t* s = data + layer * layer_stride + mv.src[k] * page_bytes + at;
-        uint8_t* d = data + layer * layer_stride + mv.dst[k] * page_bytes + at;
+        const int src = mv.src[k], dst = mv.dst[k];
+        if (!DFL_IN_BOUNDS(err.word, src, num_pages) || !DFL_IN_BOUNDS(err.word, dst, num_pages)) continue;
+        const uint8_t* s = data + layer * layer_stride + src * page_bytes + at;
+        uint8_t* d = data + layer * layer_stride + dst * page_bytes + at;
         const int n16 = (int)(min((int64_t)PG_PIECE, page_bytes - at) / 16);
         uint4 v[PG_PIECE / 16 / PG_THREADS];
         #pragma unroll
@@ -235,9 +247,10 @@ __device__ __forceinline__ void copy_pages(const PgMoves& mv, uint8_t* data, int
 }
 
 __global__ void __launch_bounds__(PG_THREADS) pages_copy_kernel(const PgMoves mv, uint8_t* data, int64_t layer_stride,
-                                                               int layers, int64_t page_bytes) {
+                                                               int layers, int64_t page_bytes, int num_pages,
+                                                               const DevErr err) {
     grid_dep_begin();
-    copy_pages(mv, data, layer_stride, layers, page_bytes);
+    copy_pages(mv, data, layer_stride, layers, page_bytes, num_pages, err);
 }
 
 // ------------------------------------------------------------------ remap --
@@ -274,8 +287,8 @@ __device__ __forceinline__ RemapRow remap_row(const PgArgs& a, int n, const int3
     return RemapRow{p, ok ? (l + a.page - 1) / a.page : a.max_pages, l};
 }
 
-__device__ __forceinline__ void remap_entry(const PgArgs& a, int64_t at, int was, int now) {
-    if (was == now) return;
+__device__ __forceinline__ void remap_entry(const PgArgs& a, int64_t at, int was, int now, const DevErr& err) {
+    if (was == now || !DFL_IN_BOUNDS(err.word, at, (int64_t)a.N * a.max_pages)) return;
     a.table[at] = now;
     if (was >= 0 && was < a.num_pages) atomicSub(&a.ref[was], 1);
     if (now >= 0 && now < a.num_pages) atomicAdd(&a.ref[now], 1);
@@ -290,11 +303,12 @@ __global__ void __launch_bounds__(PG_PLAN) pages_remap_small_kernel(const PgArgs
     for (int n = warp; n < a.N; n += PG_PLAN / 32) {
         const RemapRow w = remap_row(a, n, a.len, parent, keep_len, lane == 0, err);
         for (int j = lane; j < a.max_pages; j += 32)
-            held[n * a.max_pages + j] = j < w.keep ? a.table[w.parent * a.max_pages + j] : -1;
+            if (DFL_IN_BOUNDS(err.word, n * a.max_pages + j, PG_HELD))
+                held[n * a.max_pages + j] = j < w.keep ? a.table[w.parent * a.max_pages + j] : -1;
         if (lane == 0) lens[n] = w.len;
     }
     __syncthreads();
-    for (int at = threadIdx.x; at < a.N * a.max_pages; at += PG_PLAN) remap_entry(a, at, a.table[at], held[at]);
+    for (int at = threadIdx.x; at < a.N * a.max_pages; at += PG_PLAN) remap_entry(a, at, a.table[at], held[at], err);
     for (int n = threadIdx.x; n < a.N; n += PG_PLAN) a.len[n] = lens[n];
 }
 
@@ -314,14 +328,14 @@ __global__ void __launch_bounds__(PG_THREADS) pages_remap_kernel(const PgArgs a,
     const RemapRow w = remap_row(a, n, len0, parent, keep_len, threadIdx.x == 0, err);
     for (int j = threadIdx.x; j < a.max_pages; j += PG_THREADS)
         remap_entry(a, (int64_t)n * a.max_pages + j, table0[(int64_t)n * a.max_pages + j],
-                    j < w.keep ? table0[(int64_t)w.parent * a.max_pages + j] : -1);
+                    j < w.keep ? table0[(int64_t)w.parent * a.max_pages + j] : -1, err);
     if (threadIdx.x == 0) a.len[n] = w.len;
 }
 
 // ---------------------------------------------------------------- compact --
 
 __global__ void __launch_bounds__(PG_PLAN) pages_compact_plan_kernel(const PgArgs a, int32_t* map, int32_t* live,
-                                                                    const PgMoves mv) {
+                                                                    const PgMoves mv, const DevErr err) {
     __shared__ int red[PG_PLAN / 32];
     grid_dep_begin();
     const uint32_t used0 = used_mask(a.ref, a.num_pages, 0);
@@ -340,8 +354,10 @@ __global__ void __launch_bounds__(PG_PLAN) pages_compact_plan_kernel(const PgArg
         int sh, sv;
         int kh = holes + block_exscan<PG_PLAN>(__popc(h), red, &sh);
         int kv = movers + block_exscan<PG_PLAN>(__popc(v), red, &sv);
-        for (uint32_t f = h; f; f &= f - 1) mv.dst[kh++] = first + __ffs(f) - 1;
-        for (uint32_t f = v; f; f &= f - 1) mv.src[kv++] = first + __ffs(f) - 1;
+        for (uint32_t f = h; f; f &= f - 1, ++kh)
+            if (DFL_IN_BOUNDS(err.word, kh, a.num_pages)) mv.dst[kh] = first + __ffs(f) - 1;
+        for (uint32_t f = v; f; f &= f - 1, ++kv)
+            if (DFL_IN_BOUNDS(err.word, kv, a.num_pages)) mv.src[kv] = first + __ffs(f) - 1;
         const int first0 = first - 32 * lane;   // of the warp's 1024 pages
         for (int i = 0; i < 32 && first0 + 32 * i < a.num_pages; ++i) {
             const int pg = first0 + 32 * i + lane;
@@ -355,6 +371,7 @@ __global__ void __launch_bounds__(PG_PLAN) pages_compact_plan_kernel(const PgArg
     #pragma unroll 4
     for (int k = threadIdx.x; k < movers; k += PG_PLAN) {
         const int s = mv.src[k], d = mv.dst[k];
+        if (!DFL_IN_BOUNDS(err.word, s, a.num_pages) || !DFL_IN_BOUNDS(err.word, d, a.num_pages)) continue;
         map[s] = d;
         a.ref[d] = a.ref[s];
         a.ref[s] = 0;
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_move_kernel(const Pg
         const int q = map[p];
         if (q != p) a.table[i] = q;
     }
-    copy_pages(mv, data, layer_stride, layers, page_bytes);
+    copy_pages(mv, data, layer_stride, layers, page_bytes, a.num_pages, err);
 }
 
 }  // namespace
@@ -412,7 +429,7 @@ dfl_status pages_reserve_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, const dfl
     const int64_t most = (int64_t)pg.N * pool.layers * ((bytes + PG_PIECE - 1) / PG_PIECE);
     const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)ctx->sm_count * 8);
     return launch_pdl(pages_copy_kernel, grid, PG_THREADS, 0, st, p.cow, static_cast<uint8_t*>(pool.data),
-                      pool.layer_stride, pool.layers, bytes);
+                      pool.layer_stride, pool.layers, bytes, pool.num_pages, dev_err(ctx));
 }
 
 dfl_status pages_remap_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, const dfl_pages& pg, const int32_t* parent,
@@ -448,7 +465,7 @@ dfl_status pages_compact_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, const dfl
     dfl_status rc;
     {
         ProfScope ps("pages_compact_plan", st);
-        if ((rc = launch_pdl(pages_compact_plan_kernel, 1, PG_PLAN, 0, st, a, map, live, mv)) != DFL_OK) return rc;
+        if ((rc = launch_pdl(pages_compact_plan_kernel, 1, PG_PLAN, 0, st, a, map, live, mv, dev_err(ctx))) != DFL_OK) return rc;
     }
     ProfScope ps("pages_compact_move", st);
     const int64_t most = std::max((int64_t)pool.num_pages * pool.layers * ((bytes + PG_PIECE - 1) / PG_PIECE),
