@@ -543,10 +543,12 @@ size_t sg_scratch_bytes(int N, int G, int V) {
 
 size_t sg_ws_bytes(int N, int G, int V) { return al256((size_t)N * (G + 1) * 4) + sg_scratch_bytes(N, G, V); }
 
+bool sg_fits(int V) { return (int64_t)V <= (int64_t)65535 * 8 * RG; }   // groups of a row: grid.y
+
 dfl_status sg_run(const void* vlog, bool bf, const int32_t* drafts, const int32_t* sel, int N, int K, int G, int V,
                   uint64_t seed, int32_t* accept_len, int32_t* next_token, const float* lse_v, bool lse_all,
                   void* scratch, cudaStream_t st) {
-    if ((int64_t)V > (int64_t)65535 * 8 * RG) return DFL_ERR_UNSUPPORTED_SHAPE;   // groups of a row: grid.y
+    if (!sg_fits(V)) return DFL_ERR_UNSUPPORTED_SHAPE;
     ProfScope ps("sampled_greedy", st);
     SgArgs sa{RowMap{vlog, K, G + 1, sel, err_word()}, lse_v, lse_all ? 1 : 0, G, V, (uint32_t)(seed & 0xFFFFFFFFu),
               (uint32_t)(seed >> 32), nullptr, nullptr, (V + RG - 1) / RG};

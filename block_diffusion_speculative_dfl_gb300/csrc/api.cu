@@ -768,12 +768,26 @@ dfl_status rc_fc_shape(const dfl_step_args* a) {
     return DFL_OK;
 }
 
+// Rules of the calls a step makes past its first launches: a step that is
+// refused has launched nothing, and left a cache's lengths and pages as they were.
+dfl_status step_call_rules(const dfl_step_args* a) {
+    const bool bf = a->dtype == DFL_BF16;
+    if (a->sample && (a->sample->K < 1 || a->sample->K > 64 || !(a->sample->T > 0.f))) return DFL_ERR_INVALID_ARG;
+    if (a->vlog && a->B - 1 > 1024) return DFL_ERR_INVALID_ARG;
+    if (!rmsnorm_fits(a->d) || (!a->W_fc && !mix_fits(a->L, a->D, a->d, bf))) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (bf && a->F % 64 != 0) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (a->sample && !sample_fits((a->V + 255) / 256)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (a->vlog && a->accept_rule == 2 && !sg_fits(a->V)) return DFL_ERR_UNSUPPORTED_SHAPE;
+    return DFL_OK;
+}
+
 // Host-side checks of a step's arguments (no launch).
 // `paged`: the paged form (never together with `cache`).
 dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const void* ws,
                       const dfl_paged_ctx* paged = nullptr) {
     if (!a || !ws) return DFL_ERR_INVALID_ARG;
     const int dt = a->dtype;
+    dfl_status rc;
     if (dt != DFL_F32 && dt != DFL_BF16) return DFL_ERR_INVALID_ARG;
     if (a->N <= 0 || a->C <= 0 || a->B < 2 || a->d <= 0 || a->D < 1 || a->D > 8 || a->L < 1 || a->V < 0)
         return DFL_ERR_INVALID_ARG;
@@ -821,22 +835,21 @@ dfl_status step_check(const dfl_step_args* a, const dfl_ctx_cache* cache, const 
         if ((int64_t)a->N * a->C >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
         if (!aligned16(cache->K) || !aligned16(cache->V) || (cache->layer_stride * 2) % 16 != 0)
             return DFL_ERR_MISALIGNED;
-        return step_bf16_shape(a);
+        if ((rc = step_bf16_shape(a)) != DFL_OK) return rc;
     }
     if (paged) {
         if (dt != DFL_BF16) return DFL_ERR_UNSUPPORTED_SHAPE;
         if (!paged->n_new || !paged->start || paged->R < 1 || !paged->pages.ref) return DFL_ERR_INVALID_ARG;
-        dfl_status rc = kv4_check(paged->pool, 0, &paged->pages);
-        if (rc != DFL_OK) return rc;
+        if ((rc = kv4_check(paged->pool, 0, &paged->pages)) != DFL_OK) return rc;
         const dfl_kv4_pool& p = *paged->pool;
         if (p.layers < a->D || p.Hkv != a->Hkv || p.hd != a->hd || paged->pages.N != a->N) return DFL_ERR_INVALID_ARG;
         if ((int64_t)paged->pages.max_pages * p.page > a->C) return DFL_ERR_INVALID_ARG;
         if (!aligned4(paged->n_new) || !aligned4(paged->start)) return DFL_ERR_MISALIGNED;
         if (!pages_fit(paged->pages)) return DFL_ERR_UNSUPPORTED_SHAPE;
         if ((rc = kv4_attn_check(p, paged->pages, a->B, a->Hq)) != DFL_OK) return rc;
-        return step_bf16_shape(a);
+        if ((rc = step_bf16_shape(a)) != DFL_OK) return rc;
     }
-    return DFL_OK;
+    return step_call_rules(a);
 }
 
 dfl_shape step_shape(const dfl_step_args* a, const dfl_ctx_cache* cache, const dfl_paged_ctx* paged = nullptr) {

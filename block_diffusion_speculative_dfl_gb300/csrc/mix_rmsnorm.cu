@@ -435,6 +435,15 @@ __global__ void mix_rmsnorm_f32_kernel(const float* H, int64_t layer_stride, int
 
 using namespace dfl;
 
+namespace dfl {
+
+bool mix_fits(int L, int D, int d, bool bf16) {
+    if (!bf16) return (size_t)(D * L + D * 32 + (size_t)D * d) * sizeof(float) <= 200 * 1024;
+    return d % 16 == 0 && d <= 16 * MIX_TEAM_WARPS * MIX_MAXG && mix_smem_plan(L, D, d, 1).total <= 227 * 1024;
+}
+
+}  // namespace dfl
+
 extern "C" dfl_status dfl_layer_mix_rmsnorm(const void* H, int64_t layer_stride, int32_t L, int64_t rows,
                                             int32_t d, dfl_dtype dt, int32_t D, const float* mix_logits,
                                             const float* gain, float eps, void* Xc, int64_t xc_layer_stride,
@@ -452,11 +461,10 @@ extern "C" dfl_status dfl_layer_mix_rmsnorm(const void* H, int64_t layer_stride,
     if (!ctx) return DFL_ERR_NO_DEVICE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dt == DFL_BF16) {
-        if (d % 16 != 0 || d > 16 * MIX_TEAM_WARPS * MIX_MAXG) return DFL_ERR_UNSUPPORTED_SHAPE;
+        if (!mix_fits(L, D, d, true)) return DFL_ERR_UNSUPPORTED_SHAPE;
         int nstage = MIX_MAXSTAGE;   // as many rows in flight as shared memory holds
         while (nstage > 1 && mix_smem_plan(L, D, d, nstage).total > 227 * 1024) --nstage;
         const int smem = mix_smem_plan(L, D, d, nstage).total;
-        if (smem > 227 * 1024) return DFL_ERR_UNSUPPORTED_SHAPE;
         const int gpw = (d / 16 + MIX_TEAM_WARPS - 1) / MIX_TEAM_WARPS;
         const int gi = gpw <= 4 ? 0 : gpw <= 8 ? 1 : gpw <= 12 ? 2 : gpw <= 16 ? 3 : 4;
         using KernFn = void (*)(const MixArgs, const int, const DevErr);
@@ -479,7 +487,7 @@ extern "C" dfl_status dfl_layer_mix_rmsnorm(const void* H, int64_t layer_stride,
         return last_launch();
     }
     const size_t smem = (size_t)(D * L + D * 32 + (size_t)D * d) * sizeof(float);
-    if (smem > 200 * 1024) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (!mix_fits(L, D, d, false)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(mix_rmsnorm_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
             cudaSuccess)

@@ -90,9 +90,11 @@ __global__ void __launch_bounds__(RN_THREADS) rmsnorm_rows_kernel(const float* i
     }
 }
 
+bool rmsnorm_fits(int d) { return d <= RN_THREADS * 4 * RN_MAXV && d % 4 == 0; }
+
 dfl_status rmsnorm_rows(const float* in, int d, int64_t M, int per, int stride, int off, const float* gain,
                         float eps, void* out, bool bf16, cudaStream_t st, float* copy) {
-    if (d > RN_THREADS * 4 * RN_MAXV || d % 4 != 0) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (!rmsnorm_fits(d)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (M > 0x7FFFFFFF) return DFL_ERR_UNSUPPORTED_SHAPE;
     ProfScope ps("rmsnorm_rows", st);
     if (bf16)
@@ -309,11 +311,16 @@ __global__ void sample_kernel(const float* logits, int64_t ld, const float* pmax
     }
 }
 
+constexpr int SAMPLE_WARPS = 4;
+static size_t sample_smem(int tiles) { return (size_t)SAMPLE_WARPS * (tiles + 1) * sizeof(double); }
+
+bool sample_fits(int tiles) { return sample_smem(tiles) <= 200 * 1024; }
+
 dfl_status sample_rows(const float* logits, int64_t ld, const float* pmax, const double* psum, int64_t M, int per,
                        int tiles, int bn, int V, int K, float T, uint64_t seed, int32_t* samples, cudaStream_t st) {
-    const int warps = 4;
-    const size_t smem = (size_t)warps * (tiles + 1) * sizeof(double);
-    if (smem > 200 * 1024) return DFL_ERR_UNSUPPORTED_SHAPE;
+    const int warps = SAMPLE_WARPS;
+    const size_t smem = sample_smem(tiles);
+    if (!sample_fits(tiles)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if (smem > 48 * 1024 &&
         cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return DFL_ERR_CUDA;

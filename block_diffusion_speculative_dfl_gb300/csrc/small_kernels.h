@@ -27,6 +27,14 @@ dfl_status greedy_accept(const int32_t* draft, const int32_t* target, int N, int
                          int32_t* bonus, cudaStream_t st);
 dfl_status argmax_combine(const float* pmax, const int* pidx, int64_t M, int tiles, int32_t* out,
                           cudaStream_t st);
+// Whether a row's tiles of 256 logits fit the sampler's shared memory, a row of
+// d the RMSNorm's registers, L target layers of d the mix's shared memory, V the
+// sampled-greedy rule's grid: the calls' own checks, and a step's before its
+// first launch.
+bool sample_fits(int tiles);
+bool rmsnorm_fits(int d);
+bool mix_fits(int L, int D, int d, bool bf16);
+bool sg_fits(int V);
 dfl_status sample_rows(const float* logits, int64_t ld, const float* pmax, const double* psum, int64_t M, int per,
                        int tiles, int bn, int V, int K, float T, uint64_t seed, int32_t* samples, cudaStream_t st);
 dfl_status tile_partials(const float* logits, int64_t ld, int64_t M, int V, int bn, int tiles, float inv_T,

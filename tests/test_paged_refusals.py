@@ -47,3 +47,38 @@ def test_a_negative_count_of_pages_matters_to_its_ops_only(op):
     paged = op in (dfl.DFL_OP_PAGES_RESERVE, dfl.DFL_OP_PAGES_REMAP, dfl.DFL_OP_PAGES_COMPACT, dfl.DFL_OP_DRAFT_STEP_PAGED)
     assert (dfl.workspace_size(op, pages=-1, **sizes) == 0) == paged
     assert dfl.workspace_size(op, pages=9, **sizes) > 0
+
+
+def _paged_step(F=0, sample=None, vlog=False, accept_rule=0, d=256, L=3, V=1000):
+    lib = dfl._lib
+    layers = (lib.LayerWeights * 2)()
+    for w in layers:
+        for n, _ in lib.LayerWeights._fields_:
+            setattr(w, n, FAKE)
+    a = lib.StepArgs()
+    a.N, a.C, a.B, a.d, a.Hq, a.Hkv, a.hd, a.D, a.L, a.V, a.dtype, a.F = 2, 64, 16, d, 4, 2, 64, 2, L, V, 1, F
+    a.eps, a.h_layer_stride, a.accept_rule = 1e-6, 2 * 64 * d, accept_rule
+    for n in ("H", "mix_logits", "mix_gain", "blk_gain", "final_gain", "W_lm", "Xb0", "Xb", "draft", "ffn_gain", "samples",
+              "scores", "selected", "accept_len", "bonus"):
+        setattr(a, n, FAKE)
+    a.layers = layers
+    sp = dfl._lib.SampleParams(*sample) if sample else None
+    if sp is not None:
+        a.sample = C.pointer(sp)
+    if vlog:
+        a.vlog = FAKE
+    pool = dfl.Kv4Pool(FAKE, 8 * dfl.dfl_kv4_page_bytes(32, 2, 64), 2, 8, 32, 2, 64, 0, 0)
+    ctx = dfl.PagedCtx(pool=C.pointer(pool), pages=dfl.Pages(FAKE, FAKE, FAKE, 2, 2), R=8, n_new=FAKE, start=FAKE)
+    return dfl.load().dfl_draft_step_paged(C.byref(a), C.byref(ctx), FAKE, 0, None)
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(), WORKSPACE), (dict(F=128), WORKSPACE), (dict(F=72), SHAPE),                      # the feed-forward's K blocks
+    (dict(d=5120), WORKSPACE), (dict(d=5152), SHAPE), (dict(d=8192), SHAPE),                 # the mix's and the norm's rows
+    (dict(sample=(4, 1.0, 1)), WORKSPACE), (dict(sample=(0, 1.0, 1)), 1), (dict(sample=(65, 1.0, 1)), 1),
+    (dict(sample=(4, 0.0, 1)), 1), (dict(sample=(4, float("nan"), 1)), 1), (dict(sample=(4, -1.0, 1)), 1),
+    (dict(sample=(4, 1.0, 1), V=6398 * 256), WORKSPACE), (dict(sample=(4, 1.0, 1), V=6400 * 256), SHAPE),
+    (dict(sample=(4, 1.0, 1), vlog=True, accept_rule=2), WORKSPACE)])
+def test_a_paged_step_that_is_refused_has_launched_nothing(kw, rc):
+    # a workspace of 0 bytes is looked at last, before the reservation of pages, the first launch
+    assert _paged_step(**kw) == rc
