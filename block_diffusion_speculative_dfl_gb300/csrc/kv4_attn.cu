@@ -29,9 +29,9 @@
 // 9/8 hd that arrive, and that traffic alone takes longer than the reads from
 // HBM (18 B per token and dimension pair through 128 B per clock and SM).
 // Single tokens of 48 sequences of 65 to 16,000 (8 heads of 128, 4 query heads
-// each): 96 us, 4.6 TB/s, 68 % of a copy's rate.  A cell of 16 tokens is about
+// each): 93.4 us, 4.8 TB/s, 70 % of a copy's rate.  A cell of 16 tokens is about
 // 370 warp instructions, 192 of them the conversions, scales and products; the
-// schedulers issue in 64 % of the clocks, waiting for dependent results and for
+// schedulers issue in 66 % of the clocks, waiting for dependent results and for
 // the conversion pipe.  More warps do not fit (five groups spill: 130 us).
 //
 // Numbers.  Expanded codes are exact in fp16.  Q is brought to fp16 after a
@@ -541,8 +541,11 @@ constexpr int KA_SMS = 152;   // SMs of a GB300
 // Row tiles of 8 query rows when a group has at most 8, of 16 up to 16: a wider
 // tile expands each key for more rows at once.  More rows go to the
 // tensor-memory kernel: 32 sequences of 2,048 tokens with 16 rows to a head take
-// 37 us here and 52 there, with 32 rows 64 and 52.
-// See KaLine.  The weight: a triple costs some 4.5 us beside 1.1 us per unit
+// 35.5 us here and 52 there, with 32 rows, as two tiles of 16, 64 and 52; there
+// 17 to 64 rows cost the same (17 53, 24 51, 64 52 us).
+// See KaLine.  The seam, 0, 8 and 16 (one token, 32/8 heads of 128): 64 sequences
+// of 300 18.5, 16.4 and 16.4 us, 70 of 2,000 47.1, 45.1 and 45.1, 4 of 300 10.3,
+// 10.4 and 12.3.  The weight: a triple costs some 4.5 us beside 1.1 us per unit
 // (the batch above 107, 102 and 103 us with weights 2, 4 and 6).
 constexpr int KA_SEAM = 8;
 constexpr int KA_WEIGHT = 4;

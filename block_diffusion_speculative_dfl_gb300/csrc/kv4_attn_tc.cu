@@ -2,9 +2,9 @@
 // on the 5th-generation tensor cores.  The same sum and the same line of work
 // units as kv4_attn.cu, with up to 128 rows to a triple, where products and
 // exponentials, not bytes, are most of the work.  A block of 16 at 4 query heads
-// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 52 us, 310 TFLOP/s
-// of products and 1.6 TB/s of cache; 64 rows of a head of 64 over 33,333 to
-// 100,001 tokens: 75 us.
+// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 51 us, 338 TFLOP/s
+// of products and 1.7 TB/s of cache; 64 rows of a head of 64 over 33,333 to
+// 100,001 tokens: 71.7 us; 128 rows: 74 and 106 us.
 //
 // One CTA per SM, two pipelines of eight warps, each with a range of the line of
 // its own, so that one pipeline's products run under the other's exponentials:
@@ -800,8 +800,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     }
 }
 
-// See KaLine.  The block of 16 above took 57 us as whole triples and 60 cut,
-// with twice the query heads 79 and 88.  Weights of 1 and 3 give the same times.
+// See KaLine.  The seam, 0, 4, 8 and 16: the block of 16 above 59.8 us with 0 and
+// 49.2 with the others, 32 sequences of 900 52.9 and 32.8, 16 of 900 29.4, 29.5,
+// 26.7 and 26.7.  Weights of 1 and 3 give the same times.
 constexpr int KT_SEAM = 8;
 constexpr int KT_WEIGHT = 1;
 constexpr int KT_SMS = 152;   // SMs of a GB300

@@ -5,7 +5,10 @@ lengths and reference counts of N sequences, and the scratch of its calls.
 Calls run on the current stream (or the one given) and read nothing back, so
 they can be captured into CUDA graphs.  The scratch is shared by the calls of
 one cache: calls on one cache belong on one stream, or ordered after one
-another, and so do two graphs captured from it.
+another, and so do two graphs captured from it.  The buffers are made and
+filled on the stream that is current at construction: calls on another stream
+belong after that, and the cache, like any tensor a call is given, is kept until
+the calls have run.
 """
 from __future__ import annotations
 
@@ -114,7 +117,8 @@ class PagedCache:
         """Block attention over each sequence's cached tokens and the block's own rows.
 
         Q bf16 [N, B, Hq, hd], Kb, Vb bf16 [N, B, Hkv, hd]; returns O bf16 [N, B, Hq, hd], allocated on the stream of
-        the call unless ``out`` is given.
+        the call unless ``out`` is given.  Own rows count as at most 65,504 units of 2^k_exp and 2^v_exp, and keep
+        bf16's 8 bits from 2^-14 of a unit up.
         """
         q, B = self._rows(Q, "Q")
         Hq = Q.shape[2]

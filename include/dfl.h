@@ -649,7 +649,9 @@ dfl_status dfl_kv4_read(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages
  *   Kb, Vb  in, bf16 [N*B][Hkv][hd]
  *   O       out, bf16 [N*B][Hq][hd]
  *   ws      dfl_workspace_size(DFL_OP_KV4_ATTN) bytes
- *   fp32 sums, softmax weights rounded to 11 bits.  The block's own rows are
+ *   fp32 sums, softmax weights rounded to 11 bits.  A query's elements are taken
+ *   to fp16 after a power of two brings its largest to [1, 2): those below 2^-14
+ *   of the largest lose bits.  The block's own rows are
  *   taken to fp16 in units of 2^k_exp and 2^v_exp: bf16's 8 bits survive from
  *   2^-14 of the unit up, finite values past 65504 units count as that.  The
  *   same inputs give the same bits.  A length outside
