@@ -145,7 +145,8 @@ def _logits(case, seed):
     step = max(1, (1 << 27) // V)
     for r in range(0, rows, step):
         z = torch.randn((min(step, rows - r), V), generator=g, device="cuda") * 2.5
-        peak = torch.randint(0, V, (z.shape[0], 6), generator=g, device="cuda")
+        # (six different places of a row: a scatter to one place twice would not depend on the seed alone)
+        peak = (torch.randint(0, V, (z.shape[0], 1), generator=g, device="cuda") + torch.arange(6, device="cuda") * (V // 6)) % V
         z.scatter_(1, peak, 8 + 6 * torch.rand(peak.shape, generator=g, device="cuda"))
         if case["banned"]:       # tokens that a grammar or a vocabulary mask forbids
             ban = torch.rand(z.shape, generator=g, device="cuda") < case["banned"]
