@@ -18,8 +18,10 @@ from ._lib import (DflError, load, version, status_string, workspace_size, ptr, 
                    dfl_sampled_greedy_accept, DFL_OP_SAMPLED_GREEDY, dfl_philox4x32_10,
                    Kv4Pool, Pages, PagedCtx, dfl_kv4_page_bytes, dfl_kv4_append, dfl_kv4_read, dfl_kv4_attn,
                    DFL_OP_KV4_ATTN, dfl_pages_reserve, DFL_OP_PAGES_RESERVE, dfl_pages_remap, DFL_OP_PAGES_REMAP,
-                   dfl_pages_compact, DFL_OP_PAGES_COMPACT, dfl_draft_step_paged, DFL_OP_DRAFT_STEP_PAGED)
+                   dfl_pages_compact, DFL_OP_PAGES_COMPACT, dfl_draft_step_paged, DFL_OP_DRAFT_STEP_PAGED,
+                   dfl_kv4_append_rows, dfl_kv4_attn_masked, dfl_token_logprobs, dfl_draft_tree, dfl_tree_accept)
 from .paged import PagedCache
+from .tree import DraftTree, TokenLogprobs, token_logprobs
 from .step import DraftShape, DraftModel, CachedDraftModel, PagedDraftModel
 
 __all__ = [n for n in dir() if not n.startswith("_")]

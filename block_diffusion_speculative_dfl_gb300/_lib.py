@@ -28,7 +28,8 @@ EXPORTED = ("dfl_version", "dfl_status_string", "dfl_workspace_size", "dfl_rope_
             "dfl_self_select_noalloc", "dfl_tv_acceptance", "dfl_spec_accept", "dfl_block_ffn",
             "dfl_draft_step_cached", "dfl_draft_step_host", "dfl_fc_fuse", "dfl_sampled_greedy_accept",
             "dfl_philox4x32_10", "dfl_kv4_page_bytes", "dfl_kv4_append", "dfl_kv4_read", "dfl_kv4_attn",
-            "dfl_pages_reserve", "dfl_pages_remap", "dfl_pages_compact", "dfl_draft_step_paged")
+            "dfl_pages_reserve", "dfl_pages_remap", "dfl_pages_compact", "dfl_draft_step_paged",
+            "dfl_kv4_append_rows", "dfl_kv4_attn_masked", "dfl_token_logprobs", "dfl_draft_tree", "dfl_tree_accept")
 
 
 class DflError(RuntimeError):
@@ -122,6 +123,12 @@ _SIGS = {
     "dfl_pages_remap": ([C.POINTER(Kv4Pool), C.POINTER(Pages), _P, _P, _P, _SZ, _P], _I32),
     "dfl_pages_compact": ([C.POINTER(Kv4Pool), C.POINTER(Pages), _P, _P, _P, _SZ, _P], _I32),
     "dfl_draft_step_paged": ([C.POINTER(StepArgs), C.POINTER(PagedCtx), _P, _SZ, _P], _I32),
+    "dfl_kv4_append_rows": ([C.POINTER(Kv4Pool), _I32, C.POINTER(Pages), _P, _P, _P, _I32, _P, _P, _P], _I32),
+    "dfl_kv4_attn_masked": ([C.POINTER(Kv4Pool), _I32, C.POINTER(Pages), _P, _P, _P, _I32, _I32, _P, _I32, _I32, _P, _P,
+                             _SZ, _P], _I32),
+    "dfl_token_logprobs": ([_P, _I32, _I64, _I32, _I64, _F, _P, _I32, _P, _P, _I32, _P, _P, _P], _I32),
+    "dfl_draft_tree": ([_P, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P], _I32),
+    "dfl_tree_accept": ([_P, _P, _P, _I32, _I32, _P, _P, _P, _P, _P], _I32),
 }
 
 _lib = None
@@ -359,3 +366,34 @@ def dfl_pages_compact(pool: Kv4Pool, pages: Pages, map_, live, ws, ws_bytes, str
 def dfl_draft_step_paged(args: StepArgs, ctx: PagedCtx, ws, ws_bytes, stream=None):
     _check("dfl_draft_step_paged",
            load().dfl_draft_step_paged(C.byref(args), C.byref(ctx), ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dfl_kv4_append_rows(pool: Kv4Pool, layer, pages: Pages, start, n_new, rows, R, K, V, stream=None):
+    _check("dfl_kv4_append_rows",
+           load().dfl_kv4_append_rows(C.byref(pool), layer, C.byref(pages), ptr(start), ptr(n_new), ptr(rows), R, ptr(K),
+                                      ptr(V), _stream(stream)))
+
+
+def dfl_kv4_attn_masked(pool: Kv4Pool, layer, pages: Pages, Q, Kb, Vb, B, Hq, mask, window, sinks, O, ws, ws_bytes,
+                        stream=None):
+    _check("dfl_kv4_attn_masked",
+           load().dfl_kv4_attn_masked(C.byref(pool), layer, C.byref(pages), ptr(Q), ptr(Kb), ptr(Vb), B, Hq, ptr(mask),
+                                      window, sinks, ptr(O), ptr(ws), ws_bytes, _stream(stream)))
+
+
+def dfl_token_logprobs(logits, dt, rows, V, row_stride, T, ids, M, logp, entropy, K, top_ids, top_logp, stream=None):
+    _check("dfl_token_logprobs",
+           load().dfl_token_logprobs(ptr(logits), dt, rows, V, row_stride, T, ptr(ids), M, ptr(logp), ptr(entropy), K,
+                                     ptr(top_ids), ptr(top_logp), _stream(stream)))
+
+
+def dfl_draft_tree(anchor, top_ids, top_logp, N, G, K, B, token, parent, depth, mask, count, stream=None):
+    _check("dfl_draft_tree",
+           load().dfl_draft_tree(ptr(anchor), ptr(top_ids), ptr(top_logp), N, G, K, B, ptr(token), ptr(parent), ptr(depth),
+                                 ptr(mask), ptr(count), _stream(stream)))
+
+
+def dfl_tree_accept(token, parent, target, N, B, path, accept_len, n_rows, bonus, stream=None):
+    _check("dfl_tree_accept",
+           load().dfl_tree_accept(ptr(token), ptr(parent), ptr(target), N, B, ptr(path), ptr(accept_len), ptr(n_rows),
+                                  ptr(bonus), _stream(stream)))

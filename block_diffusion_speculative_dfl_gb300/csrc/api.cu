@@ -967,13 +967,14 @@ dfl_status draft_step_impl(const dfl_step_args* a, const dfl_ctx_cache* cache, c
                                         w.Wq, w.Wkc, w.Wvc, w.Wkb, w.Wvb, a->Hq, a->Hkv, a->hd, a->rope, Q, Kc, Vc,
                                         Kb, Vb, sub, &plan, st, l == 0 ? a->Xb0 : nullptr)) != DFL_OK)
                 return rc;
-            if ((rc = kv4_append_run(dctx, *paged->pool, l, paged->pages, paged->start, paged->n_new, R, Kc, Vc, st)) !=
+            if ((rc = kv4_append_run(dctx, *paged->pool, l, paged->pages, paged->start, paged->n_new, nullptr, R, Kc, Vc, st)) !=
                 DFL_OK)
                 return rc;
             uint8_t* q = sub;
             void* O = carve(q, (size_t)N * B * a->Hq * a->hd * 2);
             void* aws = carve(q, kv4_attn_ws_bytes(N, B, a->Hq, a->Hkv, a->hd));
-            if ((rc = kv4_attn_run(dctx, *paged->pool, l, paged->pages, Q, Kb, Vb, B, a->Hq, O, aws, st)) != DFL_OK)
+            if ((rc = kv4_attn_run(dctx, *paged->pool, l, paged->pages, Q, Kb, Vb, B, a->Hq, nullptr, 0, 0, O, aws, st)) !=
+                DFL_OK)
                 return rc;
             if ((rc = o_proj_bf16(dctx, O, N * B, a->Hq * a->hd, w.Wo, d, a->Xb, reinterpret_cast<float*>(q),
                                   ws_oproj_split((int64_t)N * B, d), st)) != DFL_OK)

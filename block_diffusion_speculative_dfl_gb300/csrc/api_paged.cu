@@ -62,7 +62,20 @@ extern "C" dfl_status dfl_kv4_append(const dfl_kv4_pool* pool, int32_t layer, co
     if (rc != DFL_OK) return rc;
     DeviceCtx* ctx = current_ctx();
     if (!ctx) return DFL_ERR_NO_DEVICE;
-    return kv4_append_run(ctx, *pool, layer, *pages, start, n_new, R, K, V, static_cast<cudaStream_t>(stream));
+    return kv4_append_run(ctx, *pool, layer, *pages, start, n_new, nullptr, R, K, V, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dfl_status dfl_kv4_append_rows(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
+                                          const int32_t* start, const int32_t* n_new, const int32_t* rows, int32_t R,
+                                          const void* K, const void* V, dfl_stream stream) {
+    const dfl::ApiRange nvtx_range("dfl_kv4_append_rows");
+    if (!rows) return DFL_ERR_INVALID_ARG;
+    const dfl_status rc = rows_check(pool, layer, pages, start, n_new, R, K, V);
+    if (rc != DFL_OK) return rc;
+    if (!aligned4(rows)) return DFL_ERR_MISALIGNED;
+    DeviceCtx* ctx = current_ctx();
+    if (!ctx) return DFL_ERR_NO_DEVICE;
+    return kv4_append_run(ctx, *pool, layer, *pages, start, n_new, rows, R, K, V, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" dfl_status dfl_kv4_read(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
@@ -76,21 +89,41 @@ extern "C" dfl_status dfl_kv4_read(const dfl_kv4_pool* pool, int32_t layer, cons
     return kv4_read_run(ctx, *pool, layer, *pages, start, count, R, K, V, static_cast<cudaStream_t>(stream));
 }
 
-extern "C" dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages, const void* Q,
-                                   const void* Kb, const void* Vb, int32_t B, int32_t Hq, void* O, void* ws,
-                                   size_t ws_bytes, dfl_stream stream) {
-    const dfl::ApiRange nvtx_range("dfl_kv4_attn");
-    if (!pages || !Q || !Kb || !Vb || !O || !ws || B < 1 || Hq < 1) return DFL_ERR_INVALID_ARG;
+namespace {
+
+dfl_status attn_call(const dfl_kv4_pool* pool, int layer, const dfl_pages* pages, const void* Q, const void* Kb, const void* Vb,
+                     int B, int Hq, const uint64_t* mask, int window, int sinks, void* O, void* ws, size_t ws_bytes,
+                     dfl_stream stream) {
+    if (!pages || !Q || !Kb || !Vb || !O || !ws || B < 1 || Hq < 1 || window < 0 || sinks < 0) return DFL_ERR_INVALID_ARG;
     dfl_status rc = kv4_check(pool, layer, pages);
     if (rc != DFL_OK) return rc;
     if (Hq % pool->Hkv != 0) return DFL_ERR_INVALID_ARG;
     if ((rc = kv4_attn_check(*pool, *pages, B, Hq)) != DFL_OK) return rc;
     const void* ptrs[] = {Q, Kb, Vb, O, ws};
     for (const void* p : ptrs) if (!aligned16(p)) return DFL_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(mask) & 7u) return DFL_ERR_MISALIGNED;
     if (ws_bytes < kv4_attn_ws_bytes(pages->N, B, Hq, pool->Hkv, pool->hd)) return DFL_ERR_WORKSPACE;
     DeviceCtx* ctx = current_ctx();
     if (!ctx) return DFL_ERR_NO_DEVICE;
-    return kv4_attn_run(ctx, *pool, layer, *pages, Q, Kb, Vb, B, Hq, O, ws, static_cast<cudaStream_t>(stream));
+    return kv4_attn_run(ctx, *pool, layer, *pages, Q, Kb, Vb, B, Hq, mask, window, sinks, O, ws,
+                        static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages, const void* Q,
+                                   const void* Kb, const void* Vb, int32_t B, int32_t Hq, void* O, void* ws,
+                                   size_t ws_bytes, dfl_stream stream) {
+    const dfl::ApiRange nvtx_range("dfl_kv4_attn");
+    return attn_call(pool, layer, pages, Q, Kb, Vb, B, Hq, nullptr, 0, 0, O, ws, ws_bytes, stream);
+}
+
+extern "C" dfl_status dfl_kv4_attn_masked(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages, const void* Q,
+                                          const void* Kb, const void* Vb, int32_t B, int32_t Hq, const uint64_t* mask,
+                                          int32_t window, int32_t sinks, void* O, void* ws, size_t ws_bytes,
+                                          dfl_stream stream) {
+    const dfl::ApiRange nvtx_range("dfl_kv4_attn_masked");
+    return attn_call(pool, layer, pages, Q, Kb, Vb, B, Hq, mask, window, sinks, O, ws, ws_bytes, stream);
 }
 
 extern "C" dfl_status dfl_pages_reserve(const dfl_kv4_pool* pool, const dfl_pages* pages, const int32_t* n_new,

@@ -29,7 +29,7 @@ struct DeviceCtx {
     std::atomic<bool> gemm_attr_set[19] = {};   // gemm instantiations
     std::atomic<bool> mix_attr_set{false};
     std::atomic<bool> attn_attr_set[4] = {};    // tcgen05 attention: head dim 64 / 128, M = 64 / 128 products
-    std::atomic<bool> kv4_attr_set[8] = {};     // 4-bit cache attention: head dim 128 / 64, 8 / 16 (then 64 / 128) rows
+    std::atomic<bool> kv4_attr_set[16] = {};    // 4-bit cache attention: head dim 128 / 64, 8 / 16 (then 64 / 128) rows; masked
     // Host-input draft step: a copy stream and events, created on first use.
     // host_mu is held while a call issues its work: the events are shared, and
     // a wait must see the record its own call made.

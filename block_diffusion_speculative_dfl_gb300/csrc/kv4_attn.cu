@@ -46,6 +46,8 @@
 #include "kv4_attn.cuh"
 #include "paged.h"
 
+#include <type_traits>
+
 namespace dfl {
 
 namespace {
@@ -87,7 +89,7 @@ struct KaCfg {
 
 // The cells of one warp, copied ahead of their use.  Lane i holds the pool cell
 // of the warp's tokens in unit win + i.
-template <int HD, int ROWS>
+template <int HD, int ROWS, bool MASK>
 struct KaFeed {
     static constexpr int CELL = Kv4Cell<HD>::BYTES;
     const KaArgs& a;
@@ -95,13 +97,14 @@ struct KaFeed {
     uint8_t* ring;
     uint64_t* full;
     int w, lane;
-    KaPos pos;                 // the segment after the one being copied
+    KaPos<MASK> pos;           // the segment after the one being copied
     int x, x1;                 // units of the range up to it, and in all
     int u = 0, end = 0, win = 0, cells = 0, len = 0, n = 0, head = 0;
+    KaSkip gap{0, 0};
     uint32_t issued = 0;
 
     __device__ __forceinline__ KaFeed(const KaArgs& a_, const DevErr& err_, uint8_t* ring_, uint64_t* full_, int w_, int lane_,
-                                      const KaPos& pos_, int x0, int x1_)
+                                      const KaPos<MASK>& pos_, int x0, int x1_)
         : a(a_), err(err_), ring(ring_), full(full_), w(w_), lane(lane_), pos(pos_), x(x0), x1(x1_) {}
 
     // The next cell into a free slot, if any is left.
@@ -111,8 +114,10 @@ struct KaFeed {
             if (!pos.enter(x, x1)) return;
             u = pos.u;
             len = pos.len; n = pos.n; head = pos.head;
+            if constexpr (MASK) gap = pos.gap;
             const int u1 = min(pos.nu, u + (x1 - x));
-            end = max(u, min(u1, (len - w * KV4_CELL_TOKENS + KA_UNIT - 1) / KA_UNIT));   // units with a token of this warp's
+            const int held = (len - w * KV4_CELL_TOKENS + KA_UNIT - 1) / KA_UNIT;   // units with a token of this warp's
+            end = max(u, min(u1, MASK ? held - gap.skip : held));
             x += u1 - u;
             // this triple's queries and own rows on their way to L2
             const int r = pos.tile * ROWS + 8 * w + lane / 4, b = w * KV4_CELL_TOKENS + lane / 2;
@@ -127,7 +132,8 @@ struct KaFeed {
         }
         if (u == win + 32) {
             win = u;
-            const int k = (u + lane) * KA_UNIT + w * KV4_CELL_TOKENS;
+            const int at = MASK && u + lane >= gap.before ? u + lane + gap.skip : u + lane;
+            const int k = at * KA_UNIT + w * KV4_CELL_TOKENS;
             if (k < len) cells = ka_cell(a, n, head, k, err);
         }
         const int cell = __shfl_sync(0xFFFFFFFFu, cells, u - win);
@@ -190,7 +196,7 @@ __device__ __forceinline__ void ka_softmax(KaAcc<HD, NT>& acc, float (&s)[NT][4]
     }
 }
 
-template <int HD, int NT>
+template <int HD, int NT, bool MASK>
 __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(const KaArgs a, const DevErr err) {
     using Cfg = KaCfg<HD, NT>;
     using Cell = Kv4Cell<HD>;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
     ka_check_lengths<Cfg::THREADS>(a, err);
     // ranges go round the CTAs, so that a few of them spread over the SMs
     const int ranges = Cfg::GROUPS * gridDim.x, range = group * gridDim.x + blockIdx.x;
-    const KaLine line = ka_locate<Cfg::THREADS, Cfg::GROUPS>(a, ranges, line_sm, [&](int i, int per, int total) {
+    const KaLine line = ka_locate<MASK, Cfg::THREADS, Cfg::GROUPS>(a, ranges, line_sm, [&](int i, int per, int total) {
         const int64_t x = (int64_t)(i * gridDim.x + blockIdx.x) * per;
         return x < total ? (int)x : -1;
     });
@@ -224,12 +230,12 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
     if (line.whole ? range >= a.N * a.HS : x0l >= line.total) return;   // no block-wide barrier follows
     const int x0 = line.whole ? 0 : (int)x0l;
 
-    KaPos pos;   // the triple being computed
+    KaPos<MASK> pos;   // the triple being computed
     if (line.whole) pos.set_triple(a, range);
     else pos.set(a, line_sm.at[group], x0);
     const int x1 = line.whole ? pos.nu : min(line.total - x0, line.per) + x0;
 
-    KaFeed<HD, Cfg::ROWS> feed(a, err, ring, full, warp, lane, pos, x0, x1);
+    KaFeed<HD, Cfg::ROWS, MASK> feed(a, err, ring, full, warp, lane, pos, x0, x1);
     uint32_t taken = 0;
     bool dead = false;         // a wait ran out: no more copies, no more computation
     #pragma unroll 1
@@ -296,7 +302,8 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
         const int ctx_end = min(u1, pos.nu - 1);
         #pragma unroll 1
         for (int u = u0; u < ctx_end; ++u) {
-            const int left = pos.len - u * KA_UNIT - warp * KV4_CELL_TOKENS;   // tokens from this cell on
+            const int k0 = pos.token(a, u) + warp * KV4_CELL_TOKENS;
+            const int left = pos.len - k0;   // tokens from this cell on
             if (left <= 0 || dead) continue;
             const int sl = taken % KA_SLOTS;
             const bool ok = mbar_wait(&full[sl], (taken / KA_SLOTS) & 1, err);
@@ -364,6 +371,25 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     if (!v1) s[nt][2] = s[nt][3] = -INFINITY;
                 }
             }
+            // tokens that some rows do not see, through their window
+            const bool edge = MASK && ka_edge(a, pos.len, k0, KV4_CELL_TOKENS);
+            // first token behind the sinks that this lane's row r of tile nt sees
+            auto first = [&](int nt, int r) {
+                const int q = row0 + nt * 8 + 2 * t + r;
+                return q < a.R ? ka_first(a, pos.len, ka_depth(a, pos.n, ka_block_row(a, q))) : 0;
+            };
+            if constexpr (MASK)
+                if (edge) {
+                    const int k1 = k0 + Cell::token(g), k2 = k0 + Cell::token(g + 8);
+                    #pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        #pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int lo = first(nt, r);
+                            if (k1 >= a.sinks && k1 < lo) s[nt][r] = -INFINITY;
+                            if (k2 >= a.sinks && k2 < lo) s[nt][r + 2] = -INFINITY;
+                        }
+                }
             ka_softmax<HD, NT>(acc, s);
             uint32_t pb[NT][2];
             #pragma unroll
@@ -371,9 +397,20 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 pb[nt][0] = transpose8x8(pack_half(s[nt][0], s[nt][1]));
                 pb[nt][1] = transpose8x8(pack_half(s[nt][2], s[nt][3]));
             }
+            uint32_t nans = 0;   // of an edge's cell: tokens whose values of this lane's dims are NaN
             {   // O^T: tokens t, 4 + t (slots 2t, 2t + 1) and 8 + t, 12 + t
                 const int vg = HD == 128 ? g : g >> 1;
                 uint32_t sw = *reinterpret_cast<const uint32_t*>(cell + Cell::V_SCALES + vg * 16 + t * 4);
+                if constexpr (MASK)
+                    if (edge) {   // a weight of 0 times NaN would be NaN: taken out, and given to the rows that see them below
+                        const uint32_t bytes = __vcmpeq4(sw & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                        sw &= ~bytes;
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) nans |= (bytes >> 8 * i & 1u) << (4 * i + t);
+                        nans |= __shfl_xor_sync(0xFFFFFFFFu, nans, 1);
+                        nans |= __shfl_xor_sync(0xFFFFFFFFu, nans, 2);
+                        if (left < KV4_CELL_TOKENS) nans &= (1u << left) - 1;
+                    }
                 uint32_t sp[2] = {e4m3x2_to_half(sw & 0xFFFFu), e4m3x2_to_half(sw >> 16)};
                 if (left < KV4_CELL_TOKENS) {   // weight 0 times a stored NaN would be NaN
                     #pragma unroll
@@ -419,6 +456,23 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     }
                 }
             }
+            if constexpr (MASK)
+                if (nans) {
+                    #pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        #pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int lo = first(nt, r);
+                            bool sees = false;
+                            #pragma unroll 1
+                            for (int k = 0; k < KV4_CELL_TOKENS; ++k)
+                                sees |= (nans >> k & 1u) && (k0 + k < a.sinks || k0 + k >= lo);
+                            if (sees) {
+                                #pragma unroll
+                                for (int i = 0; i < Cfg::MT; ++i) acc.o[nt][i][r] = acc.o[nt][i][r + 2] = __int_as_float(0x7FFFFFFF);
+                            }
+                        }
+                }
             __syncwarp();   // the slot has been read by every lane
             feed.produce();
         }
@@ -443,10 +497,24 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     mma_f16(s[nt], f1, qw.z, qw.w);
                 }
             }
+            uint64_t sees[NT][2];   // own rows that this lane's rows see
+            if constexpr (MASK) {
+                #pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    #pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int q = row0 + nt * 8 + 2 * t + r;
+                        sees[nt][r] = q < a.R ? ka_own_sees(a, pos.n, ka_block_row(a, q), pos.len) >> (warp * KV4_CELL_TOKENS) : 0;
+                    }
+            }
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[nt][c] = (c < 2 ? b0 : b1) < a.B ? __fmul_rn(s[nt][c], mult[nt][c & 1]) : -INFINITY;
+                for (int c = 0; c < 4; ++c) {
+                    bool see = (c < 2 ? b0 : b1) < a.B;
+                    if constexpr (MASK) see = sees[nt][c & 1] >> Cell::token(c < 2 ? g : g + 8) & 1;
+                    s[nt][c] = see ? __fmul_rn(s[nt][c], mult[nt][c & 1]) : -INFINITY;
+                }
             ka_softmax<HD, NT>(acc, s);
             uint32_t pb[NT][2];
             #pragma unroll
@@ -454,14 +522,16 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 pb[nt][0] = transpose8x8(pack_half(s[nt][0], s[nt][1]));
                 pb[nt][1] = transpose8x8(pack_half(s[nt][2], s[nt][3]));
             }
+            bool bad = false;   // (MASK) infinities or NaN among the values
             #pragma unroll
             for (int w = 0; w < HD / 64; ++w) {   // 8 dims of the lane's eighth at a time
                 uint32_t v[4][4];
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int b = warp * KV4_CELL_TOKENS + 4 * i + t;
-                    const uint4 x4 = block_half8(b < a.B ? *reinterpret_cast<const uint4*>(
-                        a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0), a.v_inv);
+                    const uint4 raw = b < a.B ? *reinterpret_cast<const uint4*>(
+                        a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0);
+                    const uint4 x4 = MASK ? block_half8_finite(raw, a.v_inv, bad) : block_half8(raw, a.v_inv);
                     v[i][0] = x4.x; v[i][1] = x4.y; v[i][2] = x4.z; v[i][3] = x4.w;
                 }
                 #pragma unroll
@@ -472,6 +542,26 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     for (int nt = 0; nt < NT; ++nt) mma_f16(acc.o[nt][4 * w + i], af, pb[nt][0], pb[nt][1]);
                 }
             }
+            if constexpr (MASK)
+                if (__any_sync(0xFFFFFFFFu, bad)) {   // such values to the rows that see them
+                    #pragma unroll 1
+                    for (int k = 0; k < KV4_CELL_TOKENS && warp * KV4_CELL_TOKENS + k < a.B; ++k) {
+                        const __nv_bfloat16* src = a.Vb + ((int64_t)(pos.n * a.B + warp * KV4_CELL_TOKENS + k) * Hkv + head) * HD + g * (HD / 8);
+                        #pragma unroll
+                        for (int i = 0; i < Cfg::MT; ++i) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t*>(src + 2 * i);
+                            const float e = (w & 0x7F80u) == 0x7F80u ? bf16lo(w) : 0.f, f = (w >> 16 & 0x7F80u) == 0x7F80u ? bf16hi(w) : 0.f;
+                            #pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                #pragma unroll
+                                for (int r = 0; r < 2; ++r)
+                                    if (sees[nt][r] >> k & 1) {
+                                        acc.o[nt][i][r] += e;
+                                        acc.o[nt][i][r + 2] += f;
+                                    }
+                        }
+                    }
+                }
         }
         // ---- the warps' parts of this triple
         #pragma unroll
@@ -511,7 +601,9 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
                 }
                 if (whole) {
-                    const float inv = __fdividef(a.v_pow2, L);
+                    float inv = __fdividef(a.v_pow2, L);
+                    if constexpr (MASK)
+                        if (ka_blank(a, pos.n, ka_block_row(a, r), pos.len)) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
                     const int64_t at = ka_row(a, pos.n, head, r, HD) + c;
                     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
                         *reinterpret_cast<uint2*>(a.O + at) =
@@ -591,7 +683,8 @@ size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd) {
 }
 
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
-                        const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st) {
+                        const void* Kb, const void* Vb, int B, int Hq, const uint64_t* mask, int window, int sinks, void* O,
+                        void* ws, cudaStream_t st) {
     const int G = Hq / pool.Hkv, R = B * G, nt = ka_nt(R);
     const bool tc = R > KA_MAX_ROWS;
     const int rows = ka_rows(R);
@@ -615,7 +708,9 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.seam = tc ? kv4_attn_tc_seam() : KA_SEAM;
     static_assert(KA_UNIT == 64, "unit_log2");
     const int64_t units = ka_most_units(pool, pg, R) * pg.N * a.HS;   // < 2^31: kv4_attn_check
-    if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, st);
+    const bool masked = mask || window > 0;
+    a.mask = mask; a.window = window; a.sinks = sinks;
+    if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, masked, st);
     const size_t parts = 2 * (size_t)KA_SMS * ka_groups(pool.hd, nt) * rows;
     a.Opart = static_cast<float*>(ws);
     a.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + al256(parts * pool.hd * 4));
@@ -636,11 +731,16 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
         ProfScope ps("kv4_attn_join", st);
         return launch_pdl(join, dim3(grid * groups, rows / KJ_ROWS), pool.hd / 4 * KJ_ROWS, 0, st, a, err);
     };
-    if (pool.hd == 128)
-        return nt == 1 ? run(kv4_attn_kernel<128, 1>, kv4_attn_join_kernel<128, 8>, KaCfg<128, 1>::SMEM, 0)
-                       : run(kv4_attn_kernel<128, 2>, kv4_attn_join_kernel<128, 16>, KaCfg<128, 2>::SMEM, 1);
-    return nt == 1 ? run(kv4_attn_kernel<64, 1>, kv4_attn_join_kernel<64, 8>, KaCfg<64, 1>::SMEM, 2)
-                   : run(kv4_attn_kernel<64, 2>, kv4_attn_join_kernel<64, 16>, KaCfg<64, 2>::SMEM, 3);
+    auto pick = [&](auto flag) -> dfl_status {
+        constexpr bool MASK = decltype(flag)::value;
+        constexpr int S = MASK ? 8 : 0;
+        if (pool.hd == 128)
+            return nt == 1 ? run(kv4_attn_kernel<128, 1, MASK>, kv4_attn_join_kernel<128, 8, MASK>, KaCfg<128, 1>::SMEM, S)
+                           : run(kv4_attn_kernel<128, 2, MASK>, kv4_attn_join_kernel<128, 16, MASK>, KaCfg<128, 2>::SMEM, S + 1);
+        return nt == 1 ? run(kv4_attn_kernel<64, 1, MASK>, kv4_attn_join_kernel<64, 8, MASK>, KaCfg<64, 1>::SMEM, S + 2)
+                       : run(kv4_attn_kernel<64, 2, MASK>, kv4_attn_join_kernel<64, 16, MASK>, KaCfg<64, 2>::SMEM, S + 3);
+    };
+    return masked ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace dfl

@@ -34,6 +34,9 @@ struct KaArgs {
     KaCross* cross;           // [ranges]
     float scale_log2;         // log2(e) / sqrt(hd)
     float k_pow2, k_inv, v_pow2, v_inv;   // 2^k_exp, 2^-k_exp, 2^v_exp, 2^-v_exp
+    // the masked kernels' (MASK)
+    const uint64_t* mask;     // [N*B] own rows that a row sees, nullable: all
+    int window, sinks;        // window 0: none
 };
 
 // The tensor-memory kernel (kv4_attn_tc.cu): rows of its triples, scratch, launch
@@ -43,7 +46,7 @@ int kv4_attn_tc_unit_log2(int R, int hd);
 int kv4_attn_tc_seam();
 int kv4_attn_tc_weight();
 size_t kv4_attn_tc_ws_bytes(int R, int hd);
-dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, cudaStream_t st);
+dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, bool masked, cudaStream_t st);
 
 namespace {
 
@@ -88,6 +91,25 @@ __device__ __forceinline__ uint4 block_half8(const uint4 v, float inv) {
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// The same for values that some rows may not see: infinities and NaN become 0, as
+// a weight of 0 times one of them would be NaN; `bad` says that there were some.
+__device__ __forceinline__ uint4 block_half8_finite(const uint4 v, float inv, bool& bad) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(h[i]) : "f"(bf16hi(w[i]) * inv), "f"(bf16lo(w[i]) * inv));
+    const uint32_t m = max_u16x2(max_u16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), max_u16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    if (m >= 0x7F800000u || (m & 0xFFFFu) >= 0x7F80u) {
+        bad = true;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+            #pragma unroll
+            for (int s = 0; s < 32; s += 16)
+                if ((w[i] >> s & 0x7F80u) == 0x7F80u) h[i] &= ~(0xFFFFu << s);
+    }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
 // Biased exponent of the power of two that takes a query row's largest element
 // (magnitude mx, a bf16) to [1, 2), or to below 4 at the top of the range, whose
 // inverse is to stay normal.  Rows of zeros and subnormals: as they are.
@@ -103,9 +125,14 @@ __device__ __forceinline__ float ka_mult(const KaArgs& a, float up) {
     return fminf(fmaxf(up * a.scale_log2 * a.k_pow2, 1.175494351e-38f), 3.402823466e38f);
 }
 
+// Block row of query row r of a group.
+__device__ __forceinline__ int ka_block_row(const KaArgs& a, int r) {
+    return (int)(((uint64_t)(uint32_t)r * a.g_inv) >> 40);   // r / G: r G < 2^40
+}
+
 // Block row and head of query row r of a group: element offset of its Q and O.
 __device__ __forceinline__ int64_t ka_row(const KaArgs& a, int n, int head, int r, int hd) {
-    const int b = (int)(((uint64_t)(uint32_t)r * a.g_inv) >> 40);   // r / G: r G < 2^40
+    const int b = ka_block_row(a, r);
     return ((int64_t)(n * a.B + b) * a.Hq + head * a.G + (r - b * a.G)) * hd;
 }
 
@@ -131,8 +158,64 @@ __device__ __forceinline__ void ka_check_lengths(const KaArgs& a, const DevErr& 
         if (a.len[n] != ka_len(a, n)) record_error(err, DFL_ERR_INVALID_ARG);
 }
 
+// What a row sees (MASK): the own rows of its mask, and through a window of W the
+// keys at positions p with q - p < W or p < sinks, q its own position: the length
+// + its depth.
+//
+// Depth of block row b: rows of the tree above it; without a mask its number.
+__device__ __forceinline__ uint64_t ka_row_bits(const KaArgs& a, int n, int b) {
+    const uint64_t all = ~0ull >> (64 - a.B);
+    return a.mask ? a.mask[(int64_t)n * a.B + b] & all : all;
+}
+__device__ __forceinline__ int ka_depth(const KaArgs& a, int n, int b) {
+    return a.mask ? max(__popcll(ka_row_bits(a, n, b)) - 1, 0) : b;
+}
+// First token behind the sinks that a row of this depth sees.
+__device__ __forceinline__ int ka_first(const KaArgs& a, int len, int depth) { return a.window > 0 ? len + depth - a.window + 1 : 0; }
+// The own rows that block row b sees.
+__device__ __forceinline__ uint64_t ka_own_sees(const KaArgs& a, int n, int b, int len) {
+    uint64_t bits = ka_row_bits(a, n, b);
+    const int d = ka_depth(a, n, b);
+    if (a.window > 0 && d >= a.window) {   // rows above it fall out of the window
+        uint64_t left = bits;
+        #pragma unroll 1
+        while (left) {
+            const int j = __ffsll((long long)left) - 1, dj = ka_depth(a, n, j);
+            left &= left - 1;
+            if (d - dj >= a.window && len + dj >= a.sinks) bits &= ~(1ull << j);
+        }
+    }
+    return bits;
+}
+// Whether block row b sees nothing: its output is 0.
+__device__ __forceinline__ bool ka_blank(const KaArgs& a, int n, int b, int len) {
+    if (ka_row_bits(a, n, b) == 0) return true;
+    if (len > 0 && (a.sinks > 0 || ka_first(a, len, ka_depth(a, n, b)) < len)) return false;
+    return ka_own_sees(a, n, b, len) == 0;
+}
+// Whether some row may not see one of the tokens k .. k + count - 1 (no row is deeper than B - 1).
+__device__ __forceinline__ bool ka_edge(const KaArgs& a, int len, int k, int count) {
+    return a.window > 0 && k + count > a.sinks && k < len + a.B - a.window;
+}
+
+// Units that hold tokens some row sees: the first `before`, then from `before +
+// skip` on.  (Rows of depth 0 see the earliest tokens behind the sinks.)
+struct KaSkip {
+    int before, skip;
+};
+template <bool MASK>
+__device__ __forceinline__ KaSkip ka_skip(const KaArgs& a, int len) {
+    if (!MASK || a.window == 0) return KaSkip{0, 0};
+    const int lo = max(0, ka_first(a, len, 0)), unit = 1 << a.unit_log2;
+    const int before = (min(a.sinks, lo) + unit - 1) >> a.unit_log2;
+    return KaSkip{before, max(0, (lo >> a.unit_log2) - before)};
+}
+
 // Units of a sequence: its tokens, then the block's own keys.
-__device__ __forceinline__ int ka_units(const KaArgs& a, int len) { return ((len + (1 << a.unit_log2) - 1) >> a.unit_log2) + 1; }
+template <bool MASK>
+__device__ __forceinline__ int ka_units(const KaArgs& a, int len) {
+    return ((len + (1 << a.unit_log2) - 1) >> a.unit_log2) + 1 - ka_skip<MASK>(a, len).skip;
+}
 
 // The line of units and how it is cut: into ranges of `per` units, or, when
 // there are no more triples than ranges and none is much longer than the rest,
@@ -162,15 +245,15 @@ struct KaLineSmem {
 // The line cut into `ranges`; of the P positions at(i, per, total), those in
 // 0 .. total - 1 are located in sm.at[i].  All threads of the block call; one
 // read of the lengths when there are no more sequences than threads.
-template <int THREADS, int P, typename At>
+template <bool MASK, int THREADS, int P, typename At>
 __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineSmem<THREADS, P>& sm, At at) {
     const int chunk = (a.N + THREADS - 1) / THREADS;
     const int n0 = min(a.N, (int)threadIdx.x * chunk), n1 = min(a.N, n0 + chunk);
     const int len0 = n0 < n1 ? ka_len(a, n0) : 0, len1 = n0 + 1 < a.N ? ka_len(a, n0 + 1) : 0;
-    int sum = n0 < n1 ? ka_units(a, len0) + a.weight : 0, longest = sum;
+    int sum = n0 < n1 ? ka_units<MASK>(a, len0) + a.weight : 0, longest = sum;
     #pragma unroll 1
     for (int n = n0 + 1; n < n1; ++n) {
-        const int nu = ka_units(a, ka_len(a, n)) + a.weight;
+        const int nu = ka_units<MASK>(a, ka_len(a, n)) + a.weight;
         sum += nu;
         longest = max(longest, nu);
     }
@@ -191,7 +274,7 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
         int p = pre, len = len0, next = len1;
         #pragma unroll 1
         for (int n = n0; ; ++n) {
-            const int w = (ka_units(a, len) + a.weight) * a.HS;
+            const int w = (ka_units<MASK>(a, len) + a.weight) * a.HS;
             if (x < p + w) { sm.at[i] = KaFound{n, p, len, next}; break; }
             p += w;
             len = next;
@@ -204,14 +287,21 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
 
 // A position on the line as (sequence, head and row tile, unit); u < 0 in the
 // places ahead of a triple's units.  The next sequence's length is read ahead.
+template <bool MASK>
 struct KaPos {
     int n, hs, head, tile, u, nu, len, next;
+    KaSkip gap;
+    // First token of unit v of the sequence.
+    __device__ __forceinline__ int token(const KaArgs& a, int v) const {
+        return (MASK && v >= gap.before ? v + gap.skip : v) << a.unit_log2;
+    }
     // Position x of the line, which ka_locate found.
     __device__ __forceinline__ void set(const KaArgs& a, const KaFound& f, int x) {
         n = f.n;
         len = f.len;
         next = f.next;
-        nu = ka_units(a, len);
+        nu = ka_units<MASK>(a, len);
+        gap = ka_skip<MASK>(a, len);
         hs = (x - f.before) / (nu + a.weight);
         u = x - f.before - hs * (nu + a.weight) - a.weight;
         head = hs / a.subs;
@@ -223,7 +313,8 @@ struct KaPos {
         hs = t - n * a.HS;
         len = ka_len(a, n);
         next = 0;
-        nu = ka_units(a, len);
+        nu = ka_units<MASK>(a, len);
+        gap = ka_skip<MASK>(a, len);
         u = 0;
         head = hs / a.subs;
         tile = hs - head * a.subs;
@@ -242,7 +333,8 @@ struct KaPos {
             hs = head = 0;
             ++n;
             len = next;
-            nu = ka_units(a, len);
+            nu = ka_units<MASK>(a, len);
+            gap = ka_skip<MASK>(a, len);
             next = n + 1 < a.N ? ka_len(a, n + 1) : 0;
         }
     }
@@ -258,7 +350,7 @@ struct KjCfg {
     static constexpr int AT_ONCE = ROWS < 64 ? 8 : 16;   // rows of a block
     static constexpr int THREADS = HD / 4 * AT_ONCE;
 };
-template <int HD, int ROWS>
+template <int HD, int ROWS, bool MASK>
 __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
     constexpr int TPR = HD / 4;
     grid_dep_begin();
@@ -291,11 +383,14 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
         #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const float f = j0 + i > last ? 0.f : ex2_ftz(ml[i].x - M);
+            if (MASK && j0 + i > last) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // (0 times an infinity that a row sees)
             L += f * ml[i].y;
             o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
         }
     }
-    const float inv = __fdividef(a.v_pow2, L);
+    float inv = __fdividef(a.v_pow2, L);
+    if constexpr (MASK)
+        if (ka_blank(a, t.n, ka_block_row(a, r), ka_len(a, t.n))) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
     const int64_t at = ka_row(a, t.n, t.head, r, HD) + c;
     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
         *reinterpret_cast<uint2*>(a.O + at) =

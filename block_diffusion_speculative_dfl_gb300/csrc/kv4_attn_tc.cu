@@ -38,6 +38,8 @@
 #include "kv4_attn.cuh"
 #include "paged.h"
 
+#include <type_traits>
+
 namespace dfl {
 
 namespace {
@@ -185,7 +187,8 @@ struct KtExpandK {   // scores of tokens past the length are masked
 
 template <int HD, int KU>
 struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times whatever is stored there must add nothing
-    static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane, int left) {
+    // (nan0, nan1): of tokens nan0 .. nan1 - 1 NaN becomes 0
+    static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane, int left, int nan0 = 0, int nan1 = 0) {
         using Cell = Kv4Cell<HD>;
         constexpr int WPR = HD / 8, RPL = 32 / WPR;
         const int pos = lane % WPR, h = lane / WPR;
@@ -207,6 +210,18 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
                 sw[b] &= held == 4 ? 0xFFFFFFFFu : (1u << 8 * held) - 1;
             }
         }
+        if (nan0 < nan1) {
+            #pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t bytes = __vcmpeq4(sw[b] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = 4 * i + RPL * b + h;
+                    if (tok < nan0 || tok >= nan1) bytes &= ~(0xFFu << 8 * i);
+                }
+                sw[b] &= ~bytes;
+            }
+        }
         #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int c = HD == 128 && b ? pos ^ 8 : pos;
@@ -224,16 +239,18 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
 
 // 16 rows of a tile from bf16 rows of the block (zeros from `left` on), as fp16
 // in units of the pool's power of two, like the cached values.
-template <int HD, int KU>
-__device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t row_stride, uint32_t tile, int lane, int left,
-                                              float inv) {
+// FINITE: infinities and NaN become 0 (block_half8_finite); the rows that have some
+// are returned as bits.
+template <int HD, int KU, bool FINITE = false>
+__device__ __forceinline__ uint32_t kt_block_rows(const __nv_bfloat16* src, int64_t row_stride, uint32_t tile, int lane, int left,
+                                                  float inv) {
     constexpr int WPR = HD / 8, RPL = 32 / WPR, NR = 16 / RPL;
     const int c = lane % WPR, h = lane / WPR;
     const uint32_t at = kt_piece<KU>(tile, h, c);
     if (left <= 0) {
         #pragma unroll
         for (int i = 0; i < NR; ++i) sts128((at ^ (((RPL * i) & 7) << 4)) + RPL * i * 128, make_uint4(0, 0, 0, 0));
-        return;
+        return 0;
     }
     uint4 v[NR];   // all on their way before the first is used
     #pragma unroll
@@ -241,18 +258,22 @@ __device__ __forceinline__ void kt_block_rows(const __nv_bfloat16* src, int64_t 
         const int tok = RPL * i + h;
         v[i] = tok < left ? *reinterpret_cast<const uint4*>(src + tok * row_stride + c * 8) : make_uint4(0, 0, 0, 0);
     }
+    uint32_t rows = 0;
     #pragma unroll
     for (int i = 0; i < NR; ++i) {
         const int r = RPL * i;
-        sts128((at ^ ((r & 7) << 4)) + r * 128, block_half8(v[i], inv));
+        bool bad = false;
+        sts128((at ^ ((r & 7) << 4)) + r * 128, FINITE ? block_half8_finite(v[i], inv, bad) : block_half8(v[i], inv));
+        if (FINITE && bad) rows |= 1u << (r + h);
     }
+    return FINITE ? __reduce_or_sync(0xFFFFFFFFu, rows) : 0;
 }
 
 // Bulk copies of the half cells that one expander warp needs, ahead of their use.
 // A warp's share of a unit is KU / 4 keys; its cells are one ring slot and one
 // step (PARTS = 1), or its K half cells are and its V half cells the next (2).
 // Steps are numbered along a sequence.
-template <int HD, int KU, int RST, int PARTS>
+template <int HD, int KU, int RST, int PARTS, bool MASK>
 struct KtFeed {
     static constexpr int PART = Kv4Cell<HD>::BYTES / PARTS, SHARE = KU / 4, NC = SHARE / KV4_CELL_TOKENS;
     static constexpr int WIN = 32 / NC;   // units whose cells the lanes hold
@@ -261,19 +282,21 @@ struct KtFeed {
     uint8_t* ring;
     uint64_t* full;
     int w, lane;
-    KaPos pos;                 // the segment after the one being copied
+    KaPos<MASK> pos;           // the segment after the one being copied
     int x, x1;                 // units of the range up to it, and in all
     int st = 0, end = 0, win = 0, len = 0, n = 0, head = 0;   // step copied next, end of the segment's, first unit of the window
     int cells = 0;             // lane NC i + j: pool cell j of the warp's in unit win + i
     uint32_t slot = 0, issued = 0;
+    KaSkip gap{0, 0};
 
     __device__ __forceinline__ KtFeed(const KaArgs& a_, const DevErr& err_, uint8_t* ring_, uint64_t* full_, int w_, int lane_,
-                                      const KaPos& pos_, int x0, int x1_)
+                                      const KaPos<MASK>& pos_, int x0, int x1_)
         : a(a_), err(err_), ring(ring_), full(full_), w(w_), lane(lane_), pos(pos_), x(x0), x1(x1_) {}
 
+    __device__ __forceinline__ int unit(int u) const { return MASK && u >= gap.before ? u + gap.skip : u; }
     __device__ __forceinline__ void window(int u) {
         win = u;
-        const int k = (u + lane / NC) * KU + w * SHARE + lane % NC * KV4_CELL_TOKENS;
+        const int k = unit(u + lane / NC) * KU + w * SHARE + lane % NC * KV4_CELL_TOKENS;
         if (k < len) cells = ka_cell(a, n, head, k, err);
     }
     // Whether a step with a token is left; moves to it.
@@ -284,7 +307,9 @@ struct KtFeed {
             const int u1 = min(pos.nu, pos.u + (x1 - x));
             st = PARTS * pos.u;
             len = pos.len; n = pos.n; head = pos.head;
-            end = max(st, PARTS * min(u1, (len - w * SHARE + KU - 1) / KU));   // units with a token of this warp's
+            if constexpr (MASK) gap = pos.gap;
+            const int held = (len - w * SHARE + KU - 1) / KU;   // units with a token of this warp's
+            end = max(st, PARTS * min(u1, MASK ? held - gap.skip : held));
             x += u1 - pos.u;
             if (u1 == pos.nu) pos.next_triple(a);
             win = st / PARTS - WIN;
@@ -297,7 +322,7 @@ struct KtFeed {
         if (u == win + WIN) window(u);
         const int c0 = __shfl_sync(0xFFFFFFFFu, cells, NC * (u - win));
         const int c1 = NC == 2 ? __shfl_sync(0xFFFFFFFFu, cells, NC * (u - win) + 1) : 0;
-        const bool more_than_one = NC == 2 && u * KU + w * SHARE + KV4_CELL_TOKENS < len;
+        const bool more_than_one = NC == 2 && unit(u) * KU + w * SHARE + KV4_CELL_TOKENS < len;
         if (elect_one()) {
             uint8_t* d = ring + slot * NC * PART;
             const uint8_t* base = a.slab.data + st % PARTS * PART;
@@ -314,18 +339,22 @@ struct KtFeed {
 
 // One expander warp: a quarter of the keys of the K tile, then of the V tile, of
 // all units of a range.
-template <int HD, int KU, int RST, int PARTS, int ST>
+// (MASK) own_bad: rows of the triple's own keys whose values are not all finite, a
+// word per triple of four in turn: the softmax warps read triple t's after its P V,
+// before the tiles after the next ST of them are filled.
+template <int HD, int KU, int RST, int PARTS, int ST, bool MASK>
 __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, volatile int* abort, int w, int lane,
                                             uint8_t* ring, uint64_t* raw_full, uint32_t tiles, int tile_bytes,
-                                            uint64_t (*t_full)[ST], uint64_t (*t_empty)[ST], KaPos pos, int x0, int x1) {
+                                            uint64_t (*t_full)[ST], uint64_t (*t_empty)[ST], KaPos<MASK> pos, int x0, int x1,
+                                            uint32_t (*own_bad)[4]) {
     constexpr int HALF = Kv4Cell<HD>::BYTES / 2;
-    using Feed = KtFeed<HD, KU, RST, PARTS>;
+    using Feed = KtFeed<HD, KU, RST, PARTS, MASK>;
     constexpr int PART = Feed::PART;
     constexpr int SHARE = Feed::SHARE, NC = Feed::NC;
     Feed feed(a, err, ring, raw_full, w, lane, pos, x0, x1);
     KtRing<RST> r;
     KtRing<ST> ts;
-    uint32_t taken = 0;
+    uint32_t taken = 0, triple = 0;
     bool ok = true;
     int x = x0;
     pos.enter(x, x1);
@@ -342,7 +371,9 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
     while (x < x1) {
         const bool own = u == pos.nu - 1;
         const int share = w * SHARE;
-        const int left = (own ? a.B : pos.len - u * KU) - share;   // keys of the unit from this warp's first on
+        const int k0 = pos.token(a, u);
+        const int left = (own ? a.B : pos.len - k0) - share;   // keys of the unit from this warp's first on
+        const bool edge = MASK && !own && ka_edge(a, pos.len, k0 + share, SHARE);
         auto turn = [&](int half, auto&& expand) {
             if (PARTS == 2 || half == 0)
                 if (feed.issued < taken + RST && feed.more()) feed.produce();
@@ -357,7 +388,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
             if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
             if (PARTS == 2 || half) { ++taken; r.step(); }
         };
-        if (!own && left >= SHARE && feed.issued > taken + 1) {
+        if (!own && left >= SHARE && feed.issued > taken + 1 && !edge) {
             turn(0, [&](uint32_t src, uint32_t t) { KtExpandK<HD, KU>::run(src, t, lane); });
             if (ok) turn(1, [&](uint32_t src, uint32_t t) { KtExpandV<HD, KU>::run(src, t, lane, KV4_CELL_TOKENS); });
         } else
@@ -371,18 +402,27 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
             const uint32_t src = smem_u32(ring) + r.i * NC * PART + (PARTS == 1 ? half * HALF : 0);
+            uint32_t bad = 0;
             #pragma unroll 1
             for (int j = 0; j < NC; ++j) {   // 16 tokens at a time
                 const int lj = left - j * KV4_CELL_TOKENS;
                 if (!own && lj > 0) {
-                    if (half) KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, lj);
+                    if (MASK && half) {   // NaN of tokens that some row does not see
+                        const int kj = k0 + share + j * KV4_CELL_TOKENS;
+                        KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, lj, edge ? max(a.sinks - kj, 0) : 0,
+                                               edge ? min(pos.len + a.B - a.window - kj, KV4_CELL_TOKENS) : 0);
+                    } else if (half) KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, lj);
                     else KtExpandK<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane);
                 } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
                     const int64_t at = ((int64_t)(pos.n * a.B + share + j * 16) * a.slab.Hkv + pos.head) * HD;
-                    kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj,
-                                          half ? a.v_inv : a.k_inv);
+                    if (MASK && half)
+                        bad |= kt_block_rows<HD, KU, true>(a.Vb + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj, a.v_inv) << (16 * j);
+                    else
+                        kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj,
+                                              half ? a.v_inv : a.k_inv);
                 }
             }
+            if (MASK && own && half && lane == 0) own_bad[triple & 3][w] = bad;
             fence_proxy_async_smem();
             __syncwarp();   // the slot has been read, the rows are written by every lane
             if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
@@ -393,6 +433,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         ++x;
         if (++u == u1) {
             if (u1 == pos.nu) pos.next_triple(a);
+            ++triple;
             pos.enter(x, x1);
             u = pos.u;
             u1 = min(pos.nu, u + (x1 - x));
@@ -445,7 +486,58 @@ __device__ __forceinline__ void kt_load_q(const KaArgs& a, int n, int head, int 
 // Softmax side: M = 128 gives a thread one row (its tensor-memory lane); at
 // M = 64 the 16 rows of a warp's quadrant are shared by its two half-warps,
 // each with half of a row's columns.
-template <int HD, int MM>
+// Tokens k0 .. k1 - 1 (at most 64) with a NaN among their values, as bits from k0 on.  A converged warp.
+template <int HD>
+__device__ __noinline__ uint64_t kt_edge_nans(const KaArgs& a, const DevErr& err, int n, int head, int k0, int k1, int lane) {
+    using Cell = Kv4Cell<HD>;
+    uint64_t nans = 0;
+    #pragma unroll
+    for (int s = 0; s < 64; s += 32) {
+        const int k = k0 + s + lane;
+        bool bad = false;
+        if (k < k1) {
+            const uint8_t* cell = a.slab.data + (int64_t)ka_cell(a, n, head, k & ~(KV4_CELL_TOKENS - 1), err) * Cell::BYTES;
+            #pragma unroll
+            for (int g = 0; g < Cell::GROUPS; ++g) bad |= (cell[Cell::v_scale(k & (KV4_CELL_TOKENS - 1), g)] & 0x7F) == 0x7F;
+        }
+        nans |= (uint64_t)__ballot_sync(0xFFFFFFFFu, bad) << s;
+    }
+    return nans;
+}
+
+// What weights times infinite and NaN values come to, for a row's dims c .. c + 31:
+// of the own rows `bad` and the tokens `nans` from k0 on, which the row sees and
+// whose tiles hold 0 in their place.
+template <int HD>
+__device__ __noinline__ void kt_add_unfinite(const KaArgs& a, const DevErr& err, int n, int head, uint64_t bad, uint64_t nans, int k0,
+                                             int c, float (&o)[32]) {
+    using Cell = Kv4Cell<HD>;
+    #pragma unroll 1
+    for (; bad; bad &= bad - 1) {
+        const __nv_bfloat16* v = a.Vb + ((int64_t)(n * a.B + __ffsll((long long)bad) - 1) * a.slab.Hkv + head) * HD + c;
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float x = __bfloat162float(v[j]);
+            if (!(fabsf(x) < INFINITY)) o[j] += x;
+        }
+    }
+    #pragma unroll 1
+    for (; nans; nans &= nans - 1) {
+        const int k = k0 + __ffsll((long long)nans) - 1;
+        const uint8_t* cell = a.slab.data + (int64_t)ka_cell(a, n, head, k & ~(KV4_CELL_TOKENS - 1), err) * Cell::BYTES;
+        #pragma unroll
+        for (int g = 0; g < 2; ++g)
+            if ((cell[Cell::v_scale(k & (KV4_CELL_TOKENS - 1), c / 16 + g)] & 0x7F) == 0x7F) {
+                #pragma unroll
+                for (int j = 0; j < 16; ++j) o[16 * g + j] = __int_as_float(0x7FFFFFFF);
+            }
+    }
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint64_t kt_ones(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+template <int HD, int MM, bool MASK>
 __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs a, const DevErr err) {
     using Cfg = KtCfg<HD, MM>;
     using Bars = KtBars<Cfg::RST, Cfg::ST>;
@@ -453,6 +545,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     __shared__ Bars bars[KT_PIPES];
     __shared__ KaLineSmem<KT_THREADS, KT_PIPES> line_sm;
     __shared__ float q_up[KT_PIPES][MM];
+    __shared__ uint32_t own_bad[MASK ? KT_PIPES : 1][4][4];   // see kt_expander
+    __shared__ uint64_t row_sees[MASK ? KT_PIPES : 1][MM];    // own rows that a row sees,
+    __shared__ int row_first[MASK ? KT_PIPES : 1][MM];        // its first token behind the sinks
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_flag;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -485,13 +580,13 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
     // ranges go round the CTAs, so that a few of them spread over the SMs
     const int ranges = KT_PIPES * gridDim.x;
     ka_check_lengths<KT_THREADS>(a, err);
-    const KaLine line = ka_locate<KT_THREADS, KT_PIPES>(a, ranges, line_sm, [&](int p, int per, int total) {
+    const KaLine line = ka_locate<MASK, KT_THREADS, KT_PIPES>(a, ranges, line_sm, [&](int p, int per, int total) {
         const int64_t x = (int64_t)(p * gridDim.x + blockIdx.x) * per;
         return x < total ? (int)x : -1;
     });
     const int range = pipe * gridDim.x + blockIdx.x;
     const int64_t x0l = (int64_t)range * line.per;
-    KaPos pos{};
+    KaPos<MASK> pos{};
     int x0 = 0, x1 = 0;   // the range's units (none: x0 = x1)
     if (line.whole) {
         if (range < a.N * a.HS) {
@@ -506,8 +601,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 
     if (warp >= 8) {
         const int w = warp & 3;
-        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::PARTS, Cfg::ST>(a, err, abort, w, lane, sR + w * Cfg::RST * Cfg::SLOT, bb.raw_full[w], smem_u32(sK),
-                                                   Cfg::TILE, bb.t_full, bb.t_empty, pos, x0, x1);
+        kt_expander<HD, Cfg::KU, Cfg::RST, Cfg::PARTS, Cfg::ST, MASK>(a, err, abort, w, lane, sR + w * Cfg::RST * Cfg::SLOT, bb.raw_full[w], smem_u32(sK),
+                                                   Cfg::TILE, bb.t_full, bb.t_empty, pos, x0, x1, own_bad[MASK ? pipe : 0]);
     } else {
         // ------------------------------------------------------------- softmax
         constexpr bool HALF = MM == 64;
@@ -580,6 +675,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             if (elect_one()) mbar_arrive(&bb.q_full);
             if (issuer && !issue_s(true)) { ok = false; break; }
             const float mult = ka_mult(a, q_up[pipe][row]);
+            uint64_t nans = 0;   // tokens from nan0 on that some row does not see, with NaN among their values
+            const int nan0 = MASK && a.window > 0 ? max(max(ka_first(a, pos.len, 0), a.sinks), 0) : 0;
+            if constexpr (MASK) {   // read again by the thread that writes it
+                const int r = row0 + row;
+                row_sees[pipe][row] = r < a.R ? ka_own_sees(a, pos.n, ka_block_row(a, r), pos.len) : 0;
+                row_first[pipe][row] = r < a.R ? ka_first(a, pos.len, ka_depth(a, pos.n, ka_block_row(a, r))) : 0;
+                if (a.window > 0 && u0 == 0) nans = kt_edge_nans<HD>(a, err, pos.n, head, nan0, min(pos.len, pos.len + a.B - a.window), lane);
+            }
             if (x + u1 - u0 < x1) {   // the next triple's Q on its way to L2
                 const bool wrap = pos.hs + 1 == a.HS;
                 const int hs = wrap ? 0 : pos.hs + 1, nn = pos.n + wrap;
@@ -599,8 +702,33 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                 if (!pad) {
                     // The maximum first: O is rescaled only where it grows by more than 2^8
                     // (S of this unit was issued after the P V of the units before had ended).
-                    const int keys = (u == pos.nu - 1 ? a.B : pos.len - u * KU) - hh * KPT;   // from this thread's first on
-                    if (__any_sync(0xFFFFFFFFu, keys < KPT)) {   // a unit's keys past the last: their scores become -inf
+                    const bool own = u == pos.nu - 1;
+                    const int k0u = pos.token(a, u);
+                    const int keys = (own ? a.B : pos.len - k0u) - hh * KPT;   // from this thread's first on
+                    if (MASK && __any_sync(0xFFFFFFFFu, own || keys < KPT || ka_edge(a, pos.len, k0u, KU))) {   // what a row does not see
+                        uint64_t see[2] = {0, 0};   // of this thread's keys
+                        if (own) {
+                            if (hh * KPT < 64) see[0] = row_sees[pipe][row] >> (hh * KPT);
+                        } else {
+                            const int lo = row_first[pipe][row] - k0u - hh * KPT, sk = min(a.sinks, pos.len) - k0u - hh * KPT;
+                            see[0] = kt_ones(keys) & (~kt_ones(lo) | kt_ones(sk));
+                            see[1] = kt_ones(keys - 64) & (~kt_ones(lo - 64) | kt_ones(sk - 64));
+                        }
+                        #pragma unroll 1
+                        for (int k0 = 0; k0 < KPT; k0 += 16) {
+                            const uint32_t bits = (uint32_t)(see[k0 >> 6] >> (k0 & 63));
+                            float s[16];
+                            if constexpr (HALF) tmem_ld16_hx2<KPT>(s_at + k0, s);
+                            else tmem_ld16(s_at + k0, s);
+                            uint32_t v[16];
+                            #pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = bits >> j & 1 ? __float_as_uint(s[j]) : 0xFF800000u;
+                            if constexpr (HALF) tmem_st16u_hx2<KPT>(s_at + k0, v);
+                            else tmem_st16(s_at + k0, v);
+                        }
+                        tmem_st_wait();
+                    }
+                    if (!MASK && __any_sync(0xFFFFFFFFu, keys < KPT)) {   // a unit's keys past the last: their scores become -inf
                         #pragma unroll 1
                         for (int k0 = 0; k0 < KPT; k0 += 16) {
                             float s[16];
@@ -645,7 +773,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                             }
                             l *= al;
                             m = mn;
-                            big = __any_sync(0xFFFFFFFFu, fabsf(m) >= KT_BIG);
+                            big = __any_sync(0xFFFFFFFFu, fabsf(m) >= KT_BIG && (!MASK || m != KA_NONE));   // (no key yet)
                         }
                     };
                     // The weights' exponent is s mult + (7 - m), one fused product and sum: the product is exact there and
@@ -749,7 +877,22 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             const int64_t qrow = real ? ka_row(a, pos.n, head, rr, 1) : 0;
             const int64_t part = ((int64_t)2 * range + (u0 == 0 ? 1 : 0)) * MM + row;
             if constexpr (HALF) l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            const float inv = whole ? __fdividef(a.v_pow2, l) : 1.f;
+            float inv = whole ? __fdividef(a.v_pow2, l) : 1.f;
+            bool blank = false;
+            uint64_t bad = 0;   // own rows that this one sees, with values that are not finite
+            if constexpr (MASK) {
+                blank = real && whole && ka_blank(a, pos.n, ka_block_row(a, rr), pos.len);
+                if (u1 == pos.nu) {
+                    constexpr int SHARE = KU / 4;
+                    #pragma unroll
+                    for (int w = 0; w < 4 && w * SHARE < 64; ++w) bad |= (uint64_t)own_bad[pipe][triple & 3][w] << (w * SHARE);
+                    bad &= row_sees[pipe][row];
+                }
+                uint64_t gone = 0;   // tokens that it does not see
+                if (nans) gone = kt_ones(row_first[pipe][row] - nan0);
+                nans &= ~gone;
+                if (!real) bad = nans = 0;
+            }
             #pragma unroll 1
             for (int c0 = 0; c0 < OPT && !pad; c0 += 32) {
                 float o[32];
@@ -758,6 +901,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                 else tmem_ld32(my + Cfg::O_COL + c0, o);
                 if (!real) continue;
                 const int c = hh * OPT + c0;
+                if constexpr (MASK) {
+                    if (bad | nans) kt_add_unfinite<HD>(a, err, pos.n, head, bad, nans, nan0, c, o);
+                    if (blank) {
+                        inv = 0.f;
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                    }
+                }
                 if (whole) {
                     if (!DFL_IN_BOUNDS(err.word, qrow * HD + c + 31, (int64_t)a.N * a.B * a.Hq * HD)) continue;
                     uint4* dst = reinterpret_cast<uint4*>(a.O + qrow * HD + c);
@@ -824,7 +975,7 @@ size_t kv4_attn_tc_ws_bytes(int R, int hd) {
     return al256(rows * hd * 4) + al256(rows * 8) + al256(sizeof(KaCross) * KT_PIPES * KT_SMS);
 }
 
-dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, cudaStream_t st) {
+dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, bool masked, cudaStream_t st) {
     const int mm = kv4_attn_tc_rows(a.R);
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * mm;
     a.Opart = static_cast<float*>(ws);
@@ -846,15 +997,20 @@ dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void
         ProfScope ps("kv4_attn_join", st);
         return launch_pdl(join, dim3(KT_PIPES * grid, mm / at_once), hd / 4 * at_once, 0, st, a, err);
     };
-    if (hd == 128)
-        return mm == 64 ? run(kv4_attn_tc_kernel<128, 64>, kv4_attn_join_kernel<128, 64>, KtCfg<128, 64>::SMEM, 4,
-                              KjCfg<128, 64>::AT_ONCE)
-                        : run(kv4_attn_tc_kernel<128, 128>, kv4_attn_join_kernel<128, 128>, KtCfg<128, 128>::SMEM, 5,
-                              KjCfg<128, 128>::AT_ONCE);
-    return mm == 64 ? run(kv4_attn_tc_kernel<64, 64>, kv4_attn_join_kernel<64, 64>, KtCfg<64, 64>::SMEM, 6,
+    auto pick = [&](auto flag) -> dfl_status {
+        constexpr bool M = decltype(flag)::value;
+        constexpr int S = M ? 12 : 4;
+        if (hd == 128)
+            return mm == 64 ? run(kv4_attn_tc_kernel<128, 64, M>, kv4_attn_join_kernel<128, 64, M>, KtCfg<128, 64>::SMEM, S,
+                                  KjCfg<128, 64>::AT_ONCE)
+                            : run(kv4_attn_tc_kernel<128, 128, M>, kv4_attn_join_kernel<128, 128, M>, KtCfg<128, 128>::SMEM, S + 1,
+                                  KjCfg<128, 128>::AT_ONCE);
+        return mm == 64 ? run(kv4_attn_tc_kernel<64, 64, M>, kv4_attn_join_kernel<64, 64, M>, KtCfg<64, 64>::SMEM, S + 2,
                               KjCfg<64, 64>::AT_ONCE)
-                    : run(kv4_attn_tc_kernel<64, 128>, kv4_attn_join_kernel<64, 128>, KtCfg<64, 128>::SMEM, 7,
+                        : run(kv4_attn_tc_kernel<64, 128, M>, kv4_attn_join_kernel<64, 128, M>, KtCfg<64, 128>::SMEM, S + 3,
                               KjCfg<64, 128>::AT_ONCE);
+    };
+    return masked ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace dfl

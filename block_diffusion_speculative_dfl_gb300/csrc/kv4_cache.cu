@@ -38,6 +38,7 @@ struct Kv4Rows {
     int max_pages;
     const int32_t* start;   // [N] position of row 0 (negative: the sequence is skipped)
     const int32_t* count;   // [N] rows of each sequence
+    const int32_t* pick;    // [N][R] row that goes to place i, nullable: row i (append)
     int N, R;
     int width;              // groups of a row: Hkv * hd / 16
     int rows;               // rows of a block
@@ -131,7 +132,15 @@ template <int HD>
 __global__ void __launch_bounds__(KR_THREADS, 5) kv4_append_kernel(const Kv4Rows a, const uint4* K, const uint4* V, const DevErr err) {
     grid_dep_begin();
     using Cell = Kv4Cell<HD>;
-    kv4_each<HD>(a, err, [&](const Kv4Item& t) {
+    kv4_each<HD>(a, err, [&](Kv4Item t) {
+        if (a.pick) {
+            const int from = a.pick[(int64_t)t.n * a.R + t.i];
+            if (from < 0 || from >= a.R) {
+                record_error(err, DFL_ERR_INVALID_ARG);
+                return;
+            }
+            t.at += (int64_t)(from - t.i) * a.width;
+        }
         const uint4 k0 = K[2 * t.at], k1 = K[2 * t.at + 1], v0 = V[2 * t.at], v1 = V[2 * t.at + 1];
         int tok;
         uint8_t* cell = row_cell<HD>(a, t, err, tok);
@@ -189,8 +198,8 @@ __global__ void __launch_bounds__(KR_THREADS, 5) kv4_read_kernel(const Kv4Rows a
 }
 
 Kv4Rows rows_args(const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const int32_t* start, const int32_t* count,
-                  int R) {
-    Kv4Rows a{kv4_slab(pool, layer), pg.table, pg.max_pages, start, count, pg.N, R};
+                  const int32_t* pick, int R) {
+    Kv4Rows a{kv4_slab(pool, layer), pg.table, pg.max_pages, start, count, pick, pg.N, R};
     a.width = pool.Hkv * (pool.hd / 16);
     a.rows = std::max(1, KR_THREADS / a.width);
     a.cells_inv = (((uint64_t)1 << 36) + a.slab.cells - 1) / a.slab.cells;
@@ -211,10 +220,10 @@ dim3 rows_grid(const DeviceCtx* ctx, const Kv4Rows& a) {
 }  // namespace
 
 dfl_status kv4_append_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg,
-                          const int32_t* start, const int32_t* n_new, int R, const void* K, const void* V,
-                          cudaStream_t st) {
+                          const int32_t* start, const int32_t* n_new, const int32_t* rows, int R, const void* K,
+                          const void* V, cudaStream_t st) {
     ProfScope ps("kv4_append", st);
-    const Kv4Rows a = rows_args(pool, layer, pg, start, n_new, R);
+    const Kv4Rows a = rows_args(pool, layer, pg, start, n_new, rows, R);
     auto kern = pool.hd == 128 ? kv4_append_kernel<128> : kv4_append_kernel<64>;
     return launch_pdl(kern, rows_grid(ctx, a), KR_THREADS, 0, st, a, static_cast<const uint4*>(K),
                       static_cast<const uint4*>(V), dev_err(ctx));
@@ -223,7 +232,7 @@ dfl_status kv4_append_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, c
 dfl_status kv4_read_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const int32_t* start,
                         const int32_t* count, int R, void* K, void* V, cudaStream_t st) {
     ProfScope ps("kv4_read", st);
-    const Kv4Rows a = rows_args(pool, layer, pg, start, count, R);
+    const Kv4Rows a = rows_args(pool, layer, pg, start, count, nullptr, R);
     auto kern = pool.hd == 128 ? kv4_read_kernel<128> : kv4_read_kernel<64>;
     return launch_pdl(kern, rows_grid(ctx, a), KR_THREADS, 0, st, a, static_cast<uint4*>(K), static_cast<uint4*>(V),
                       dev_err(ctx));

@@ -26,14 +26,15 @@ inline bool pages_fit(const dfl_pages& pg) { return (int64_t)pg.N * pg.max_pages
 // Host-side checks of a pool, a layer of it and (nullable) its page tables.
 dfl_status kv4_check(const dfl_kv4_pool* pool, int layer, const dfl_pages* pg);
 
-// Rows n*R + i (i < n_new[n]) of K / V [N*R][Hkv][hd] to / from positions start[n] + i.
+// Rows n*R + i (i < n_new[n]; with `rows` n*R + rows[n*R + i]) of K / V [N*R][Hkv][hd] to / from positions start[n] + i.
 dfl_status kv4_append_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg,
-                          const int32_t* start, const int32_t* n_new, int R, const void* K, const void* V,
-                          cudaStream_t st);
+                          const int32_t* start, const int32_t* n_new, const int32_t* rows, int R, const void* K,
+                          const void* V, cudaStream_t st);
 dfl_status kv4_read_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const int32_t* start,
                         const int32_t* count, int R, void* K, void* V, cudaStream_t st);
 
-// Attention over the cache and the block's own keys (kv4_attn.cu).
+// Attention over the cache and the block's own keys (kv4_attn.cu).  mask (nullable), window (0: none), sinks: what
+// its rows see.
 constexpr int KV4_MAX_HEAD_ROWS = 65536;   // query rows of a K/V head: B * Hq / Hkv
 // Tokens of a sequence that attention takes: its positions are 32-bit and are
 // looked up as much as 32 units of 128 ahead.
@@ -42,7 +43,8 @@ constexpr int64_t KV4_ATTN_TOKENS = ((int64_t)1 << 31) - 8192;
 dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq);
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd);
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
-                        const void* Kb, const void* Vb, int B, int Hq, void* O, void* ws, cudaStream_t st);
+                        const void* Kb, const void* Vb, int B, int Hq, const uint64_t* mask, int window, int sinks, void* O,
+                        void* ws, cudaStream_t st);
 
 // Page operations (pages.cu).  max_new: a larger n_new is out of range.
 size_t pages_reserve_ws(int64_t N, int64_t num_pages);

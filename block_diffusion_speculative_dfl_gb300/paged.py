@@ -20,6 +20,16 @@ from . import _lib
 from ._lib import Kv4Pool, Pages
 
 
+def alloc_on(index, stream, f, *args, **kw):
+    """f(*args, **kw) with its memory from the stream (None: the current one) that a call launches on."""
+    if stream is None:
+        return f(*args, **kw)
+    if isinstance(stream, int):   # (ExternalStream takes no null handle)
+        stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
+    with torch.cuda.stream(stream):
+        return f(*args, **kw)
+
+
 class PagedCache:
     """Pool, page tables and scratch for N sequences on one device.
 
@@ -72,13 +82,7 @@ class PagedCache:
 
     def _alloc(self, stream, f, *args, **kw):
         """f(*args, **kw) with its memory from the stream that the call launches on."""
-        if stream is None:
-            return f(*args, **kw)
-        if isinstance(stream, int):   # (ExternalStream takes no null handle)
-            stream = (torch.cuda.ExternalStream(stream, device=self._index) if stream else
-                      torch.cuda.default_stream(self._index))
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
+        return alloc_on(self._index, stream, f, *args, **kw)
 
     def _i32(self, x, what):
         if x.dtype is not torch.int32 or not x.is_contiguous() or x.get_device() != self._index or x.numel() != self.N:
@@ -94,10 +98,22 @@ class PagedCache:
                              f"{self.hd}] on {self.book.device}")
         return x.data_ptr(), shape[1]
 
-    def append(self, layer, K, V, start, n_new, stream=None):
-        """Rows K[n, i], V[n, i] (i < n_new[n]) to positions start[n] + i; K, V bf16 [N, R, Hkv, hd]."""
+    def append(self, layer, K, V, start, n_new, stream=None, rows=None):
+        """Rows K[n, i], V[n, i] (i < n_new[n]) to positions start[n] + i; K, V bf16 [N, R, Hkv, hd].
+
+        With ``rows`` int32 [N, R] rows K[n, rows[n, i]], V[n, rows[n, i]]: those of an accepted path.
+        """
         k, R = self._rows(K, "K", self.Hkv)
         v, _ = self._rows(V, "V", self.Hkv, R)
+        if rows is not None:
+            if rows.dtype is not torch.int32 or not rows.is_contiguous() or rows.get_device() != self._index or \
+                    rows.shape != (self.N, R):
+                raise ValueError(f"rows must be a contiguous int32 tensor [{self.N}, {R}] on {self.book.device}")
+            rc = self._lib.dfl_kv4_append_rows(self._pool, layer, self._pages, self._i32(start, "start"),
+                                               self._i32(n_new, "n_new"), rows.data_ptr(), R, k, v, self._st(stream))
+            if rc:
+                _lib._check("dfl_kv4_append_rows", rc)
+            return
         rc = self._lib.dfl_kv4_append(self._pool, layer, self._pages, self._i32(start, "start"),
                                       self._i32(n_new, "n_new"), R, k, v, self._st(stream))
         if rc:
@@ -113,12 +129,16 @@ class PagedCache:
             _lib._check("dfl_kv4_read", rc)
         return K, V
 
-    def attn(self, layer, Q, Kb, Vb, out=None, stream=None):
+    def attn(self, layer, Q, Kb, Vb, out=None, stream=None, mask=None, window=0, sinks=0):
         """Block attention over each sequence's cached tokens and the block's own rows.
 
         Q bf16 [N, B, Hq, hd], Kb, Vb bf16 [N, B, Hkv, hd]; returns O bf16 [N, B, Hq, hd], allocated on the stream of
         the call unless ``out`` is given.  Own rows count as at most 65,504 units of 2^k_exp and 2^v_exp, and keep
         bf16's 8 bits from 2^-14 of a unit up.
+
+        ``mask`` int64 [N, B]: row i sees the own rows whose bits are set, as ``DraftTree.mask`` has them; a row without a
+        bit is no row, its output 0.  ``window``: a row at position q (the cached length + the row's number, or with a
+        mask + its bits less one) sees the keys at positions p with q - p < window or p < ``sinks`` (0: all of them).
         """
         q, B = self._rows(Q, "Q")
         Hq = Q.shape[2]
@@ -135,9 +155,21 @@ class PagedCache:
                 ws = self._alloc(stream, torch.empty, max(need, 16), dtype=torch.uint8, device=self.book.device)
                 ws = self._scratch[need] = (ws, ws.data_ptr(), ws.numel())
             self._attn_ws[(B, Hq)] = ws
-        rc = self._lib.dfl_kv4_attn(self._pool, layer, self._pages, q, k, v, B, Hq, o, ws[1], ws[2], self._st(stream))
+        if mask is None and window == 0 and sinks == 0:
+            rc = self._lib.dfl_kv4_attn(self._pool, layer, self._pages, q, k, v, B, Hq, o, ws[1], ws[2], self._st(stream))
+            if rc:
+                _lib._check("dfl_kv4_attn", rc)
+            return out
+        m = None
+        if mask is not None:
+            if mask.dtype is not torch.int64 or not mask.is_contiguous() or mask.get_device() != self._index or \
+                    mask.shape != (self.N, B):
+                raise ValueError(f"mask must be a contiguous int64 tensor [{self.N}, {B}] on {self.book.device}")
+            m = mask.data_ptr()
+        rc = self._lib.dfl_kv4_attn_masked(self._pool, layer, self._pages, q, k, v, B, Hq, m, window, sinks, o, ws[1], ws[2],
+                                           self._st(stream))
         if rc:
-            _lib._check("dfl_kv4_attn", rc)
+            _lib._check("dfl_kv4_attn_masked", rc)
         return out
 
     def reserve(self, n_new, stream=None):

@@ -18,6 +18,7 @@ import torch
 from . import _lib
 from ._lib import DFL_BF16, DFL_F32, LayerWeights, SampleParams, StepArgs
 from .paged import PagedCache
+from .tree import DraftTree, token_logprobs
 
 
 @dataclass(frozen=True)
@@ -136,6 +137,17 @@ class DraftModel:
         """One draft step on device-resident inputs (H [L][N*C][d], Xb0 [N][B][d] fp32)."""
         self._last_args = self._args(H, Xb0, target, vlog)
         _lib.dfl_draft_step(self._last_args, self.ws, self.ws_bytes, stream)
+
+    def tree(self, tree: DraftTree, anchor, top=8, T=1.0, stream=None) -> DraftTree:
+        """The most probable tree of the last step's drafted positions, behind ``anchor`` int32 [N].
+
+        ``top`` alternatives of each position from softmax(logits / T); the step's logits are kept (``want_logits``).
+        """
+        s = self.shape
+        if self.logits is None:
+            raise ValueError("a tree is built from the step's logits: call want_logits() before the step")
+        lp = token_logprobs(self.logits.view(s.N, s.B - 1, s.V), top=top, T=T, entropy=False, stream=stream)
+        return tree.build(anchor, lp.top_ids, lp.top_logp, stream)
 
     def _step_host(self, H_host, H_dev, Xb0, target, vlog, chunks, stream):
         """``dfl_draft_step_host``: H from (pinned) host memory through ``H_dev``."""

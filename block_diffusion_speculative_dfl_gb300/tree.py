@@ -1,0 +1,144 @@
+"""Trees of drafted tokens over the C ABI: alternatives with log probabilities, a tree of them, acceptance along it.
+
+One serving step with a tree: ``token_logprobs`` gives the drafted positions'
+alternatives, ``DraftTree.build`` the most probable tree of them, the target runs
+over the tree's rows (``PagedCache.attn`` with ``mask=tree.mask``, positions
+``len + tree.depth``), ``DraftTree.accept`` walks along its tokens, and
+``PagedCache.append`` with ``rows=tree.path`` caches what was accepted.  Calls run
+on the current stream (or the one given) and read nothing back, so they can be
+captured into CUDA graphs.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+from ._lib import DFL_BF16, DFL_F32
+from .paged import alloc_on
+
+
+class TokenLogprobs(NamedTuple):
+    """``logp`` of the given tokens (None without any), ``entropy`` (None if not wanted), ``top_ids``, ``top_logp``."""
+    logp: Optional[torch.Tensor]
+    entropy: Optional[torch.Tensor]
+    top_ids: torch.Tensor
+    top_logp: torch.Tensor
+
+
+def _index(x, what):
+    index = x.get_device()
+    if index < 0 or torch.cuda.current_device() != index:
+        raise ValueError(f"{what} must be on the current CUDA device, not on {x.device}")
+    return index
+
+
+def _handle(index, stream):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _lib._stream(stream)
+
+
+def token_logprobs(logits, ids=None, top=0, T=1.0, entropy=True, stream=None) -> TokenLogprobs:
+    """Log probabilities of ``softmax(logits / T)``: of given tokens, its entropy, its ``top`` largest.
+
+    logits bf16 or fp32 [..., V] (the last dim contiguous, the leading dims one behind the other at any stride, the
+    data 16-byte aligned); ids int32 [..., M], contiguous, with the same leading dims: logp fp32 [..., M], -inf for a
+    token outside 0 .. V-1.  entropy fp32 [...]; top_ids int32, top_logp fp32 [..., top], largest first, ties to the
+    lowest id, -1 and -inf where a row has fewer tokens above -inf.  The outputs are allocated on the stream of the
+    call.
+    """
+    index = _index(logits, "logits")
+    if logits.dtype is torch.bfloat16:
+        dt = DFL_BF16
+    elif logits.dtype is torch.float32:
+        dt = DFL_F32
+    else:
+        raise ValueError(f"logits must be bf16 or fp32, not {logits.dtype}")
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError("logits must have at least one token")
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    rows = lead.numel()
+    # the rows' common stride
+    stride = V
+    step, known = 1, False
+    for size, s in zip(reversed(lead), reversed(logits.stride()[:-1])):
+        if size == 1:
+            continue
+        if not known:
+            stride, known = s, True
+        elif s != step * stride:
+            raise ValueError("the rows of logits must lie at one stride")
+        step *= size
+    if (V > 1 and logits.stride(-1) != 1) or (rows > 1 and stride < V):
+        raise ValueError("a row of logits must be contiguous and the rows apart")
+    M = 0
+    if ids is not None:
+        if ids.dtype is not torch.int32 or not ids.is_contiguous() or ids.get_device() != index or ids.shape[:-1] != lead or \
+                ids.dim() != logits.dim():
+            raise ValueError(f"ids must be a contiguous int32 tensor {list(lead)} + [tokens] on {logits.device}")
+        M = ids.shape[-1]
+    top = int(top)
+    if not 0 <= top <= 64:
+        raise ValueError(f"top={top} outside 0..64")
+
+    def new(shape, dtype):
+        return alloc_on(index, stream, torch.empty, shape, dtype=dtype, device=logits.device)
+
+    out = TokenLogprobs(new((*lead, M), torch.float32) if ids is not None else None,
+                        new(lead, torch.float32) if entropy else None,
+                        new((*lead, top), torch.int32), new((*lead, top), torch.float32))
+    if rows == 0 or (M == 0 and not top and not entropy):
+        return out
+    _lib.dfl_token_logprobs(logits, dt, rows, V, stride, float(T), ids if M else None, M, out.logp if M else None, out.entropy,
+                            top, out.top_ids if top else None, out.top_logp if top else None, _handle(index, stream))
+    return out
+
+
+class DraftTree:
+    """Trees of at most B rows (the anchor among them) for N sequences: buffers and calls.
+
+    ``token``, ``parent``, ``depth`` int32 [N][B], ``mask`` int64 [N][B] (bit j: the row sees row j), ``count`` int32
+    [N], written by ``build`` (or by the caller: a fixed tree); ``path`` int32 [N][B], ``accept_len``, ``n_rows``,
+    ``bonus`` int32 [N], written by ``accept``.  The buffers stay where they are between calls; calls on one tree belong
+    on one stream, or ordered after one another.
+    """
+
+    def __init__(self, N, B, device="cuda"):
+        if N < 1 or not 1 <= B <= 64:
+            raise ValueError(f"trees of {B} rows for {N} sequences: 1 to 64 rows, at least one sequence")
+        dev = torch.device(device)
+        self.N, self.B = N, B
+
+        def buf(*shape, dtype=torch.int32, fill=0):
+            return torch.full(shape, fill, dtype=dtype, device=dev)
+
+        self.token, self.parent, self.depth = buf(N, B, fill=-1), buf(N, B, fill=-2), buf(N, B)
+        self.mask, self.count = buf(N, B, dtype=torch.int64), buf(N)
+        self.path, self.accept_len, self.n_rows, self.bonus = buf(N, B, fill=-1), buf(N), buf(N), buf(N)
+        self._at = self.token.get_device()
+
+    def _check(self, x, what, shape, dtype=torch.int32):
+        if x.dtype is not dtype or not x.is_contiguous() or x.get_device() != self._at or tuple(x.shape) != shape:
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {self.token.device}")
+
+    def build(self, anchor, top_ids, top_logp, stream=None):
+        """The most probable tree of the alternatives of G positions behind the anchor.
+
+        anchor int32 [N]; top_ids int32, top_logp fp32 [N, G, K], best first, as ``token_logprobs`` gives them.
+        """
+        _index(self.token, "the tree")
+        G, K = top_ids.shape[1:] if top_ids.dim() == 3 else (0, 0)
+        self._check(anchor, "anchor", (self.N,))
+        self._check(top_ids, "top_ids", (self.N, max(G, 1), max(K, 1)))
+        self._check(top_logp, "top_logp", (self.N, G, K), torch.float32)
+        _lib.dfl_draft_tree(anchor, top_ids, top_logp, self.N, G, K, self.B, self.token, self.parent, self.depth, self.mask,
+                            self.count, _handle(self._at, stream))
+        return self
+
+    def accept(self, target, stream=None):
+        """Greedy acceptance: target int32 [N, B], the target's token behind each row; returns (path, accept_len, bonus)."""
+        _index(self.token, "the tree")
+        self._check(target, "target", (self.N, self.B))
+        _lib.dfl_tree_accept(self.token, self.parent, target, self.N, self.B, self.path, self.accept_len, self.n_rows,
+                             self.bonus, _handle(self._at, stream))
+        return self.path, self.accept_len, self.bonus

@@ -667,6 +667,40 @@ dfl_status dfl_kv4_attn(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages
                         void* ws, size_t ws_bytes, dfl_stream stream);
 
 /*
+ * dfl_kv4_append_rows -- dfl_kv4_append of chosen rows: row n*R + rows[n*R + i]
+ *   goes to position start[n] + i, for i < n_new[n] (the rows of an accepted path).
+ *   rows    in, device int32 [N*R]; an entry outside 0..R-1 writes nothing and
+ *           records DFL_ERR_INVALID_ARG, alone
+ */
+dfl_status dfl_kv4_append_rows(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
+                               const int32_t* start, const int32_t* n_new, const int32_t* rows, int32_t R,
+                               const void* K, const void* V, dfl_stream stream);
+
+/*
+ * dfl_kv4_attn_masked -- dfl_kv4_attn of rows that do not see everything: a tree
+ *   of drafted tokens (or a causal run of them, its own kind of tree), a sliding
+ *   window with the first tokens kept visible (sinks), or both.
+ *   Row i of a sequence with len cached tokens has the position len + depth,
+ *   depth = (bits of mask[i]) - 1, or len + i without a mask.  It sees the cached
+ *   tokens and the own rows j whose bit of mask[i] is set (without a mask all),
+ *   and with a window of those the keys at positions p with
+ *     q - p < window  or  p < sinks.
+ *   mask    in, nullable device uint64 [N*B], 8-byte aligned (as dfl_draft_tree
+ *           gives them); bits from B on count for nothing
+ *   window  0: none; sinks >= 0
+ *   A row whose mask is 0 (no row of the tree) sees nothing, cached tokens among
+ *   it.  A row that sees nothing has the output 0.  What a row does not see does not touch its
+ *   output, NaN and infinities among it; an infinite or NaN element of an own value that
+ *   a row sees makes that element of its output NaN or infinite.
+ *   Bytes read are those of the tokens that some row sees, to whole units of 64 or 128.
+ *   The rest, and the errors, as dfl_kv4_attn; ws: as for it.
+ */
+dfl_status dfl_kv4_attn_masked(const dfl_kv4_pool* pool, int32_t layer, const dfl_pages* pages,
+                               const void* Q, const void* Kb, const void* Vb, int32_t B, int32_t Hq,
+                               const uint64_t* mask, int32_t window, int32_t sinks, void* O, void* ws,
+                               size_t ws_bytes, dfl_stream stream);
+
+/*
  * dfl_pages_reserve -- room for n_new[n] more tokens of each sequence.
  *   Sequences are served in order; the k-th page asked for is the k-th lowest
  *   free one (ref 0).  A last page that is partly filled and held by others too
@@ -734,6 +768,82 @@ typedef struct dfl_paged_ctx {
  */
 dfl_status dfl_draft_step_paged(const dfl_step_args* args, const dfl_paged_ctx* ctx, void* ws,
                                 size_t ws_bytes, dfl_stream stream);
+
+/*
+ * Trees of drafted tokens.
+ *
+ * A tree has B rows, at most 64.  Row 0 is the anchor (the last token already
+ * decided, position 0 of the drafted block); every other row is a drafted token
+ * with an earlier row as its parent.  parent[i]: that row, -1 for the anchor,
+ * -2 where there is no row; mask[i]: bit j set where row i sees row j (itself
+ * and its ancestors); depth[i]: rows above it, so that its position is the
+ * cached length + depth[i].
+ */
+
+/*
+ * dfl_token_logprobs -- log probabilities of given tokens, entropy and the top
+ *   alternatives of each row of logits, from one read of them.
+ *   SpecDiff-2 notes, "Parallel drafting with diffusion language models": the
+ *   drafter's marginals softmax(z / T) of a position.
+ *     lse = log sum exp(z / T),  logp = z[id] / T - lse,
+ *     entropy = lse - sum p z / T
+ *   logits    in, [rows] rows of V elements (dt: fp32 or bf16), row_stride
+ *             elements apart (any stride >= V; the base 16-byte aligned)
+ *   T         temperature, 1e-6 .. 1e6
+ *   ids       in, nullable int32 [rows][M]; logp out, fp32 [rows][M]; -inf for an
+ *             id outside 0..V-1
+ *   entropy   out, nullable fp32 [rows]
+ *   top_ids   out, nullable int32 [rows][K], K <= 64: the tokens of the K largest
+ *             logits, largest first, ties to the lowest id; top_logp out, fp32
+ *             [rows][K].  Tokens at -inf are none: -1 and -inf fill up a row
+ *   fp32 sums.  A row of -inf throughout, and one with a NaN or +inf, is no
+ *   distribution: its entropy and the logp of its tokens are NaN.  (Its top ids
+ *   are those of the order all the same, NaNs left out.)
+ *   The same inputs give the same bits.
+ *   Errors: INVALID_ARG (no output asked for, T, K above 64), UNSUPPORTED_SHAPE
+ *   (rows 2^31, V above 2^30, row_stride above 2^40), MISALIGNED.
+ */
+dfl_status dfl_token_logprobs(const void* logits, int32_t dt, int64_t rows, int32_t V,
+                              int64_t row_stride, float T, const int32_t* ids, int32_t M, float* logp,
+                              float* entropy, int32_t K, int32_t* top_ids, float* top_logp,
+                              dfl_stream stream);
+
+/*
+ * dfl_draft_tree -- the most probable tree of B rows from the alternatives of G
+ *   drafted positions.  DFlare post, "Generating candidates in parallel, the
+ *   target decides acceptance": the positions' marginals are independent given
+ *   the context, so a path has the product of its tokens' probabilities.
+ *   A row of depth g (the anchor: 0) has the K alternatives of position g as
+ *   children, each with the score: row's score + logp (fp64; the anchor's is 0).  Rows
+ *   are added best first, an alternative after its better ranks; ties go to the
+ *   lowest parent.  -inf and NaN are no alternatives, nor are those behind them.
+ *   anchor    in, int32 [N]
+ *   top_ids, top_logp   in, [N][G][K], best first (as dfl_token_logprobs gives them)
+ *   token, parent, depth   out, int32 [N][B]; mask out, uint64 [N][B]
+ *   count     out, int32 [N]: rows of the tree.  Rows behind them: token -1,
+ *             parent -2, depth 0, mask 0
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (B above 64), MISALIGNED.
+ */
+dfl_status dfl_draft_tree(const int32_t* anchor, const int32_t* top_ids, const float* top_logp, int32_t N,
+                          int32_t G, int32_t K, int32_t B, int32_t* token, int32_t* parent,
+                          int32_t* depth, uint64_t* mask, int32_t* count, dfl_stream stream);
+
+/*
+ * dfl_tree_accept -- greedy acceptance along a tree; dfl_greedy_accept where
+ *   every row has one child.  DFlare post, "Generating candidates in parallel,
+ *   the target decides acceptance".  From the anchor on, the child (the lowest row of
+ *   several) whose token is the target's behind the current row, until none is.
+ *   token, parent   in, int32 [N][B]
+ *   target      in, int32 [N][B]: the target's token behind each row
+ *   path        out, int32 [N][B]: the rows passed, row 0 first, then -1
+ *   accept_len  out, int32 [N]: drafted tokens accepted, 0..B-1
+ *   n_rows      out, nullable int32 [N]: accept_len + 1, the rows to be cached
+ *   bonus       out, int32 [N]: the target's token behind the last row
+ *   Errors: INVALID_ARG, UNSUPPORTED_SHAPE (B above 64), MISALIGNED.
+ */
+dfl_status dfl_tree_accept(const int32_t* token, const int32_t* parent, const int32_t* target, int32_t N,
+                           int32_t B, int32_t* path, int32_t* accept_len, int32_t* n_rows,
+                           int32_t* bonus, dfl_stream stream);
 
 /* Synchronise `stream`, then read and clear this device's error word (DFL_OK
  * if no kernel recorded an error). */
