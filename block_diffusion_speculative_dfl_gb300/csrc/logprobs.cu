@@ -9,27 +9,30 @@
 // reference serves that is near the maximum; rows whose maximum is past 2^20 in y take
 // differences of logits first, in a second pass.
 //
-// Alternatives cost the pass one maximum an element: a thread keeps its largest
-// logit and where it met it first.  Order all elements by (logit, then lowest
-// index).  Were a thread that holds one of the K best not among the K threads whose
-// own best are first in that order, K elements would be before it; so the K best
-// lie with these K threads, at or before the K-th of their bests.  Those threads'
-// elements are read once more (from L2), and the few at or before that place are
-// ranked by counting.
+// Alternatives cost the pass one maximum an element: each group of vectors (a
+// thread's) has its largest logit and where it was met first.  Order all elements by
+// (logit, then lowest index).  Were a group that holds one of the K best not among the
+// K groups whose own best are first in that order, K elements would be before it; so
+// the K best lie in these K groups, at or before the K-th of their bests.  The
+// vectors of those bests are read once more, and a group throughout only where its
+// second best vector reaches that place too; the few elements that do are ranked by
+// counting.
 //
 // A row is cut among 1 to 8 CTAs of a cluster, which join their parts through
 // distributed shared memory in a fixed order: results repeat bit for bit.
 #include "internal.h"
 #include "tree.h"
 
+#include <type_traits>
+
 namespace dfl {
 
 namespace {
 
 constexpr int LP_THREADS = 256;
-constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_WARPS = LP_THREADS / 32;   // of a CTA
 constexpr int LP_UNROLL = 4;       // 16-byte loads in flight per thread
-constexpr int LP_CAND = 512;       // candidates ranked at once
+constexpr int LP_MAX_CLUSTER = 8;
 constexpr float LP_LAZY = 8.f;     // a thread's reference moves when passed by more (log2)
 constexpr float LP_FAR = 1048576.f;  // references stay within: rounded by 2^-5 at most, which a sum takes
 constexpr float LP_TINY = -1000.f; // exponents stay above: 2^-1000 is 0 and 0 * -1000 is 0, where 0 * -inf is NaN
@@ -99,11 +102,28 @@ struct LpSums {
     }
 };
 
+// Joins the sums and maxima of each LANES lanes, with the same result in all of them.
+template <int LANES>
+__device__ __forceinline__ void lp_join_lanes(LpSums& t, float& zmax) {
+    #pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        LpSums q;
+        q.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
+        q.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
+        q.w = __shfl_xor_sync(0xFFFFFFFFu, t.w, o);
+        t.join(q);
+        zmax = fmaxf(zmax, __shfl_xor_sync(0xFFFFFFFFu, zmax, o));
+    }
+    t.m = __shfl_sync(0xFFFFFFFFu, t.m, 0);
+    t.s = __shfl_sync(0xFFFFFFFFu, t.s, 0);
+    t.w = __shfl_sync(0xFFFFFFFFu, t.w, 0);
+    zmax = __shfl_sync(0xFFFFFFFFu, zmax, 0);
+}
+
 struct LpPart {              // what a CTA of a row's cluster leaves for the first of them
     LpSums sum;
     float zmax;
-    int top;                 // its best elements, first come first
-    uint64_t key[LP_MAX_TOP];
+    uint64_t key[LP_MAX_TOP];   // its best K elements, first come first; 0: none
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t a) {
@@ -117,29 +137,59 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t a) {
     return v;
 }
 
-template <typename T, bool TOP>
+// The threads of a row's part: NW warps, one of them eight to a CTA.
+template <int NW>
+__device__ __forceinline__ void team_sync() {
+    if constexpr (NW == 1) __syncwarp();
+    else __syncthreads();
+}
+
+template <int NW>
+struct LpTeam {
+    static constexpr int THREADS = 32 * NW;
+    // Groups of the row's vectors, each with its best element: a thread's vectors, or each load slot's of a lone warp (its 32
+    // lanes would be too few: many elements would lie in the groups of the K best).
+    static constexpr int PER_THREAD = NW == 1 ? LP_UNROLL : 1, GROUPS = PER_THREAD * THREADS;
+    static constexpr int CAND = NW == 1 ? 128 : 512;   // candidates ranked at once
+    uint64_t cand[CAND];
+    uint64_t warp_key[NW];
+    LpPart part;
+    LpSums red[NW];
+    float red_z[NW];
+    uint32_t best_o[GROUPS];    // groups' largest logits in order,
+    uint32_t best_v[GROUPS];    // the vectors they were met in first,
+    float next_z[GROUPS];       // the largest logit of their other vectors
+    int hot[LP_MAX_TOP];        // groups with the first of these, in their order
+    int again[LP_MAX_TOP];      // those of them to be read once more
+    int n_hot, n_again, n_cand;
+};
+
+__device__ __forceinline__ uint32_t lp_ordered(float z) {
+    const uint32_t b = __float_as_uint(z + 0.f);   // -0 as 0
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+constexpr uint32_t LP_NONE = 0x007FFFFFu;          // -inf in that order
+
+// NW = 8: a CTA per row or part of one (C of a cluster); NW = 1: a warp per row.
+template <typename T, bool TOP, int NW>
 __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpArgs a, int C, const DevErr err) {
     using Vec = LpVec<T>;
-    constexpr int EPV = Vec::N;
-    __shared__ LpPart part;
-    __shared__ LpSums red[LP_WARPS];
-    __shared__ float red_z[LP_WARPS];
-    __shared__ float best_z[LP_THREADS];      // threads' largest logits,
-    __shared__ uint32_t best_v[LP_THREADS];   // the vectors they were met in first
-    __shared__ int hot[LP_MAX_TOP];           // threads with the first of these, in their order
-    __shared__ uint64_t cand[LP_CAND];
-    __shared__ uint64_t warp_key[LP_WARPS];
-    __shared__ int n_cand;
+    using Team = LpTeam<NW>;
+    constexpr int EPV = Vec::N, THREADS = Team::THREADS, TEAMS = LP_THREADS / THREADS;
+    __shared__ Team teams[TEAMS];
     grid_dep_begin();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / C;
-    const int rank = (int)(blockIdx.x - row * C);
+    const int tid = threadIdx.x % THREADS, lane = threadIdx.x & 31, warp = tid >> 5;
+    Team& sm = teams[threadIdx.x / THREADS];
+    LpPart& part = sm.part;
+    const int64_t row = NW == 1 ? (int64_t)blockIdx.x * TEAMS + threadIdx.x / THREADS : blockIdx.x / C;
+    if (NW == 1 && row >= a.rows) return;
+    const int rank = NW == 1 ? 0 : (int)(blockIdx.x - (unsigned)row * C);
     const T* z0 = static_cast<const T*>(a.logits) + row * a.stride;
     // the row as 16-byte vectors: vector v holds elements v EPV - head .. + EPV - 1
     const int head = (int)((reinterpret_cast<uintptr_t>(z0) & 15) / sizeof(T));
     const uint4* vec = reinterpret_cast<const uint4*>(z0 - head);
     const int nv = (head + a.V + EPV - 1) / EPV, whole0 = head > 0, whole1 = (head + a.V) / EPV;
-    const int per = (nv + C - 1) / C, v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
+    const int per = NW == 1 ? nv : (nv + C - 1) / C, v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
     // elements of vector v that belong to the row, the others as -inf
     auto load = [&](int v, float (&z)[EPV]) {
         if (v >= whole0 && v < whole1) { Vec::get(vec[v], z); return; }
@@ -151,15 +201,21 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     };
 
     LpSums t{-LP_FAR, 0.f, 0.f};
-    float zmax = -INFINITY;
-    uint32_t zat = 0xFFFFFFFFu;
-    auto add = [&](const float (&z)[EPV], int v) {
+    constexpr int PT = Team::PER_THREAD;
+    float best_z[PT], next_z[PT];
+    uint32_t best_at[PT];
+    #pragma unroll
+    for (int i = 0; i < PT; ++i) { best_z[i] = next_z[i] = -INFINITY; best_at[i] = 0xFFFFFFFFu; }
+    auto add = [&](const float (&z)[EPV], int v, int i) {
         float m4[2] = {z[0], z[1]};
         #pragma unroll
         for (int e = 2; e < EPV; e += 2) { m4[0] = fmaxf(m4[0], z[e]); m4[1] = fmaxf(m4[1], z[e + 1]); }
         const float mx = fmaxf(m4[0], m4[1]);
-        if (TOP && (mx > zmax || (mx == zmax && (uint32_t)v < zat))) zat = (uint32_t)v;
-        zmax = fmaxf(zmax, mx);
+        if (TOP) {
+            if (mx > best_z[i] || (mx == best_z[i] && (uint32_t)v < best_at[i])) best_at[i] = (uint32_t)v;
+            next_z[i] = fmaxf(next_z[i], fminf(best_z[i], mx));
+        }
+        best_z[i] = fmaxf(best_z[i], mx);
         const float ref = mx * a.c;
         if (ref > t.m + LP_LAZY) t.move(ref);
         #pragma unroll
@@ -171,11 +227,11 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     };
     const int lo = max(v0, whole0), hi = min(v1, whole1);
     #pragma unroll 1
-    for (int v = v0 + tid; v < hi; v += LP_UNROLL * LP_THREADS) {
+    for (int v = v0 + tid; v < hi; v += LP_UNROLL * THREADS) {
         uint4 raw[LP_UNROLL];
         #pragma unroll
         for (int u = 0; u < LP_UNROLL; ++u) {
-            const int at = v + u * LP_THREADS;
+            const int at = v + u * THREADS;
             raw[u] = make_uint4(Vec::NONE, Vec::NONE, Vec::NONE, Vec::NONE);
             if (at >= lo && at < hi) raw[u] = ldg_stream(vec + at);
         }
@@ -183,143 +239,199 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
         for (int u = 0; u < LP_UNROLL; ++u) {
             float z[EPV];
             Vec::get(raw[u], z);
-            add(z, v + u * LP_THREADS);
+            add(z, v + u * THREADS, u % PT);
         }
     }
     // the row's ends, where they share a vector with something else
     #pragma unroll 1
     for (int end = 0; end < 2; ++end) {
         const int v = end ? nv - 1 : 0;
-        if (v >= v0 && v < v1 && (end ? v >= whole1 && v >= whole0 : v < whole0) && (v - v0) % LP_THREADS == tid) {
+        if (v >= v0 && v < v1 && (end ? v >= whole1 && v >= whole0 : v < whole0) && (v - v0) % THREADS == tid) {
             float z[EPV];
             load(v, z);
-            add(z, v);
-        }
-    }
-
-    // ---- sums of the CTA
-    if (TOP) { best_z[tid] = zmax; best_v[tid] = zat; }
-    #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        LpSums q;
-        q.m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
-        q.s = __shfl_xor_sync(0xFFFFFFFFu, t.s, o);
-        q.w = __shfl_xor_sync(0xFFFFFFFFu, t.w, o);
-        t.join(q);
-        zmax = fmaxf(zmax, __shfl_xor_sync(0xFFFFFFFFu, zmax, o));
-    }
-    if (lane == 0) { red[warp] = t; red_z[warp] = zmax; }
-    if (tid == 0) n_cand = 0;
-    if (TOP && tid < LP_MAX_TOP) hot[tid] = -1;
-    __syncthreads();
-    t = red[0];
-    zmax = red_z[0];
-    #pragma unroll 1
-    for (int w = 1; w < LP_WARPS; ++w) { t.join(red[w]); zmax = fmaxf(zmax, red_z[w]); }
-
-    // ---- the CTA's best K elements
-    if constexpr (TOP) {
-        const float bz = best_z[tid];
-        const uint32_t bv = best_v[tid];
-        int before = 0;
-        #pragma unroll 4
-        for (int j = 0; j < LP_THREADS; ++j) {
-            const float oz = best_z[j];
-            before += oz > bz || (oz == bz && best_v[j] < bv);
-        }
-        if (before < a.K && bz > -INFINITY) hot[before] = tid;
-        __syncthreads();
-        // the last of them has the place to reach: its first largest element
-        int nh = 0;
-        while (nh < a.K && hot[nh] >= 0) ++nh;
-        uint64_t least = 0;
-        if (nh == a.K) {   // (fewer: every element above -inf is a candidate)
-            const int th = hot[nh - 1];
-            const float oz = best_z[th];
-            float z[EPV];
-            load((int)best_v[th], z);
             #pragma unroll
-            for (int e = EPV - 1; e >= 0; --e)
-                if (z[e] == oz) least = lp_key(oz, (uint32_t)((int)best_v[th] * EPV - head + e));
+            for (int i = 0; i < PT; ++i)
+                if (i == (v - v0) / THREADS % PT) add(z, v, i);
         }
-        const int len = (v1 - v0 + LP_THREADS - 1) / LP_THREADS;   // vectors of a thread, at most
-        auto each = [&](auto&& f) {
-            #pragma unroll 1
-            for (int64_t i = tid; i < (int64_t)nh * len; i += LP_THREADS) {
-                const int h = (int)(i / len), v = v0 + hot[h] + (int)(i - (int64_t)h * len) * LP_THREADS;
-                if (v >= v1) continue;
-                float z[EPV];
-                load(v, z);
-                #pragma unroll
-                for (int e = 0; e < EPV; ++e)
-                    if (z[e] > -INFINITY) f(lp_key(z[e], (uint32_t)(v * EPV - head + e)));
-            }
-        };
-        each([&](uint64_t key) {
-            if (key >= least) {
-                const int c = atomicAdd(&n_cand, 1);
-                if (c < LP_CAND) cand[c] = key;
-            }
-        });
+    }
+    float zmax = best_z[0];
+    #pragma unroll
+    for (int i = 1; i < PT; ++i) zmax = fmaxf(zmax, best_z[i]);
+
+    // ---- sums of the team
+    if constexpr (TOP) {
+        #pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            const int g = i * THREADS + tid;
+            sm.best_o[g] = lp_ordered(best_z[i]);
+            sm.best_v[g] = best_at[i];
+            sm.next_z[g] = next_z[i];
+        }
+    }
+    lp_join_lanes<32>(t, zmax);
+    if (tid == 0) sm.n_cand = sm.n_again = 0;
+    if constexpr (NW > 1) {
+        if (lane == 0) { sm.red[warp] = t; sm.red_z[warp] = zmax; }
         __syncthreads();
-        const int nc = n_cand;
-        if (nc <= LP_CAND) {
-            #pragma unroll 1
-            for (int c = tid; c < nc; c += LP_THREADS) {
-                const uint64_t key = cand[c];
-                int r = 0;
-                #pragma unroll 1
-                for (int j = 0; j < nc; ++j) r += cand[j] > key;
-                if (r < a.K) part.key[r] = key;
+        t = lane < NW ? sm.red[lane] : LpSums{-LP_FAR, 0.f, 0.f};
+        zmax = lane < NW ? sm.red_z[lane] : -INFINITY;
+        lp_join_lanes<NW>(t, zmax);
+    } else {
+        __syncwarp();
+    }
+
+    // ---- the team's best K elements
+    if constexpr (TOP) {
+        // The K groups whose bests come first, one after the other, by the first warp.  (By counting, for every thread, those
+        // before it: 2,560 instructions of every warp, 18 us of a row's time with four CTAs to an SM.)
+        uint64_t least = 0;
+        if (warp == 0) {
+            constexpr int N = Team::GROUPS / 32;
+            uint32_t o[N], v[N];
+            #pragma unroll
+            for (int i = 0; i < N; ++i) {
+                o[i] = sm.best_o[lane + 32 * i];
+                v[i] = sm.best_v[lane + 32 * i];
             }
-            if (tid == 0) part.top = min(nc, a.K);
-        } else {   // many before that place, as in a sorted row: one after the other
-            uint64_t last = ~0ull;
             int r = 0;
             #pragma unroll 1
             for (; r < a.K; ++r) {
+                uint32_t m = o[0];
+                #pragma unroll
+                for (int i = 1; i < N; ++i) m = max(m, o[i]);
+                const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, m);
+                if (best <= LP_NONE) break;
+                uint32_t at = 0xFFFFFFFFu;
+                #pragma unroll
+                for (int i = 0; i < N; ++i) at = o[i] == best ? min(at, v[i]) : at;
+                const uint32_t first = __reduce_min_sync(0xFFFFFFFFu, at);
+                #pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (o[i] == best && v[i] == first) {
+                        o[i] = 0;
+                        sm.hot[r] = lane + 32 * i;
+                    }
+                // the last of K has the place to reach, to its vector's end (fewer: every element above -inf is a candidate)
+                if (r + 1 == a.K) least = (uint64_t)best << 32 | (0xFFFFFFFFu - (first * EPV - head + EPV - 1));
+            }
+            if (lane == 0) { sm.n_hot = r; sm.warp_key[0] = least; }
+        }
+        team_sync<NW>();
+        const int nh = sm.n_hot;
+        least = sm.warp_key[0];
+        const float from = nh == a.K ? lp_key_value(least) : -INFINITY;
+        auto push = [&](uint64_t key) {
+            if (key < least) return;
+            const int c = atomicAdd(&sm.n_cand, 1);
+            if (c < Team::CAND) sm.cand[c] = key;
+        };
+        // Nearly always a group's only vector that reaches that place is the one of its best.
+        #pragma unroll 1
+        for (int h = tid; h < nh; h += THREADS) {
+            const int g = sm.hot[h], v = (int)sm.best_v[g];
+            float z[EPV];
+            load(v, z);
+            if (sm.next_z[g] >= from && sm.next_z[g] > -INFINITY) sm.again[atomicAdd(&sm.n_again, 1)] = g;
+            #pragma unroll
+            for (int e = 0; e < EPV; ++e)
+                if (z[e] >= from && z[e] > -INFINITY) push(lp_key(z[e], (uint32_t)(v * EPV - head + e)));
+        }
+        team_sync<NW>();
+        const int na = sm.n_again, len = (v1 - v0 + Team::GROUPS - 1) / Team::GROUPS;   // vectors of a group at most; len * 64 < 2^27
+        // f of the keys from `low` on of n groups; four loads of a thread on their way at once
+        auto each = [&](const int* groups, int n, bool best_too, float low, auto&& f) {
+            const int items = n * len;
+            #pragma unroll 1
+            for (int j = tid; j < items; j += 4 * THREADS) {
+                uint4 raw[4];
+                int v[4];
+                #pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int k = min(j + u * THREADS, items - 1), h = k / len, g = groups[h];
+                    v[u] = v0 + g + (k - h * len) * Team::GROUPS;
+                    if (j + u * THREADS >= items || (!best_too && v[u] == (int)sm.best_v[g])) v[u] = v1;
+                    raw[u] = make_uint4(Vec::NONE, Vec::NONE, Vec::NONE, Vec::NONE);
+                    if (v[u] >= lo && v[u] < hi) raw[u] = vec[v[u]];
+                }
+                #pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    float z[EPV];
+                    Vec::get(raw[u], z);
+                    if (v[u] < v1 && !(v[u] >= lo && v[u] < hi)) load(v[u], z);
+                    float m = z[0];
+                    #pragma unroll
+                    for (int e = 1; e < EPV; ++e) m = fmaxf(m, z[e]);
+                    if (!(m >= low && m > -INFINITY)) continue;
+                    #pragma unroll
+                    for (int e = 0; e < EPV; ++e)
+                        if (z[e] >= low && z[e] > -INFINITY) f(lp_key(z[e], (uint32_t)(v[u] * EPV - head + e)));
+                }
+            }
+        };
+        if (na > 0) {   // (uniform)
+            each(sm.again, na, false, from, push);
+            team_sync<NW>();
+        }
+        const int nc = sm.n_cand;
+        if (nc <= Team::CAND) {
+            #pragma unroll 1
+            for (int c = tid; c < nc; c += THREADS) {
+                const uint64_t key = sm.cand[c];
+                int r = 0;
+                #pragma unroll 4
+                for (int j = 0; j < nc; ++j) r += sm.cand[j] > key;
+                if (r < a.K) part.key[r] = key;
+            }
+            #pragma unroll 1
+            for (int r = nc + tid; r < a.K; r += THREADS) part.key[r] = 0;
+        } else {   // many before that place, as in a sorted row: one after the other
+            uint64_t last = ~0ull;
+            #pragma unroll 1
+            for (int r = 0; r < a.K; ++r) {
                 uint64_t best = 0;
-                each([&](uint64_t key) { if (key < last && key > best) best = key; });
+                each(sm.hot, nh, true, -INFINITY, [&](uint64_t key) { if (key < last && key > best) best = key; });
                 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-                __syncthreads();
-                if (lane == 0) warp_key[warp] = best;
-                __syncthreads();
-                for (int w = 0; w < LP_WARPS; ++w) best = max(best, warp_key[w]);
-                if (best == 0) break;
-                if (tid == 0) part.key[r] = best;
+                if constexpr (NW > 1) {
+                    __syncthreads();
+                    if (lane == 0) sm.warp_key[warp] = best;
+                    __syncthreads();
+                    for (int w = 0; w < NW; ++w) best = max(best, sm.warp_key[w]);
+                }
+                if (tid == 0) part.key[r] = best;   // (0: no more of them)
                 last = best;
             }
-            if (tid == 0) part.top = r;
         }
     }
-    if (tid == 0) { part.sum = t; part.zmax = zmax; }
-    __syncthreads();
+    if (NW > 1 && tid == 0) { part.sum = t; part.zmax = zmax; }
+    team_sync<NW>();
 
     // ---- the row's sums, from the cluster's parts in their order
     const uint32_t base = smem_u32(&part);
-    auto word = [&](int r, const void* p) {
-        return ld_cluster_u32(mapa_shared(base, (uint32_t)r) + (uint32_t)(static_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(&part)));
+    auto remote = [&](int r, const void* p) {
+        return mapa_shared(base, (uint32_t)r) + (uint32_t)(static_cast<const uint8_t*>(p) - reinterpret_cast<const uint8_t*>(&part));
     };
     auto join_all = [&] {
-        if (C == 1) return;
+        if (NW == 1 || C == 1) return;
         cluster_sync();
-        #pragma unroll 1
-        for (int r = 0; r < C; ++r) {
-            LpSums o{__uint_as_float(word(r, &part.sum.m)), __uint_as_float(word(r, &part.sum.s)), __uint_as_float(word(r, &part.sum.w))};
-            const float oz = __uint_as_float(word(r, &part.zmax));
-            if (r == 0) { t = o; zmax = oz; }
-            else { t.join(o); zmax = fmaxf(zmax, oz); }
+        t = LpSums{-LP_FAR, 0.f, 0.f};
+        zmax = -INFINITY;
+        if (lane < C) {
+            t.m = __uint_as_float(ld_cluster_u32(remote(lane, &part.sum.m)));
+            t.s = __uint_as_float(ld_cluster_u32(remote(lane, &part.sum.s)));
+            t.w = __uint_as_float(ld_cluster_u32(remote(lane, &part.sum.w)));
+            zmax = __uint_as_float(ld_cluster_u32(remote(lane, &part.zmax)));
         }
+        lp_join_lanes<LP_MAX_CLUSTER>(t, zmax);
     };
     join_all();
     // A row whose largest logit has no such reference: differences first, then products.
     const bool far = fabsf(zmax) < INFINITY && !(fabsf(zmax * a.c) < LP_FAR);
     if (far) {
-        if (C > 1) cluster_sync();   // the parts have been read
+        if (NW > 1 && C > 1) cluster_sync();   // the parts have been read
         t = LpSums{0.f, 0.f, 0.f};
         #pragma unroll 1
-        for (int v = v0 + tid; v < v1; v += LP_THREADS) {
+        for (int v = v0 + tid; v < v1; v += THREADS) {
             float z[EPV];
             load(v, z);
             #pragma unroll
@@ -331,13 +443,15 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
         }
         t.s = warp_sum(t.s);
         t.w = warp_sum(t.w);
-        __syncthreads();
-        if (lane == 0) red[warp] = t;
-        __syncthreads();
-        t = red[0];
-        for (int w = 1; w < LP_WARPS; ++w) { t.s += red[w].s; t.w += red[w].w; }
-        if (tid == 0) part.sum = t;
-        __syncthreads();
+        if constexpr (NW > 1) {
+            __syncthreads();
+            if (lane == 0) sm.red[warp] = t;
+            __syncthreads();
+            t = sm.red[0];
+            for (int w = 1; w < NW; ++w) { t.s += sm.red[w].s; t.w += sm.red[w].w; }
+            if (tid == 0) part.sum = t;
+            __syncthreads();
+        }
         join_all();
     }
 
@@ -349,14 +463,12 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
             if (z == -INFINITY) return t.s != t.s ? t.s : -INFINITY;
             return (float)(((double)z * a.c - ref - ls) * 0.69314718055994531);   // (a product may pass fp32's range)
         };
-        if (tid < a.M) {
-            #pragma unroll 1
-            for (int i = tid; i < a.M; i += LP_THREADS) {
-                const int64_t at = row * a.M + i;
-                const int id = a.ids[at];
-                if (DFL_IN_BOUNDS(err.word, at, a.rows * a.M))
-                    a.logp[at] = id >= 0 && id < a.V ? logp(Vec::one(z0 + id)) : -INFINITY;
-            }
+        #pragma unroll 1
+        for (int i = tid; i < a.M; i += THREADS) {
+            const int64_t at = row * a.M + i;
+            const int id = a.ids[at];
+            if (DFL_IN_BOUNDS(err.word, at, a.rows * a.M))
+                a.logp[at] = id >= 0 && id < a.V ? logp(Vec::one(z0 + id)) : -INFINITY;
         }
         if (tid == 0 && a.entropy && DFL_IN_BOUNDS(err.word, row, a.rows)) a.entropy[row] = (ls - t.w / t.s) * LN2;
         if constexpr (TOP) {
@@ -366,41 +478,46 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
                 a.top_ids[at] = key ? (int)lp_key_index(key) : -1;
                 a.top_logp[at] = key ? logp(lp_key_value(key)) : -INFINITY;
             };
-            if (C == 1) {
-                if (tid < a.K) put(tid, tid < part.top ? part.key[tid] : 0);
-            } else {   // ranks among the parts' best: at most 8 * 64
-                int all = 0;
+            if (NW == 1 || C == 1) {
                 #pragma unroll 1
-                for (int r = 0; r < C; ++r) {
-                    const int n = (int)word(r, &part.top);
-                    #pragma unroll 1
-                    for (int i = tid; i < n; i += LP_THREADS) cand[all + i] = ld_cluster_u64(mapa_shared(base, (uint32_t)r) +
-                        (uint32_t)(reinterpret_cast<const uint8_t*>(&part.key[i]) - reinterpret_cast<const uint8_t*>(&part)));
-                    all += n;
+                for (int r = tid; r < a.K; r += THREADS) put(r, part.key[r]);
+            } else if constexpr (NW > 1) {   // ranks among the parts' best: at most 8 * 64
+                const int all = C * a.K;
+                #pragma unroll 1
+                for (int i = tid; i < all; i += THREADS) sm.cand[i] = ld_cluster_u64(remote(i / a.K, &part.key[i % a.K]));
+                if (tid == 0) sm.n_cand = 0;
+                __syncthreads();
+                #pragma unroll 1
+                for (int c = tid; c < all; c += THREADS) {
+                    const uint64_t key = sm.cand[c];
+                    if (key == 0) continue;
+                    atomicAdd(&sm.n_cand, 1);
+                    int r = 0;
+                    #pragma unroll 4
+                    for (int j = 0; j < all; ++j) r += sm.cand[j] > key;
+                    if (r < a.K) put(r, key);
                 }
                 __syncthreads();
                 #pragma unroll 1
-                for (int c = tid; c < all; c += LP_THREADS) {
-                    const uint64_t key = cand[c];
-                    int r = 0;
-                    #pragma unroll 1
-                    for (int j = 0; j < all; ++j) r += cand[j] > key;
-                    if (r < a.K) put(r, key);
-                }
-                if (tid >= all && tid < a.K) put(tid, 0);
+                for (int r = sm.n_cand + tid; r < a.K; r += THREADS) put(r, 0);
             }
         }
     }
-    if (C > 1) cluster_sync();   // the parts stay until the first CTA has read them
+    if (NW > 1 && C > 1) cluster_sync();   // the parts stay until the first CTA has read them
 }
 
-constexpr int LP_SMS = 152, LP_PER_SM = 4, LP_MAX_CLUSTER = 8;
+constexpr int LP_SMS = 152, LP_PER_SM = 4;
 
 // CTAs of a row: enough to fill the SMs, with some 16 KB of the row for each.
 int lp_cluster(int64_t rows, int64_t row_bytes) {
     int C = 1;
     while (C < LP_MAX_CLUSTER && rows * C * 2 <= LP_SMS * LP_PER_SM && row_bytes / (2 * C) >= 16384) C *= 2;
     return C;
+}
+
+// A warp to a row where rows are short and many.
+bool lp_warp_rows(int64_t rows, int64_t row_bytes, int K) {
+    return row_bytes <= 16384 && rows > LP_SMS * LP_PER_SM && K <= 32;
 }
 
 template <typename K>
@@ -410,13 +527,13 @@ dfl_status launch_cluster(K kern, unsigned grid, int C, cudaStream_t st, const L
     cfg.blockDim = dim3(LP_THREADS);
     cfg.stream = st;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = pdl_on() ? 2 : 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)C;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = pdl_on() ? at : at + 1;
+    cfg.numAttrs = (pdl_on() ? 1 : 0) + (C > 1 ? 1 : 0);
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, C, err));
 }
 
@@ -424,14 +541,19 @@ dfl_status launch_cluster(K kern, unsigned grid, int C, cudaStream_t st, const L
 
 dfl_status token_logprobs_run(DeviceCtx* ctx, const LpArgs& a, int dt, cudaStream_t st) {
     ProfScope ps("token_logprobs", st);
-    const int C = lp_cluster(a.rows, (int64_t)a.V * (dt == DFL_BF16 ? 2 : 4));
+    const int64_t row_bytes = (int64_t)a.V * (dt == DFL_BF16 ? 2 : 4);
+    const bool warp = lp_warp_rows(a.rows, row_bytes, a.K);
+    const int C = warp ? 1 : lp_cluster(a.rows, row_bytes);
     const DevErr err = dev_err(ctx);
-    const unsigned grid = (unsigned)(a.rows * C);
-    if (dt == DFL_BF16)
-        return a.K > 0 ? launch_cluster(token_logprobs_kernel<__nv_bfloat16, true>, grid, C, st, a, err)
-                       : launch_cluster(token_logprobs_kernel<__nv_bfloat16, false>, grid, C, st, a, err);
-    return a.K > 0 ? launch_cluster(token_logprobs_kernel<float, true>, grid, C, st, a, err)
-                   : launch_cluster(token_logprobs_kernel<float, false>, grid, C, st, a, err);
+    const unsigned grid = (unsigned)(warp ? (a.rows + LP_WARPS - 1) / LP_WARPS : a.rows * C);
+    auto run = [&](auto type, auto top) -> dfl_status {
+        using T = decltype(type);
+        constexpr bool TOP = decltype(top)::value;
+        return warp ? launch_cluster(token_logprobs_kernel<T, TOP, 1>, grid, C, st, a, err)
+                    : launch_cluster(token_logprobs_kernel<T, TOP, LP_WARPS>, grid, C, st, a, err);
+    };
+    if (dt == DFL_BF16) return a.K > 0 ? run(__nv_bfloat16{}, std::true_type{}) : run(__nv_bfloat16{}, std::false_type{});
+    return a.K > 0 ? run(float{}, std::true_type{}) : run(float{}, std::false_type{});
 }
 
 }  // namespace dfl
