@@ -20,14 +20,11 @@ from . import _lib
 from ._lib import Kv4Pool, Pages
 
 
-def alloc_on(index, stream, f, *args, **kw):
-    """f(*args, **kw) with its memory from the stream (None: the current one) that a call launches on."""
-    if stream is None:
-        return f(*args, **kw)
+def on_stream(index, stream):
+    """The context in which memory comes from the stream that a call launches on (a Stream or a handle)."""
     if isinstance(stream, int):   # (ExternalStream takes no null handle)
         stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
-    with torch.cuda.stream(stream):
-        return f(*args, **kw)
+    return torch.cuda.stream(stream)
 
 
 class PagedCache:
@@ -82,7 +79,10 @@ class PagedCache:
 
     def _alloc(self, stream, f, *args, **kw):
         """f(*args, **kw) with its memory from the stream that the call launches on."""
-        return alloc_on(self._index, stream, f, *args, **kw)
+        if stream is None:
+            return f(*args, **kw)
+        with on_stream(self._index, stream):
+            return f(*args, **kw)
 
     def _i32(self, x, what):
         if x.dtype is not torch.int32 or not x.is_contiguous() or x.get_device() != self._index or x.numel() != self.N:

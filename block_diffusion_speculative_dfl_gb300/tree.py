@@ -10,13 +10,16 @@ captured into CUDA graphs.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
 from ._lib import DFL_BF16, DFL_F32
-from .paged import alloc_on
+from .paged import on_stream
+
+_DTYPES = {torch.bfloat16: DFL_BF16, torch.float32: DFL_F32}
 
 
 class TokenLogprobs(NamedTuple):
@@ -38,6 +41,23 @@ def _handle(index, stream):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else _lib._stream(stream)
 
 
+def _row_stride(logits, rows):
+    """Elements between the rows of logits, which are contiguous and lie at one stride."""
+    V, stride, step = logits.shape[-1], None, 1
+    for size, s in zip(reversed(logits.shape[:-1]), reversed(logits.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif s != step * stride:
+            raise ValueError("the rows of logits must lie at one stride")
+        step *= size
+    stride = V if stride is None else stride
+    if (V > 1 and logits.stride(-1) != 1) or (rows > 1 and stride < V):
+        raise ValueError("a row of logits must be contiguous and the rows apart")
+    return stride
+
+
 def token_logprobs(logits, ids=None, top=0, T=1.0, entropy=True, stream=None) -> TokenLogprobs:
     """Log probabilities of ``softmax(logits / T)``: of given tokens, its entropy, its ``top`` largest.
 
@@ -47,51 +67,40 @@ def token_logprobs(logits, ids=None, top=0, T=1.0, entropy=True, stream=None) ->
     lowest id, -1 and -inf where a row has fewer tokens above -inf.  The outputs are allocated on the stream of the
     call.
     """
-    index = _index(logits, "logits")
-    if logits.dtype is torch.bfloat16:
-        dt = DFL_BF16
-    elif logits.dtype is torch.float32:
-        dt = DFL_F32
-    else:
+    index = logits.get_device()
+    if index < 0 or index != torch.cuda.current_device():
+        _index(logits, "logits")
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
         raise ValueError(f"logits must be bf16 or fp32, not {logits.dtype}")
-    if logits.dim() < 1 or logits.shape[-1] < 1:
+    shape = logits.shape
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("logits must have at least one token")
-    lead, V = logits.shape[:-1], logits.shape[-1]
+    lead, V = shape[:-1], shape[-1]
     rows = lead.numel()
-    # the rows' common stride
-    stride = V
-    step, known = 1, False
-    for size, s in zip(reversed(lead), reversed(logits.stride()[:-1])):
-        if size == 1:
-            continue
-        if not known:
-            stride, known = s, True
-        elif s != step * stride:
-            raise ValueError("the rows of logits must lie at one stride")
-        step *= size
-    if (V > 1 and logits.stride(-1) != 1) or (rows > 1 and stride < V):
-        raise ValueError("a row of logits must be contiguous and the rows apart")
+    stride = V if logits.is_contiguous() else _row_stride(logits, rows)
     M = 0
     if ids is not None:
         if ids.dtype is not torch.int32 or not ids.is_contiguous() or ids.get_device() != index or ids.shape[:-1] != lead or \
-                ids.dim() != logits.dim():
+                ids.dim() != len(shape):
             raise ValueError(f"ids must be a contiguous int32 tensor {list(lead)} + [tokens] on {logits.device}")
         M = ids.shape[-1]
-    top = int(top)
     if not 0 <= top <= 64:
         raise ValueError(f"top={top} outside 0..64")
-
-    def new(shape, dtype):
-        return alloc_on(index, stream, torch.empty, shape, dtype=dtype, device=logits.device)
-
-    out = TokenLogprobs(new((*lead, M), torch.float32) if ids is not None else None,
-                        new(lead, torch.float32) if entropy else None,
-                        new((*lead, top), torch.int32), new((*lead, top), torch.float32))
-    if rows == 0 or (M == 0 and not top and not entropy):
-        return out
-    _lib.dfl_token_logprobs(logits, dt, rows, V, stride, float(T), ids if M else None, M, out.logp if M else None, out.entropy,
-                            top, out.top_ids if top else None, out.top_logp if top else None, _handle(index, stream))
-    return out
+    with contextlib.nullcontext() if stream is None else on_stream(index, stream):
+        dev, f32 = logits.device, torch.float32
+        logp = torch.empty((*lead, M), dtype=f32, device=dev) if ids is not None else None
+        H = torch.empty(lead, dtype=f32, device=dev) if entropy else None
+        top_ids = torch.empty((*lead, top), dtype=torch.int32, device=dev)
+        top_logp = torch.empty((*lead, top), dtype=f32, device=dev)
+    if rows and (M or top or entropy):
+        rc = _lib.load().dfl_token_logprobs(logits.data_ptr(), dt, rows, V, stride, T, ids.data_ptr() if M else None, M,
+                                            logp.data_ptr() if M else None, H.data_ptr() if entropy else None, top,
+                                            top_ids.data_ptr() if top else None, top_logp.data_ptr() if top else None,
+                                            _handle(index, stream))
+        if rc:
+            _lib._check("dfl_token_logprobs", rc)
+    return TokenLogprobs(logp, H, top_ids, top_logp)
 
 
 class DraftTree:

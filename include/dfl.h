@@ -814,9 +814,10 @@ dfl_status dfl_token_logprobs(const void* logits, int32_t dt, int64_t rows, int3
  *   target decides acceptance": the positions' marginals are independent given
  *   the context, so a path has the product of its tokens' probabilities.
  *   A row of depth g (the anchor: 0) has the K alternatives of position g as
- *   children, each with the score: row's score + logp (fp64; the anchor's is 0).  Rows
+ *   children, each with the score: row's score + logp (64-bit sums in units of
+ *   2^-44; the anchor's is 0; beyond 1,024 in magnitude a logp counts as that).  Rows
  *   are added best first, an alternative after its better ranks; ties go to the
- *   lowest parent.  -inf and NaN are no alternatives, nor are those behind them.
+ *   lowest parent.  Infinities and NaN are no alternatives, nor are those behind them.
  *   anchor    in, int32 [N]
  *   top_ids, top_logp   in, [N][G][K], best first (as dfl_token_logprobs gives them)
  *   token, parent, depth   out, int32 [N][B]; mask out, uint64 [N][B]
