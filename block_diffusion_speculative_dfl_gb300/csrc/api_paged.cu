@@ -98,7 +98,7 @@ dfl_status attn_call(const dfl_kv4_pool* pool, int layer, const dfl_pages* pages
     dfl_status rc = kv4_check(pool, layer, pages);
     if (rc != DFL_OK) return rc;
     if (Hq % pool->Hkv != 0) return DFL_ERR_INVALID_ARG;
-    if ((rc = kv4_attn_check(*pool, *pages, B, Hq)) != DFL_OK) return rc;
+    if ((rc = kv4_attn_check(*pool, *pages, B, Hq, mask || window > 0)) != DFL_OK) return rc;
     const void* ptrs[] = {Q, Kb, Vb, O, ws};
     for (const void* p : ptrs) if (!aligned16(p)) return DFL_ERR_MISALIGNED;
     if (reinterpret_cast<uintptr_t>(mask) & 7u) return DFL_ERR_MISALIGNED;

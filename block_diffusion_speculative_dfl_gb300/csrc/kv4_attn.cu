@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
             // first token behind the sinks that this lane's row r of tile nt sees
             auto first = [&](int nt, int r) {
                 const int q = row0 + nt * 8 + 2 * t + r;
-                return q < a.R ? ka_first(a, pos.len, ka_depth(a, pos.n, ka_block_row(a, q))) : 0;
+                const int b = ka_block_row(a, q);
+                return q < a.R ? ka_first(a, pos.len, ka_depth(a, ka_row_bits(a, pos.n, b), b)) : 0;
             };
             if constexpr (MASK)
                 if (edge) {
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int q = row0 + nt * 8 + 2 * t + r;
-                        sees[nt][r] = q < a.R ? ka_own_sees(a, pos.n, ka_block_row(a, q), pos.len) >> (warp * KV4_CELL_TOKENS) : 0;
+                        sees[nt][r] = q < a.R ? ka_sees(a, pos.n, ka_block_row(a, q), pos.len).own >> (warp * KV4_CELL_TOKENS) : 0;
                     }
             }
             #pragma unroll
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                 if (whole) {
                     float inv = __fdividef(a.v_pow2, L);
                     if constexpr (MASK)
-                        if (ka_blank(a, pos.n, ka_block_row(a, r), pos.len)) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
+                        if (ka_sees(a, pos.n, ka_block_row(a, r), pos.len).first == KA_BLANK) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
                     const int64_t at = ka_row(a, pos.n, head, r, HD) + c;
                     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
                         *reinterpret_cast<uint2*>(a.O + at) =
@@ -654,22 +655,22 @@ int ka_grid(int64_t units) { return (int)std::min<int64_t>(units, KA_SMS); }
 int ka_rows(int R) { return R > KA_MAX_ROWS ? kv4_attn_tc_rows(R) : 8 * ka_nt(R); }
 int ka_subs(int R) { return (R + ka_rows(R) - 1) / ka_rows(R); }
 int ka_unit_log2(int R, int hd) { return R > KA_MAX_ROWS ? kv4_attn_tc_unit_log2(R, hd) : 6; }   // KA_UNIT
-int ka_weight(int R) { return R > KA_MAX_ROWS ? kv4_attn_tc_weight() : KA_WEIGHT; }
-int64_t ka_most_units(const dfl_kv4_pool& pool, const dfl_pages& pg, int R) {
-    return ((int64_t)pg.max_pages * pool.page >> ka_unit_log2(R, pool.hd)) + 2 + ka_weight(R);
+int ka_weight(int R, bool masked) { return R > KA_MAX_ROWS ? kv4_attn_tc_weight(masked) : KA_WEIGHT; }
+int64_t ka_most_units(const dfl_kv4_pool& pool, const dfl_pages& pg, int R, bool masked) {
+    return ((int64_t)pg.max_pages * pool.page >> ka_unit_log2(R, pool.hd)) + 2 + ka_weight(R, masked);
 }
 
 inline size_t al256(size_t b) { return (b + 255) & ~size_t(255); }
 
 }  // namespace
 
-dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq) {
+dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq, bool masked) {
     const int G = Hq / pool.Hkv;
     if (B > 64 || (int64_t)B * G > KV4_MAX_HEAD_ROWS || !rows_fit((int64_t)pg.N * B)) return DFL_ERR_UNSUPPORTED_SHAPE;
     if ((int64_t)pg.max_pages * pool.page > KV4_ATTN_TOKENS) return DFL_ERR_UNSUPPORTED_SHAPE;
     const int R = B * G;
     const int64_t triples = (int64_t)pool.Hkv * ka_subs(R) * pg.N;
-    if (triples >= (int64_t)1 << 31 || triples * ka_most_units(pool, pg, R) >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
+    if (triples >= (int64_t)1 << 31 || triples * ka_most_units(pool, pg, R, masked) >= (int64_t)1 << 31) return DFL_ERR_UNSUPPORTED_SHAPE;
     return DFL_OK;
 }
 
@@ -704,11 +705,11 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
     a.k_pow2 = kv4_exp2i(pool.k_exp); a.k_inv = kv4_exp2i(-pool.k_exp);
     a.v_pow2 = kv4_exp2i(pool.v_exp); a.v_inv = kv4_exp2i(-pool.v_exp);
     a.unit_log2 = ka_unit_log2(R, pool.hd);
-    a.weight = ka_weight(R);
+    const bool masked = mask || window > 0;
+    a.weight = ka_weight(R, masked);
     a.seam = tc ? kv4_attn_tc_seam() : KA_SEAM;
     static_assert(KA_UNIT == 64, "unit_log2");
-    const int64_t units = ka_most_units(pool, pg, R) * pg.N * a.HS;   // < 2^31: kv4_attn_check
-    const bool masked = mask || window > 0;
+    const int64_t units = ka_most_units(pool, pg, R, masked) * pg.N * a.HS;   // < 2^31: kv4_attn_check
     a.mask = mask; a.window = window; a.sinks = sinks;
     if (tc) return kv4_attn_tc_run(ctx, a, pool.hd, units, ws, masked, st);
     const size_t parts = 2 * (size_t)KA_SMS * ka_groups(pool.hd, nt) * rows;

@@ -44,7 +44,7 @@ struct KaArgs {
 inline int kv4_attn_tc_rows(int R) { return R <= 64 ? 64 : 128; }
 int kv4_attn_tc_unit_log2(int R, int hd);
 int kv4_attn_tc_seam();
-int kv4_attn_tc_weight();
+int kv4_attn_tc_weight(bool masked);
 size_t kv4_attn_tc_ws_bytes(int R, int hd);
 dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void* ws, bool masked, cudaStream_t st);
 
@@ -167,31 +167,32 @@ __device__ __forceinline__ uint64_t ka_row_bits(const KaArgs& a, int n, int b) {
     const uint64_t all = ~0ull >> (64 - a.B);
     return a.mask ? a.mask[(int64_t)n * a.B + b] & all : all;
 }
-__device__ __forceinline__ int ka_depth(const KaArgs& a, int n, int b) {
-    return a.mask ? max(__popcll(ka_row_bits(a, n, b)) - 1, 0) : b;
-}
-// First token behind the sinks that a row of this depth sees.
+__device__ __forceinline__ int ka_depth(const KaArgs& a, uint64_t bits, int b) { return a.mask ? max(__popcll(bits) - 1, 0) : b; }
+
+// What block row b sees: own rows as bits, and of the cached tokens the sinks and those from `first` on.  A row that sees
+// nothing, whose output is 0, has `first` = KA_BLANK.
+constexpr int KA_BLANK = 0x7FFFFFFF;
+struct KaSees {
+    uint64_t own;
+    int first;
+};
 __device__ __forceinline__ int ka_first(const KaArgs& a, int len, int depth) { return a.window > 0 ? len + depth - a.window + 1 : 0; }
-// The own rows that block row b sees.
-__device__ __forceinline__ uint64_t ka_own_sees(const KaArgs& a, int n, int b, int len) {
-    uint64_t bits = ka_row_bits(a, n, b);
-    const int d = ka_depth(a, n, b);
-    if (a.window > 0 && d >= a.window) {   // rows above it fall out of the window
-        uint64_t left = bits;
+__device__ __forceinline__ KaSees ka_sees(const KaArgs& a, int n, int b, int len) {
+    KaSees s{ka_row_bits(a, n, b), 0};
+    const int d = ka_depth(a, s.own, b);
+    s.first = ka_first(a, len, d);
+    if (s.own == 0) s.first = KA_BLANK;
+    else if (a.window > 0 && (d >= a.window || s.first >= len)) {   // rows above it fall out of the window, or all tokens do
+        uint64_t left = s.own;
         #pragma unroll 1
         while (left) {
-            const int j = __ffsll((long long)left) - 1, dj = ka_depth(a, n, j);
+            const int j = __ffsll((long long)left) - 1, dj = ka_depth(a, ka_row_bits(a, n, j), j);
             left &= left - 1;
-            if (d - dj >= a.window && len + dj >= a.sinks) bits &= ~(1ull << j);
+            if (d - dj >= a.window && len + dj >= a.sinks) s.own &= ~(1ull << j);
         }
+        if (s.own == 0 && s.first >= len && (len == 0 || a.sinks == 0)) s.first = KA_BLANK;
     }
-    return bits;
-}
-// Whether block row b sees nothing: its output is 0.
-__device__ __forceinline__ bool ka_blank(const KaArgs& a, int n, int b, int len) {
-    if (ka_row_bits(a, n, b) == 0) return true;
-    if (len > 0 && (a.sinks > 0 || ka_first(a, len, ka_depth(a, n, b)) < len)) return false;
-    return ka_own_sees(a, n, b, len) == 0;
+    return s;
 }
 // Whether some row may not see one of the tokens k .. k + count - 1 (no row is deeper than B - 1).
 __device__ __forceinline__ bool ka_edge(const KaArgs& a, int len, int k, int count) {
@@ -266,6 +267,9 @@ __device__ __forceinline__ KaLine ka_locate(const KaArgs& a, int ranges, KaLineS
     longest = (threadIdx.x & 31) < THREADS / 32 ? sm.longest[threadIdx.x & 31] : 0;
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     l.whole = (int64_t)a.N * a.HS <= ranges && longest <= l.per + a.seam;
+    // Few triples leave most ranges without work: one sequence of 517 tokens, 64 rows to a head, takes 20 us as 8 whole triples
+    // and 13 cut into 48 units; 16 of 900 28.5 as 128 whole ones and 31.3 cut.
+    if (MASK) l.whole = l.whole && (int64_t)a.N * a.HS * 4 > ranges;
     if (l.whole) return l;
     #pragma unroll 1
     for (int i = 0; i < P; ++i) {
@@ -359,6 +363,7 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
     const int first = blockIdx.x, last = t.last, row0 = t.tile * ROWS;
     const int row = blockIdx.y * KjCfg<HD, ROWS>::AT_ONCE + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;
     if (row >= ROWS || r >= a.R) return;
+    const bool blank = MASK && ka_sees(a, t.n, ka_block_row(a, r), ka_len(a, t.n)).first == KA_BLANK;
     // eight partials are read at once: a long triple waits for memory once per eight
     constexpr int BATCH = 8;
     float M = KA_NONE, L = 0.f;
@@ -389,8 +394,7 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
         }
     }
     float inv = __fdividef(a.v_pow2, L);
-    if constexpr (MASK)
-        if (ka_blank(a, t.n, ka_block_row(a, r), ka_len(a, t.n))) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
+    if (MASK && blank) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
     const int64_t at = ka_row(a, t.n, t.head, r, HD) + c;
     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
         *reinterpret_cast<uint2*>(a.O + at) =

@@ -505,33 +505,50 @@ __device__ __noinline__ uint64_t kt_edge_nans(const KaArgs& a, const DevErr& err
     return nans;
 }
 
-// What weights times infinite and NaN values come to, for a row's dims c .. c + 31:
-// of the own rows `bad` and the tokens `nans` from k0 on, which the row sees and
-// whose tiles hold 0 in their place.
+// After a row's dims c .. c + 31 have been stored at `out` (bf16) or `part` (fp32): what weights times infinite and NaN values
+// come to, of the own rows `bad` and the tokens `nans` from k0 on, which the row sees and whose tiles hold 0 in their place.
+// (On the stored row: a function that took it in registers kept all rows in local memory, 2 us a triple.)
 template <int HD>
-__device__ __noinline__ void kt_add_unfinite(const KaArgs& a, const DevErr& err, int n, int head, uint64_t bad, uint64_t nans, int k0,
-                                             int c, float (&o)[32]) {
+__device__ __noinline__ void kt_mend(const KaArgs& a, const DevErr& err, int n, int head, uint64_t bad, uint64_t nans, int k0, int c,
+                                     __nv_bfloat16* out, float* part) {
     using Cell = Kv4Cell<HD>;
     #pragma unroll 1
-    for (; bad; bad &= bad - 1) {
-        const __nv_bfloat16* v = a.Vb + ((int64_t)(n * a.B + __ffsll((long long)bad) - 1) * a.slab.Hkv + head) * HD + c;
-        #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float x = __bfloat162float(v[j]);
-            if (!(fabsf(x) < INFINITY)) o[j] += x;
+    for (int j = 0; j < 32; ++j) {
+        float x = 0.f;   // what is not finite of dim c + j
+        #pragma unroll 1
+        for (uint64_t b = bad; b; b &= b - 1) {
+            const float v = __bfloat162float(a.Vb[((int64_t)(n * a.B + __ffsll((long long)b) - 1) * a.slab.Hkv + head) * HD + c + j]);
+            if (!(fabsf(v) < INFINITY)) x += v;
         }
+        #pragma unroll 1
+        for (uint64_t b = nans; b; b &= b - 1) {
+            const int k = k0 + __ffsll((long long)b) - 1;
+            const uint8_t* cell = a.slab.data + (int64_t)ka_cell(a, n, head, k & ~(KV4_CELL_TOKENS - 1), err) * Cell::BYTES;
+            if ((cell[Cell::v_scale(k & (KV4_CELL_TOKENS - 1), (c + j) / 16)] & 0x7F) == 0x7F) x = __int_as_float(0x7FFFFFFF);
+        }
+        if (x == 0.f) continue;
+        if (out) out[j] = __float2bfloat16(x);
+        else part[j] = x;
     }
+}
+
+// Scores of a thread's keys that are not among the bits see0, see1 become -inf.  (Out of line: the units' loop barely fits the
+// instruction cache.)
+template <bool HALF, int KPT>
+__device__ __noinline__ void kt_hide(uint32_t s_at, uint64_t see0, uint64_t see1) {
     #pragma unroll 1
-    for (; nans; nans &= nans - 1) {
-        const int k = k0 + __ffsll((long long)nans) - 1;
-        const uint8_t* cell = a.slab.data + (int64_t)ka_cell(a, n, head, k & ~(KV4_CELL_TOKENS - 1), err) * Cell::BYTES;
+    for (int k0 = 0; k0 < KPT; k0 += 16) {
+        const uint32_t bits = (uint32_t)((k0 < 64 ? see0 : see1) >> (k0 & 63));
+        float s[16];
+        if constexpr (HALF) tmem_ld16_hx2<KPT>(s_at + k0, s);
+        else tmem_ld16(s_at + k0, s);
+        uint32_t v[16];
         #pragma unroll
-        for (int g = 0; g < 2; ++g)
-            if ((cell[Cell::v_scale(k & (KV4_CELL_TOKENS - 1), c / 16 + g)] & 0x7F) == 0x7F) {
-                #pragma unroll
-                for (int j = 0; j < 16; ++j) o[16 * g + j] = __int_as_float(0x7FFFFFFF);
-            }
+        for (int j = 0; j < 16; ++j) v[j] = bits >> j & 1 ? __float_as_uint(s[j]) : 0xFF800000u;
+        if constexpr (HALF) tmem_st16u_hx2<KPT>(s_at + k0, v);
+        else tmem_st16(s_at + k0, v);
     }
+    tmem_st_wait();
 }
 
 // Bits 0 .. n - 1.
@@ -668,6 +685,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             const int head = pos.head, row0 = pos.tile * MM;
             const int u0 = pos.u, u1 = min(pos.nu, u0 + (x1 - x));
             const bool pad = row0 + RPW * q4 >= a.R;   // the warp holds no row of the block
+            KaSees sees{0, 0};
+            if (MASK && row0 + row < a.R) sees = ka_sees(a, pos.n, ka_block_row(a, row0 + row), pos.len);
             // the products that read the previous Q have ended: their S has been read
             kt_load_q<HD, MM, RPW>(a, pos.n, head, row0, RPW * q4, smem_u32(sQ), q_up[pipe], lane);
             fence_proxy_async_smem();
@@ -678,9 +697,8 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             uint64_t nans = 0;   // tokens from nan0 on that some row does not see, with NaN among their values
             const int nan0 = MASK && a.window > 0 ? max(max(ka_first(a, pos.len, 0), a.sinks), 0) : 0;
             if constexpr (MASK) {   // read again by the thread that writes it
-                const int r = row0 + row;
-                row_sees[pipe][row] = r < a.R ? ka_own_sees(a, pos.n, ka_block_row(a, r), pos.len) : 0;
-                row_first[pipe][row] = r < a.R ? ka_first(a, pos.len, ka_depth(a, pos.n, ka_block_row(a, r))) : 0;
+                row_sees[pipe][row] = sees.own;
+                row_first[pipe][row] = sees.first;
                 if (a.window > 0 && u0 == 0) nans = kt_edge_nans<HD>(a, err, pos.n, head, nan0, min(pos.len, pos.len + a.B - a.window), lane);
             }
             if (x + u1 - u0 < x1) {   // the next triple's Q on its way to L2
@@ -705,7 +723,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                     const bool own = u == pos.nu - 1;
                     const int k0u = pos.token(a, u);
                     const int keys = (own ? a.B : pos.len - k0u) - hh * KPT;   // from this thread's first on
-                    if (MASK && __any_sync(0xFFFFFFFFu, own || keys < KPT || ka_edge(a, pos.len, k0u, KU))) {   // what a row does not see
+                    if (MASK && __builtin_expect(__any_sync(0xFFFFFFFFu, own || keys < KPT || ka_edge(a, pos.len, k0u, KU)), 0)) {   // what a row does not see
                         uint64_t see[2] = {0, 0};   // of this thread's keys
                         if (own) {
                             if (hh * KPT < 64) see[0] = row_sees[pipe][row] >> (hh * KPT);
@@ -714,19 +732,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                             see[0] = kt_ones(keys) & (~kt_ones(lo) | kt_ones(sk));
                             see[1] = kt_ones(keys - 64) & (~kt_ones(lo - 64) | kt_ones(sk - 64));
                         }
-                        #pragma unroll 1
-                        for (int k0 = 0; k0 < KPT; k0 += 16) {
-                            const uint32_t bits = (uint32_t)(see[k0 >> 6] >> (k0 & 63));
-                            float s[16];
-                            if constexpr (HALF) tmem_ld16_hx2<KPT>(s_at + k0, s);
-                            else tmem_ld16(s_at + k0, s);
-                            uint32_t v[16];
-                            #pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = bits >> j & 1 ? __float_as_uint(s[j]) : 0xFF800000u;
-                            if constexpr (HALF) tmem_st16u_hx2<KPT>(s_at + k0, v);
-                            else tmem_st16(s_at + k0, v);
-                        }
-                        tmem_st_wait();
+                        kt_hide<HALF, KPT>(s_at, see[0], see[1]);
                     }
                     if (!MASK && __any_sync(0xFFFFFFFFu, keys < KPT)) {   // a unit's keys past the last: their scores become -inf
                         #pragma unroll 1
@@ -877,11 +883,11 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             const int64_t qrow = real ? ka_row(a, pos.n, head, rr, 1) : 0;
             const int64_t part = ((int64_t)2 * range + (u0 == 0 ? 1 : 0)) * MM + row;
             if constexpr (HALF) l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            float inv = whole ? __fdividef(a.v_pow2, l) : 1.f;
+            const float inv = whole ? __fdividef(a.v_pow2, l) : 1.f;
             bool blank = false;
             uint64_t bad = 0;   // own rows that this one sees, with values that are not finite
             if constexpr (MASK) {
-                blank = real && whole && ka_blank(a, pos.n, ka_block_row(a, rr), pos.len);
+                blank = real && whole && row_first[pipe][row] == KA_BLANK;
                 if (u1 == pos.nu) {
                     constexpr int SHARE = KU / 4;
                     #pragma unroll
@@ -901,29 +907,27 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                 else tmem_ld32(my + Cfg::O_COL + c0, o);
                 if (!real) continue;
                 const int c = hh * OPT + c0;
-                if constexpr (MASK) {
-                    if (bad | nans) kt_add_unfinite<HD>(a, err, pos.n, head, bad, nans, nan0, c, o);
-                    if (blank) {
-                        inv = 0.f;
-                        #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
-                    }
-                }
                 if (whole) {
                     if (!DFL_IN_BOUNDS(err.word, qrow * HD + c + 31, (int64_t)a.N * a.B * a.Hq * HD)) continue;
                     uint4* dst = reinterpret_cast<uint4*>(a.O + qrow * HD + c);
                     #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(pack_bf16(o[8 * j] * inv, o[8 * j + 1] * inv),
-                                            pack_bf16(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
-                                            pack_bf16(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
-                                            pack_bf16(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 v = make_uint4(pack_bf16(o[8 * j] * inv, o[8 * j + 1] * inv),
+                                             pack_bf16(o[8 * j + 2] * inv, o[8 * j + 3] * inv),
+                                             pack_bf16(o[8 * j + 4] * inv, o[8 * j + 5] * inv),
+                                             pack_bf16(o[8 * j + 6] * inv, o[8 * j + 7] * inv));
+                        if (MASK && blank) v = make_uint4(0, 0, 0, 0);
+                        dst[j] = v;
+                    }
                 } else {
                     if (!DFL_IN_BOUNDS(err.word, part * HD + c + 31, (int64_t)2 * ranges * MM * HD)) continue;
                     float4* dst = reinterpret_cast<float4*>(a.Opart + part * HD + c);
                     #pragma unroll
                     for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
+                if (MASK && __builtin_expect((bad | nans) != 0, 0))
+                    kt_mend<HD>(a, err, pos.n, head, bad, nans, nan0, c, whole ? a.O + qrow * HD + c : nullptr,
+                                whole ? nullptr : a.Opart + part * HD + c);
             }
             if (real && !whole && hh == 0 && DFL_IN_BOUNDS(err.word, part, (int64_t)2 * ranges * MM))
                 a.ml[part] = make_float2(m, l);
@@ -956,6 +960,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 // 26.7 and 26.7.  Weights of 1 and 3 give the same times.
 constexpr int KT_SEAM = 8;
 constexpr int KT_WEIGHT = 1;
+constexpr int KT_WEIGHT_MASKED = 6;
 constexpr int KT_SMS = 152;   // SMs of a GB300
 
 int kt_grid(int64_t units) { return (int)std::min<int64_t>(units, KT_SMS); }
@@ -968,7 +973,7 @@ int kv4_attn_tc_unit_log2(int R, int hd) { return kt_unit(hd, kv4_attn_tc_rows(R
 
 int kv4_attn_tc_seam() { return KT_SEAM; }
 
-int kv4_attn_tc_weight() { return KT_WEIGHT; }
+int kv4_attn_tc_weight(bool masked) { return masked ? KT_WEIGHT_MASKED : KT_WEIGHT; }
 
 size_t kv4_attn_tc_ws_bytes(int R, int hd) {
     const size_t rows = (size_t)2 * KT_PIPES * KT_SMS * kv4_attn_tc_rows(R);

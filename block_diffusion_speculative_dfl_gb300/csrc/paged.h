@@ -40,7 +40,7 @@ constexpr int KV4_MAX_HEAD_ROWS = 65536;   // query rows of a K/V head: B * Hq /
 // looked up as much as 32 units of 128 ahead.
 constexpr int64_t KV4_ATTN_TOKENS = ((int64_t)1 << 31) - 8192;
 // kv4_attn_check: the sizes that attention takes beyond kv4_check's.
-dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq);
+dfl_status kv4_attn_check(const dfl_kv4_pool& pool, const dfl_pages& pg, int B, int Hq, bool masked = false);
 size_t kv4_attn_ws_bytes(int N, int B, int Hq, int Hkv, int hd);
 dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, const dfl_pages& pg, const void* Q,
                         const void* Kb, const void* Vb, int B, int Hq, const uint64_t* mask, int window, int sinks, void* O,
