@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(KaCfg<HD, NT>::THREADS, 1) kv4_attn_kernel(con
                     const int b = warp * KV4_CELL_TOKENS + 4 * i + t;
                     const uint4 raw = b < a.B ? *reinterpret_cast<const uint4*>(
                         a.Vb + ((int64_t)(pos.n * a.B + b) * Hkv + head) * HD + g * (HD / 8) + 8 * w) : make_uint4(0, 0, 0, 0);
-                    const uint4 x4 = MASK ? block_half8_finite(raw, a.v_inv, bad) : block_half8(raw, a.v_inv);
+                    const uint4 x4 = MASK ? block_half8_finite(raw, a.v_inv, true, bad) : block_half8(raw, a.v_inv);
                     v[i][0] = x4.x; v[i][1] = x4.y; v[i][2] = x4.z; v[i][3] = x4.w;
                 }
                 #pragma unroll

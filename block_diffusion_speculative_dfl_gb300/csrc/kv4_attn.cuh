@@ -91,9 +91,10 @@ __device__ __forceinline__ uint4 block_half8(const uint4 v, float inv) {
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// The same for values that some rows may not see: infinities and NaN become 0, as
-// a weight of 0 times one of them would be NaN; `bad` says that there were some.
-__device__ __forceinline__ uint4 block_half8_finite(const uint4 v, float inv, bool& bad) {
+// The same for values that some rows may not see: with `finite` infinities and NaN
+// become 0, as a weight of 0 times one of them would be NaN; `bad` says that there
+// were some.
+__device__ __forceinline__ uint4 block_half8_finite(const uint4 v, float inv, bool finite, bool& bad) {
     uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4];
     #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -104,8 +105,11 @@ __device__ __forceinline__ uint4 block_half8_finite(const uint4 v, float inv, bo
         #pragma unroll
         for (int i = 0; i < 4; ++i)
             #pragma unroll
-            for (int s = 0; s < 32; s += 16)
-                if ((w[i] >> s & 0x7F80u) == 0x7F80u) h[i] &= ~(0xFFFFu << s);
+            for (int s = 0; s < 32; s += 16) {
+                const uint32_t x = w[i] >> s & 0xFFFFu;
+                const uint32_t y = finite ? 0u : (x & 0x8000u) | (x & 0x7Fu ? 0x7E00u : 0x7C00u);
+                if ((x & 0x7F80u) == 0x7F80u) h[i] = (h[i] & ~(0xFFFFu << s)) | y << s;
+            }
     }
     return make_uint4(h[0], h[1], h[2], h[3]);
 }

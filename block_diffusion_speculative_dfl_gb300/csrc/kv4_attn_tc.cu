@@ -185,10 +185,22 @@ struct KtExpandK {   // scores of tokens past the length are masked
     }
 };
 
+// Scale bytes of tokens t, t + 4, t + 8, t + 12 of a cell: zeros from token `left` on, as a weight of 0 times whatever is stored
+// there must add nothing, and zeros for the NaN of tokens nan0 .. nan1 - 1.  (Out of line: few units need it.)
+__device__ __noinline__ uint32_t kt_mend_scales(uint32_t w, int t, int left, int nan0, int nan1) {
+    const uint32_t nan = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = 4 * i + t;
+        const uint32_t byte = 0xFFu << 8 * i;
+        if (k >= left || (k >= nan0 && k < nan1 && (nan & byte))) w &= ~byte;
+    }
+    return w;
+}
+
 template <int HD, int KU>
-struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times whatever is stored there must add nothing
-    // (nan0, nan1): of tokens nan0 .. nan1 - 1 NaN becomes 0
-    static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane, int left, int nan0 = 0, int nan1 = 0) {
+struct KtExpandV {
+    static __device__ __forceinline__ void run(uint32_t half, uint32_t tile, int lane, bool mend, int left, int nan0, int nan1) {
         using Cell = Kv4Cell<HD>;
         constexpr int WPR = HD / 8, RPL = 32 / WPR;
         const int pos = lane % WPR, h = lane / WPR;
@@ -203,24 +215,9 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
             #pragma unroll
             for (int i = 0; i < 4; ++i) w[4 * b + i] = lds32(codes + (4 * i + RPL * b) * Cell::ROW);
         }
-        if (left < KV4_CELL_TOKENS) {   // scale bytes of absent tokens
+        if (mend) {
             #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int held = min(max((left - RPL * b - h + 3) >> 2, 0), 4);
-                sw[b] &= held == 4 ? 0xFFFFFFFFu : (1u << 8 * held) - 1;
-            }
-        }
-        if (nan0 < nan1) {
-            #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                uint32_t bytes = __vcmpeq4(sw[b] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = 4 * i + RPL * b + h;
-                    if (tok < nan0 || tok >= nan1) bytes &= ~(0xFFu << 8 * i);
-                }
-                sw[b] &= ~bytes;
-            }
+            for (int b = 0; b < NB; ++b) sw[b] = kt_mend_scales(sw[b], RPL * b + h, left, nan0, nan1);
         }
         #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -239,11 +236,11 @@ struct KtExpandV {   // tokens from `left` on become zeros: a weight of 0 times 
 
 // 16 rows of a tile from bf16 rows of the block (zeros from `left` on), as fp16
 // in units of the pool's power of two, like the cached values.
-// FINITE: infinities and NaN become 0 (block_half8_finite); the rows that have some
-// are returned as bits.
-template <int HD, int KU, bool FINITE = false>
-__device__ __forceinline__ uint32_t kt_block_rows(const __nv_bfloat16* src, int64_t row_stride, uint32_t tile, int lane, int left,
-                                                  float inv) {
+// FINITE, and `finite`: infinities and NaN become 0 (block_half8_finite); the rows
+// that have some are returned as bits.
+template <int HD, int KU, bool FINITE>
+__device__ __noinline__ uint32_t kt_block_rows(const __nv_bfloat16* src, int64_t row_stride, uint32_t tile, int lane, int left,
+                                                  float inv, bool finite) {
     constexpr int WPR = HD / 8, RPL = 32 / WPR, NR = 16 / RPL;
     const int c = lane % WPR, h = lane / WPR;
     const uint32_t at = kt_piece<KU>(tile, h, c);
@@ -263,7 +260,7 @@ __device__ __forceinline__ uint32_t kt_block_rows(const __nv_bfloat16* src, int6
     for (int i = 0; i < NR; ++i) {
         const int r = RPL * i;
         bool bad = false;
-        sts128((at ^ ((r & 7) << 4)) + r * 128, FINITE ? block_half8_finite(v[i], inv, bad) : block_half8(v[i], inv));
+        sts128((at ^ ((r & 7) << 4)) + r * 128, FINITE ? block_half8_finite(v[i], inv, finite, bad) : block_half8(v[i], inv));
         if (FINITE && bad) rows |= 1u << (r + h);
     }
     return FINITE ? __reduce_or_sync(0xFFFFFFFFu, rows) : 0;
@@ -367,6 +364,9 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         for (int i = 0; i < HD; i += 64) { prefetch_l2(a.Kb + at + i); prefetch_l2(a.Vb + at + i); }
     };
     if (x < x1) own_ahead();
+    // the ring is filled once: a turn takes one step at most and copies the next
+    #pragma unroll 1
+    while (feed.issued + 1 < RST && feed.more()) feed.produce();
     #pragma unroll 1
     while (x < x1) {
         const bool own = u == pos.nu - 1;
@@ -374,60 +374,46 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         const int k0 = pos.token(a, u);
         const int left = (own ? a.B : pos.len - k0) - share;   // keys of the unit from this warp's first on
         const bool edge = MASK && !own && ka_edge(a, pos.len, k0 + share, SHARE);
-        auto turn = [&](int half, auto&& expand) {
+        const bool mend = left < SHARE || edge;
+        // The K tile's turn, then the V tile's.  Once each, whatever the unit is: the instruction cache holds one expansion of
+        // each kind and little more (with a loop of its own for units that are not whole, 200 sequences of 10 to 600 tokens took
+        // 214 us, a third of it waiting for instructions).
+        auto turn = [&](auto which) {
+            constexpr int half = decltype(which)::value;
             if (PARTS == 2 || half == 0)
                 if (feed.issued < taken + RST && feed.more()) feed.produce();
-            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && ((PARTS == 1 && half) || kt_wait(&raw_full[r.i], r.ph, err, abort));
+            const bool cell = !own && left > 0;
+            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && (!cell || (PARTS == 1 && half) || kt_wait(&raw_full[r.i], r.ph, err, abort));
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; return; }
             const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
             const uint32_t src = smem_u32(ring) + r.i * NC * PART + (PARTS == 1 ? half * HALF : 0);
-            #pragma unroll
-            for (int j = 0; j < NC; ++j) expand(src + j * PART, t + j * 16 * 128);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
-            if (PARTS == 2 || half) { ++taken; r.step(); }
-        };
-        if (!own && left >= SHARE && feed.issued > taken + 1 && !edge) {
-            turn(0, [&](uint32_t src, uint32_t t) { KtExpandK<HD, KU>::run(src, t, lane); });
-            if (ok) turn(1, [&](uint32_t src, uint32_t t) { KtExpandV<HD, KU>::run(src, t, lane, KV4_CELL_TOKENS); });
-        } else
-        #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {   // K, V
-            if (PARTS == 2 || half == 0)
-                #pragma unroll 1
-                while (feed.issued < taken + RST && feed.more()) feed.produce();
-            const bool cell = !own && left > 0;
-            ok = kt_wait(&t_empty[half][ts.i], ts.ph ^ 1, err, abort) && (!cell || (PARTS == 1 && half) || kt_wait(&raw_full[r.i], r.ph, err, abort));
-            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-            const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
-            const uint32_t src = smem_u32(ring) + r.i * NC * PART + (PARTS == 1 ? half * HALF : 0);
-            uint32_t bad = 0;
-            #pragma unroll 1
-            for (int j = 0; j < NC; ++j) {   // 16 tokens at a time
-                const int lj = left - j * KV4_CELL_TOKENS;
-                if (!own && lj > 0) {
-                    if (MASK && half) {   // NaN of tokens that some row does not see
-                        const int kj = k0 + share + j * KV4_CELL_TOKENS;
-                        KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, lj, edge ? max(a.sinks - kj, 0) : 0,
-                                               edge ? min(pos.len + a.B - a.window - kj, KV4_CELL_TOKENS) : 0);
-                    } else if (half) KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, lj);
-                    else KtExpandK<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane);
-                } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
-                    const int64_t at = ((int64_t)(pos.n * a.B + share + j * 16) * a.slab.Hkv + pos.head) * HD;
-                    if (MASK && half)
-                        bad |= kt_block_rows<HD, KU, true>(a.Vb + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj, a.v_inv) << (16 * j);
+            if (cell) {
+                #pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    const int kj = k0 + share + j * KV4_CELL_TOKENS;
+                    if constexpr (half)
+                        KtExpandV<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane, mend, left - j * KV4_CELL_TOKENS,
+                                               edge ? a.sinks - kj : 0, edge ? pos.len + a.B - a.window - kj : 0);
                     else
-                        kt_block_rows<HD, KU>((half ? a.Vb : a.Kb) + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane, lj,
-                                              half ? a.v_inv : a.k_inv);
+                        KtExpandK<HD, KU>::run(src + j * PART, t + j * 16 * 128, lane);
                 }
+            } else if (own || half) {   // the block's own rows, zeros past B; zero values past the length
+                uint32_t bad = 0;
+                #pragma unroll 1
+                for (int j = 0; j < NC; ++j) {   // 16 tokens at a time
+                    const int64_t at = ((int64_t)(pos.n * a.B + share + j * 16) * a.slab.Hkv + pos.head) * HD;
+                    bad |= kt_block_rows<HD, KU, MASK>((half ? a.Vb : a.Kb) + at, (int64_t)a.slab.Hkv * HD, t + j * 16 * 128, lane,
+                                                       left - j * KV4_CELL_TOKENS, half ? a.v_inv : a.k_inv, half) << (16 * j);
+                }
+                if (MASK && own && half && lane == 0) own_bad[triple & 3][w] = bad;
             }
-            if (MASK && own && half && lane == 0) own_bad[triple & 3][w] = bad;
             fence_proxy_async_smem();
             __syncwarp();   // the slot has been read, the rows are written by every lane
             if (elect_one()) mbar_arrive(&t_full[half][ts.i]);
             if (cell && (PARTS == 2 || half)) { ++taken; r.step(); }
-        }
+        };
+        turn(std::integral_constant<int, 0>{});
+        if (ok) turn(std::integral_constant<int, 1>{});
         if (!ok) break;
         ts.step();
         ++x;
