@@ -3,7 +3,8 @@
 //   O = softmax(Q [Kc; Kb]^T / sqrt(hd)) [Vc; Vb]
 // for the R = B * (Hq / Hkv) query rows that share K/V head h of sequence n:
 // Kc, Vc the len[n] cached tokens of the sequence's pages (4-bit cells, see
-// kv4.cuh), Kb, Vb the block's own B keys in bf16.  No mask.
+// kv4.cuh), Kb, Vb the block's own B keys in bf16.  No mask; or (MASK) rows that see
+// their ancestors in a tree, a window of tokens and the first ones (kv4_attn.cuh).
 //
 // Work.  The keys of a sequence are cut into units of 64: ceil(len / 64)
 // context units and one unit of the block's own keys.  All units of all
@@ -33,6 +34,13 @@
 // 370 warp instructions, 192 of them the conversions, scales and products; the
 // schedulers issue in 66 % of the clocks, waiting for dependent results and for
 // the conversion pipe.  More warps do not fit (five groups spill: 130 us).
+//
+// Masked.  Units that hold no token some row sees are not on the line, so a window
+// costs its own tokens (48 single tokens through a window of 128 with 4 sinks over 65
+// to 16,000 tokens 9.8 us, 64 query heads of 64: five dependent units, latency).  Scores
+// that a row does not see become -inf, in the own rows and in the cells at a window's
+// edge alone; their weights are 0, and what is not finite among their values is taken
+// out of the products and given to the rows that do see it.
 //
 // Numbers.  Expanded codes are exact in fp16.  Q is brought to fp16 after a
 // power of two per row takes its largest element to [1, 2): bf16's 8 bits
@@ -727,7 +735,7 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
         {
             ProfScope ps("kv4_attn", st);
             const dfl_status rc = launch_pdl(kern, grid, groups * KA_THREADS, smem, st, a, err);
-            if (rc != DFL_OK) return rc;
+            if (rc != DFL_OK || (masked && ka_always_whole(a, grid * groups))) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
         return launch_pdl(join, dim3(grid * groups, rows / KJ_ROWS), pool.hd / 4 * KJ_ROWS, 0, st, a, err);

@@ -39,6 +39,16 @@ struct KaArgs {
     int window, sinks;        // window 0: none
 };
 
+// Whether ka_locate (MASK) takes whole triples whatever the lengths, so that there is nothing to join: the units of a
+// sequence through a window, `most`, are few enough.  (48 single tokens through a window of 128 11.0 us with the join's
+// launch, 9.8 without.)
+inline bool ka_always_whole(const KaArgs& a, int ranges) {
+    if (a.window == 0) return false;
+    const int64_t triples = (int64_t)a.N * a.HS, unit = (int64_t)1 << a.unit_log2;
+    const int64_t most = (a.sinks + unit - 1) / unit + (a.window + unit - 3) / unit + 1 + 1;   // sinks, window - 1 tokens anywhere, own rows
+    return triples <= ranges && triples * 4 > ranges && most + a.weight <= 1 + a.seam;
+}
+
 // The tensor-memory kernel (kv4_attn_tc.cu): rows of its triples, scratch, launch
 // (a complete but for Opart and ml; `units` an upper bound on the line).
 inline int kv4_attn_tc_rows(int R) { return R <= 64 ? 64 : 128; }

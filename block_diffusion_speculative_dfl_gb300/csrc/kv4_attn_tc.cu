@@ -23,8 +23,9 @@
 //
 // What bounds it: how fast one warp issues, about one instruction in 4.7 clocks
 // with four warps to a scheduler (dependent instructions, branches, fetches), so
-// control code counts: the expanders' full units have a path of their own (the
-// block of 16 above 57 us without).  Clocks of a pipeline per unit of 128 keys and
+// control code counts, and so does its size: warps of one SM that are in different
+// parts of more code than the instruction cache holds wait for it (the ragged cases
+// of kt_expander's turns).  Clocks of a pipeline per unit of 128 keys and
 // 64 rows:
 //   hd = 128  expanders 2 x 1,000 of expansion, 950 of copies ahead, 1,100 of
 //             waits and arrivals: 4,100, the longest turn; S 900 to its commit,
@@ -943,7 +944,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
 
 // See KaLine.  The seam, 0, 4, 8 and 16: the block of 16 above 59.8 us with 0 and
 // 49.2 with the others, 32 sequences of 900 52.9 and 32.8, 16 of 900 29.4, 29.5,
-// 26.7 and 26.7.  Weights of 1 and 3 give the same times.
+// 26.7 and 26.7.  Weights of 1 and 3 give the same times there.  Where lengths differ, a
+// triple's cost beside its units shows: 32 trees of 32 rows over 65 to 8,000 tokens take
+// 169, 143, 145, 135, 136 and 143 us with weights of 1, 3, 4, 6, 8 and 14 (masked).
 constexpr int KT_SEAM = 8;
 constexpr int KT_WEIGHT = 1;
 constexpr int KT_WEIGHT_MASKED = 6;
@@ -983,7 +986,7 @@ dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void
         {
             ProfScope ps("kv4_attn_tc", st);
             const dfl_status rc = launch_pdl(kern, grid, KT_THREADS, smem, st, a, err);
-            if (rc != DFL_OK) return rc;
+            if (rc != DFL_OK || (masked && ka_always_whole(a, KT_PIPES * grid))) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
         return launch_pdl(join, dim3(KT_PIPES * grid, mm / at_once), hd / 4 * at_once, 0, st, a, err);

@@ -20,6 +20,15 @@
 //
 // A row is cut among 1 to 8 CTAs of a cluster, which join their parts through
 // distributed shared memory in a fixed order: results repeat bit for bit.
+//
+// What bounds it: bytes, where rows are many: 4,097 rows of 201,087 in bf16 with 2
+// alternatives 282 us, 5.8 TB/s, 86 % of a copy's rate (265 without alternatives); 480
+// rows of 151,936 in fp32 with 8 52 us, 5.6 TB/s (48 without).  What is left of that is
+// a row's end, when its CTA reads nothing: the joins, 0.1 us a round of the maximum, one
+// more read.  One row of 151,936 in bf16 takes 4.9 us without alternatives, 8.3 with 8.
+// Short rows pay their end more often: 20,000 of 4,000 in bf16 34 us without, 56 with 8.
+// CTAs of 128 threads, eight to an SM, take 372 us for the first case with 8 (290), five
+// of 256 to an SM spill.
 #include "internal.h"
 #include "tree.h"
 
@@ -69,7 +78,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either 
 
 __device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 

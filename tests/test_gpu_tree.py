@@ -598,3 +598,90 @@ def test_a_draft_model_builds_trees_of_its_step():
     lp = dfl.token_logprobs(model.logits, top=5, T=0.9)
     check_tree(tree, [1, 2, 3], host(lp.top_ids).reshape(3, 7, 5), host(lp.top_logp).reshape(3, 7, 5))
     assert torch.equal(lp.top_ids[:, 0].view(3, 7), model.draft)
+
+
+# ------------------------------------------------- shapes of several paths --
+
+@pytest.mark.parametrize("rows,V,dtype,K", [(1, 151936, torch.bfloat16, 8), (3, 60001, torch.float32, 64), (100, 40000, torch.float32, 3),
+                                            (1300, 9000, torch.bfloat16, 32), (2000, 500, torch.float32, 33), (1217, 8192, torch.float32, 5)])
+def test_rows_by_warps_ctas_and_clusters_replay_from_a_graph(rows, V, dtype, K):
+    rng = np.random.default_rng(rows)
+    z, ids = logits_of(rng, rows, V, dtype, pad=3), some_ids(rng, rows, V, 2)
+    some = sorted({0, rows // 2, rows - 1})
+    check_logprobs(z, ids, K, 0.8, some)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = dfl.token_logprobs(z, ids, top=K, T=0.8)
+    z.copy_(z.flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    again = dfl.token_logprobs(z, ids, top=K, T=0.8)
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+@pytest.mark.parametrize("N,B,Hq,Hkv,hd,window,sinks", [(40, 1, 64, 8, 64, 128, 4), (40, 1, 64, 8, 64, 129, 64), (19, 2, 32, 8, 128, 64, 0),
+                                                        (30, 16, 32, 4, 128, 128, 3), (30, 16, 32, 4, 64, 500, 3), (20, 16, 16, 4, 128, 600, 0)])
+def test_windows_whose_triples_are_always_whole(N, B, Hq, Hkv, hd, window, sinks):
+    # nothing is joined: lengths from none to long ones
+    rng = np.random.default_rng(N + window)
+    lens = rng.permutation(np.r_[[0, 1, window - 1, window, window + 1], rng.integers(0, 3000, N - 5)])
+    c = make_cache(rng, N, lens, 64, Hkv, hd)
+    K, V = fill(rng, c, 0, lens)
+    Q, Kb, Vb = bf16(rng, (N, B, Hq, hd)), bf16(rng, (N, B, Hkv, hd)), bf16(rng, (N, B, Hkv, hd))
+    for kind in ("block", "tree"):
+        mask = own_masks(rng, kind, N, B)
+        out = torch.full_like(Q, 7.0)
+        c.attn(0, Q, Kb, Vb, out=out, mask=mask_tensor(mask), window=window, sinks=sinks)
+        check_attn(c, K, V, lens, Q, Kb, Vb, mask, window, sinks, out, np.argsort(lens)[::N // 9])
+
+
+@pytest.mark.parametrize("hd,Hq", [(128, 32), (64, 64), (128, 64)])
+def test_many_ragged_trees_cut_anywhere(hd, Hq):
+    rng = np.random.default_rng(hd + Hq)
+    N, B, Hkv = 90, 16, 8
+    lens = rng.integers(0, 700, N)
+    c = make_cache(rng, N, lens, 48, Hkv, hd)
+    K, V = fill(rng, c, 0, lens)
+    mask = own_masks(rng, "tree", N, B)
+    Q, Kb, Vb = bf16(rng, (N, B, Hq, hd)), bf16(rng, (N, B, Hkv, hd)), bf16(rng, (N, B, Hkv, hd))
+    O = c.attn(0, Q, Kb, Vb, mask=mask_tensor(mask))
+    check_attn(c, K, V, lens, Q, Kb, Vb, mask, 0, 0, O, [0, 1, 44, 71, 89])
+    assert torch.equal(O, c.attn(0, Q, Kb, Vb, mask=mask_tensor(mask)))
+
+
+def test_these_cases_pass_under_the_bounds_checked_build():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    from block_diffusion_speculative_dfl_gb300._build import build
+    build(checked=True)
+    r = subprocess.run([sys.executable, "-m", "pytest", __file__, "-m", "gpu", "-q", "-x", "-p", "no:cacheprovider", "-k",
+                        "(all_sizes and not 151936 and not 201087) or unusual or acceptance or chosen or unseen or serving or ragged"],
+                       cwd=root,
+                       env=dict(os.environ, DFL_CHECKED_BUILD="1"), capture_output=True, text=True, timeout=1800)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-2000:]
+    assert " passed" in r.stdout and " failed" not in r.stdout
+
+
+def test_calls_refuse_tensors_of_the_wrong_kind():
+    rng = np.random.default_rng(1)
+    c = make_cache(rng, 2, [5, 9], 16, 2, 64)
+    Q, Kb, Vb = bf16(rng, (2, 4, 4, 64)), bf16(rng, (2, 4, 2, 64)), bf16(rng, (2, 4, 2, 64))
+    m = torch.ones((2, 4), dtype=torch.int64, device="cuda")
+    for bad in (m.int(), m[:, :3], m.cpu(), m.t(), m[:1]):
+        with pytest.raises(ValueError):
+            c.attn(0, Q, Kb, Vb, mask=bad)
+    for kw in (dict(window=-1), dict(sinks=-1), dict(window=5, sinks=-2)):
+        with pytest.raises(dfl.DflError):
+            c.attn(0, Q, Kb, Vb, mask=m, **kw)
+    t = dfl.DraftTree(2, 4)
+    anchor, ids, lp = i32([1, 2]), torch.zeros((2, 3, 2), dtype=torch.int32, device="cuda"), torch.zeros((2, 3, 2), device="cuda")
+    t.build(anchor, ids, lp)
+    for bad in ((anchor[:1], ids, lp), (anchor.long(), ids, lp), (anchor, ids.long(), lp), (anchor, ids, lp.double()), (anchor, ids[:, :2], lp),
+                (anchor, ids[0], lp[0]), (anchor.cpu(), ids, lp), (anchor, ids[:, :0], lp[:, :0])):
+        with pytest.raises(ValueError):
+            t.build(*bad)
+    for bad in (i32(np.zeros((2, 3))), torch.zeros((2, 4), device="cuda"), i32(np.zeros((4, 2))).t()):
+        with pytest.raises(ValueError):
+            t.accept(bad)

@@ -199,3 +199,13 @@ def test_python_calls_refuse_tensors_of_the_wrong_kind():
         t.build(torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, 4, dtype=torch.int32), torch.zeros(2, 3, 4))
     with pytest.raises(ValueError):
         t.accept(torch.zeros(2, 5, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("name,kernels", [("logprobs.cu", 1), ("tree.cu", 2)])
+def test_the_bounds_checked_build_covers_every_kernel(name, kernels):
+    import os
+    from test_checked_build_sources import CSRC, functions
+    fs = functions(os.path.join(CSRC, name))
+    found = [n for n, body in fs.items() if "__global__" in body]
+    assert len(found) == kernels == open(os.path.join(CSRC, name)).read().count("__global__ void")
+    assert all("DFL_IN_BOUNDS" in fs[n] for n in found)
