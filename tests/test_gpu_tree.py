@@ -624,7 +624,7 @@ def test_rows_by_warps_ctas_and_clusters_replay_from_a_graph(rows, V, dtype, K):
 def test_windows_whose_triples_are_always_whole(N, B, Hq, Hkv, hd, window, sinks):
     # nothing is joined: lengths from none to long ones
     rng = np.random.default_rng(N + window)
-    lens = rng.permutation(np.r_[[0, 1, window - 1, window, window + 1], rng.integers(0, 3000, N - 5)])
+    lens = rng.permutation(np.r_[[0, 1, window - 1, window, window + 1], rng.integers(0, 1000, N - 5)])
     c = make_cache(rng, N, lens, 64, Hkv, hd)
     K, V = fill(rng, c, 0, lens)
     Q, Kb, Vb = bf16(rng, (N, B, Hq, hd)), bf16(rng, (N, B, Hkv, hd)), bf16(rng, (N, B, Hkv, hd))
