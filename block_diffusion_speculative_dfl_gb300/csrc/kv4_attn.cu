@@ -738,16 +738,25 @@ dfl_status kv4_attn_run(DeviceCtx* ctx, const dfl_kv4_pool& pool, int layer, con
             if (rc != DFL_OK || (masked && ka_always_whole(a, grid * groups))) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
+        if (masked) return launch_pdl(join, dim3(grid * groups), rows * KjmCfg<128, 8>::TPR, 0, st, a, err);
         return launch_pdl(join, dim3(grid * groups, rows / KJ_ROWS), pool.hd / 4 * KJ_ROWS, 0, st, a, err);
     };
     auto pick = [&](auto flag) -> dfl_status {
         constexpr bool MASK = decltype(flag)::value;
         constexpr int S = MASK ? 8 : 0;
+        auto join = [](auto hd, auto rows) {
+            if constexpr (MASK) return kv4_attn_join_masked_kernel<decltype(hd)::value, decltype(rows)::value>;
+            else return kv4_attn_join_kernel<decltype(hd)::value, decltype(rows)::value>;
+        };
+        using I = std::integral_constant<int, 128>;
+        using J = std::integral_constant<int, 64>;
+        using R8 = std::integral_constant<int, 8>;
+        using R16 = std::integral_constant<int, 16>;
         if (pool.hd == 128)
-            return nt == 1 ? run(kv4_attn_kernel<128, 1, MASK>, kv4_attn_join_kernel<128, 8, MASK>, KaCfg<128, 1>::SMEM, S)
-                           : run(kv4_attn_kernel<128, 2, MASK>, kv4_attn_join_kernel<128, 16, MASK>, KaCfg<128, 2>::SMEM, S + 1);
-        return nt == 1 ? run(kv4_attn_kernel<64, 1, MASK>, kv4_attn_join_kernel<64, 8, MASK>, KaCfg<64, 1>::SMEM, S + 2)
-                       : run(kv4_attn_kernel<64, 2, MASK>, kv4_attn_join_kernel<64, 16, MASK>, KaCfg<64, 2>::SMEM, S + 3);
+            return nt == 1 ? run(kv4_attn_kernel<128, 1, MASK>, join(I{}, R8{}), KaCfg<128, 1>::SMEM, S)
+                           : run(kv4_attn_kernel<128, 2, MASK>, join(I{}, R16{}), KaCfg<128, 2>::SMEM, S + 1);
+        return nt == 1 ? run(kv4_attn_kernel<64, 1, MASK>, join(J{}, R8{}), KaCfg<64, 1>::SMEM, S + 2)
+                       : run(kv4_attn_kernel<64, 2, MASK>, join(J{}, R16{}), KaCfg<64, 2>::SMEM, S + 3);
     };
     return masked ? pick(std::true_type{}) : pick(std::false_type{});
 }

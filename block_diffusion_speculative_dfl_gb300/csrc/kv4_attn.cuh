@@ -191,8 +191,8 @@ struct KaSees {
     int first;
 };
 __device__ __forceinline__ int ka_first(const KaArgs& a, int len, int depth) { return a.window > 0 ? len + depth - a.window + 1 : 0; }
-__device__ __forceinline__ KaSees ka_sees(const KaArgs& a, int n, int b, int len) {
-    KaSees s{ka_row_bits(a, n, b), 0};
+__device__ __forceinline__ KaSees ka_sees(const KaArgs& a, int n, int b, int len, uint64_t bits) {
+    KaSees s{bits, 0};
     const int d = ka_depth(a, s.own, b);
     s.first = ka_first(a, len, d);
     if (s.own == 0) s.first = KA_BLANK;
@@ -208,6 +208,8 @@ __device__ __forceinline__ KaSees ka_sees(const KaArgs& a, int n, int b, int len
     }
     return s;
 }
+__device__ __forceinline__ KaSees ka_sees(const KaArgs& a, int n, int b, int len) { return ka_sees(a, n, b, len, ka_row_bits(a, n, b)); }
+
 // Whether some row may not see one of the tokens k .. k + count - 1 (no row is deeper than B - 1).
 __device__ __forceinline__ bool ka_edge(const KaArgs& a, int len, int k, int count) {
     return a.window > 0 && k + count > a.sinks && k < len + a.B - a.window;
@@ -368,7 +370,7 @@ struct KjCfg {
     static constexpr int AT_ONCE = ROWS < 64 ? 8 : 16;   // rows of a block
     static constexpr int THREADS = HD / 4 * AT_ONCE;
 };
-template <int HD, int ROWS, bool MASK>
+template <int HD, int ROWS>
 __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel(const KaArgs a, const DevErr err) {
     constexpr int TPR = HD / 4;
     grid_dep_begin();
@@ -377,7 +379,6 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
     const int first = blockIdx.x, last = t.last, row0 = t.tile * ROWS;
     const int row = blockIdx.y * KjCfg<HD, ROWS>::AT_ONCE + threadIdx.x / TPR, c = (threadIdx.x % TPR) * 4, r = row0 + row;
     if (row >= ROWS || r >= a.R) return;
-    const bool blank = MASK && ka_sees(a, t.n, ka_block_row(a, r), ka_len(a, t.n)).first == KA_BLANK;
     // eight partials are read at once: a long triple waits for memory once per eight
     constexpr int BATCH = 8;
     float M = KA_NONE, L = 0.f;
@@ -402,17 +403,82 @@ __global__ void __launch_bounds__(KjCfg<HD, ROWS>::THREADS) kv4_attn_join_kernel
         #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const float f = j0 + i > last ? 0.f : ex2_ftz(ml[i].x - M);
-            if (MASK && j0 + i > last) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // (0 times an infinity that a row sees)
             L += f * ml[i].y;
             o.x += f * v[i].x; o.y += f * v[i].y; o.z += f * v[i].z; o.w += f * v[i].w;
         }
     }
-    float inv = __fdividef(a.v_pow2, L);
-    if (MASK && blank) { o = make_float4(0.f, 0.f, 0.f, 0.f); inv = 0.f; }
+    const float inv = __fdividef(a.v_pow2, L);
     const int64_t at = ka_row(a, t.n, t.head, r, HD) + c;
     if (DFL_IN_BOUNDS(err.word, at + 3, (int64_t)a.N * a.B * a.Hq * HD))
         *reinterpret_cast<uint2*>(a.O + at) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
+// The same for masked rows.  Eight threads to a row, each with all of its dims' pieces of 16 bytes, so that many rows are in
+// flight at once: a row is a chain of loads (the triple, its partials) that takes 2 to 3 us.  32 trees of 32 rows over 65 to
+// 8,000 tokens, 250 triples of two or three partials: 119.5 us in all, 128 with a thread per piece.  Four partials read at once
+// take 2 us more for one tree over 517 tokens, whose triples have six.
+template <int HD, int ROWS>
+struct KjmCfg {
+    static constexpr int TPR = 8, PIECES = HD / 4 / TPR, BATCH = HD == 128 ? 6 : 8;   // partials read at once
+    static constexpr int AT_ONCE = ROWS < 16 ? ROWS : 16, THREADS = AT_ONCE * TPR;
+};
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(KjmCfg<HD, ROWS>::THREADS) kv4_attn_join_masked_kernel(const KaArgs a, const DevErr err) {
+    using Cfg = KjmCfg<HD, ROWS>;
+    constexpr int PIECES = Cfg::PIECES, BATCH = Cfg::BATCH, STEP = 4 * Cfg::TPR;
+    grid_dep_begin();
+    const KaCross t = a.cross[blockIdx.x];
+    if (t.n < 0) return;
+    const int first = blockIdx.x, last = t.last;
+    const int row = blockIdx.y * Cfg::AT_ONCE + threadIdx.x / Cfg::TPR, c = threadIdx.x % Cfg::TPR * 4, r = t.tile * ROWS + row;
+    if (row >= ROWS || r >= a.R) return;
+    const int b = ka_block_row(a, r), len = ka_len(a, t.n);
+    const uint64_t bits = ka_row_bits(a, t.n, b);
+    float M = KA_NONE, L = 0.f;
+    float4 o[PIECES];
+    #pragma unroll
+    for (int p = 0; p < PIECES; ++p) o[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+    #pragma unroll 1
+    for (int j0 = first; j0 <= last; j0 += BATCH) {
+        float2 ml[BATCH];
+        float4 v[BATCH][PIECES];
+        float mn = M;
+        #pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int j = j0 + i;
+            const bool there = j <= last;   // (0 in place of what is none: 0 times an infinity that a row sees would be NaN)
+            const int64_t at = (int64_t)(2 * j + (j == first)) * ROWS + row;
+            ml[i] = there ? a.ml[at] : make_float2(KA_NONE, 0.f);
+            #pragma unroll
+            for (int p = 0; p < PIECES; ++p)
+                v[i][p] = there ? *reinterpret_cast<const float4*>(a.Opart + at * HD + c + p * STEP) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        #pragma unroll
+        for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, ml[i].x);
+        const float old = ex2_ftz(M - mn);
+        M = mn;
+        L *= old;
+        #pragma unroll
+        for (int p = 0; p < PIECES; ++p) { o[p].x *= old; o[p].y *= old; o[p].z *= old; o[p].w *= old; }
+        #pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const float f = ex2_ftz(ml[i].x - M);
+            L += f * ml[i].y;
+            #pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                o[p].x += f * v[i][p].x; o[p].y += f * v[i][p].y; o[p].z += f * v[i][p].z; o[p].w += f * v[i][p].w;
+            }
+        }
+    }
+    const float inv = __fdividef(a.v_pow2, L);
+    const bool blank = ka_sees(a, t.n, b, len, bits).first == KA_BLANK;
+    const int64_t at = ka_row(a, t.n, t.head, r, HD) + c;
+    #pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+        if (DFL_IN_BOUNDS(err.word, at + p * STEP + 3, (int64_t)a.N * a.B * a.Hq * HD))
+            *reinterpret_cast<uint2*>(a.O + at + p * STEP) =
+                blank ? make_uint2(0, 0) : make_uint2(pack_bf16(o[p].x * inv, o[p].y * inv), pack_bf16(o[p].z * inv, o[p].w * inv));
 }
 
 }  // namespace

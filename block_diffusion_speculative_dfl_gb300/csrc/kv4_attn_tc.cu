@@ -989,19 +989,25 @@ dfl_status kv4_attn_tc_run(DeviceCtx* ctx, KaArgs a, int hd, int64_t units, void
             if (rc != DFL_OK || (masked && ka_always_whole(a, KT_PIPES * grid))) return rc;
         }
         ProfScope ps("kv4_attn_join", st);
+        using Kjm = KjmCfg<128, 64>;
+        if (masked) return launch_pdl(join, dim3(KT_PIPES * grid, mm / Kjm::AT_ONCE), Kjm::THREADS, 0, st, a, err);
         return launch_pdl(join, dim3(KT_PIPES * grid, mm / at_once), hd / 4 * at_once, 0, st, a, err);
     };
     auto pick = [&](auto flag) -> dfl_status {
         constexpr bool M = decltype(flag)::value;
         constexpr int S = M ? 12 : 4;
+        auto join = [](auto hd, auto rows) {
+            if constexpr (M) return kv4_attn_join_masked_kernel<decltype(hd)::value, decltype(rows)::value>;
+            else return kv4_attn_join_kernel<decltype(hd)::value, decltype(rows)::value>;
+        };
         if (hd == 128)
-            return mm == 64 ? run(kv4_attn_tc_kernel<128, 64, M>, kv4_attn_join_kernel<128, 64, M>, KtCfg<128, 64>::SMEM, S,
+            return mm == 64 ? run(kv4_attn_tc_kernel<128, 64, M>, join(std::integral_constant<int, 128>{}, std::integral_constant<int, 64>{}), KtCfg<128, 64>::SMEM, S,
                                   KjCfg<128, 64>::AT_ONCE)
-                            : run(kv4_attn_tc_kernel<128, 128, M>, kv4_attn_join_kernel<128, 128, M>, KtCfg<128, 128>::SMEM, S + 1,
+                            : run(kv4_attn_tc_kernel<128, 128, M>, join(std::integral_constant<int, 128>{}, std::integral_constant<int, 128>{}), KtCfg<128, 128>::SMEM, S + 1,
                                   KjCfg<128, 128>::AT_ONCE);
-        return mm == 64 ? run(kv4_attn_tc_kernel<64, 64, M>, kv4_attn_join_kernel<64, 64, M>, KtCfg<64, 64>::SMEM, S + 2,
+        return mm == 64 ? run(kv4_attn_tc_kernel<64, 64, M>, join(std::integral_constant<int, 64>{}, std::integral_constant<int, 64>{}), KtCfg<64, 64>::SMEM, S + 2,
                               KjCfg<64, 64>::AT_ONCE)
-                        : run(kv4_attn_tc_kernel<64, 128, M>, kv4_attn_join_kernel<64, 128, M>, KtCfg<64, 128>::SMEM, S + 3,
+                        : run(kv4_attn_tc_kernel<64, 128, M>, join(std::integral_constant<int, 64>{}, std::integral_constant<int, 128>{}), KtCfg<64, 128>::SMEM, S + 3,
                               KjCfg<64, 128>::AT_ONCE);
     };
     return masked ? pick(std::true_type{}) : pick(std::false_type{});
