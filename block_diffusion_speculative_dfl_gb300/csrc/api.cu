@@ -211,7 +211,7 @@ using namespace dfl;
 
 // ------------------------------------------------------------------ misc
 
-extern "C" const char* dfl_version(void) { return "dfl 0.2.0 (sm_103a)"; }
+extern "C" const char* dfl_version(void) { return "dfl 0.3.0 (sm_103a)"; }
 
 extern "C" const char* dfl_status_string(dfl_status s) {
     switch (s) {

@@ -470,9 +470,6 @@ __device__ __forceinline__ void kt_load_q(const KaArgs& a, int n, int head, int 
     }
 }
 
-// Softmax side: M = 128 gives a thread one row (its tensor-memory lane); at
-// M = 64 the 16 rows of a warp's quadrant are shared by its two half-warps,
-// each with half of a row's columns.
 // Tokens k0 .. k1 - 1 (at most 64) with a NaN among their values, as bits from k0 on.  A converged warp.
 template <int HD>
 __device__ __noinline__ uint64_t kt_edge_nans(const KaArgs& a, const DevErr& err, int n, int head, int k0, int k1, int lane) {
@@ -513,9 +510,9 @@ __device__ __noinline__ void kt_mend(const KaArgs& a, const DevErr& err, int n, 
             const uint8_t* cell = a.slab.data + (int64_t)ka_cell(a, n, head, k & ~(KV4_CELL_TOKENS - 1), err) * Cell::BYTES;
             if ((cell[Cell::v_scale(k & (KV4_CELL_TOKENS - 1), (c + j) / 16)] & 0x7F) == 0x7F) x = __int_as_float(0x7FFFFFFF);
         }
-        if (x == 0.f) continue;
-        if (out) out[j] = __float2bfloat16(x);
-        else part[j] = x;
+        if (x == 0.f) continue;   // (a NaN there stays one)
+        if (out) out[j] = __float2bfloat16(__bfloat162float(out[j]) + x);
+        else part[j] += x;
     }
 }
 
@@ -541,6 +538,9 @@ __device__ __noinline__ void kt_hide(uint32_t s_at, uint64_t see0, uint64_t see1
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint64_t kt_ones(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
+// Softmax side: M = 128 gives a thread one row (its tensor-memory lane); at
+// M = 64 the 16 rows of a warp's quadrant are shared by its two half-warps,
+// each with half of a row's columns.
 template <int HD, int MM, bool MASK>
 __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs a, const DevErr err) {
     using Cfg = KtCfg<HD, MM>;

@@ -64,8 +64,8 @@ def token_logprobs(logits, ids=None, top=0, T=1.0, entropy=True, stream=None) ->
     logits bf16 or fp32 [..., V] (the last dim contiguous, the leading dims one behind the other at any stride, the
     data 16-byte aligned); ids int32 [..., M], contiguous, with the same leading dims: logp fp32 [..., M], -inf for a
     token outside 0 .. V-1.  entropy fp32 [...]; top_ids int32, top_logp fp32 [..., top], largest first, ties to the
-    lowest id, -1 and -inf where a row has fewer tokens above -inf.  The outputs are allocated on the stream of the
-    call.
+    lowest id, -1 and -inf where a row has fewer tokens above -inf.  A row that is no distribution (all -inf, a NaN,
+    +inf) has NaN.  The outputs are allocated on the stream of the call and carry no gradients.
     """
     index = logits.get_device()
     if index < 0 or index != torch.cuda.current_device():
@@ -133,7 +133,9 @@ class DraftTree:
     def build(self, anchor, top_ids, top_logp, stream=None):
         """The most probable tree of the alternatives of G positions behind the anchor.
 
-        anchor int32 [N]; top_ids int32, top_logp fp32 [N, G, K], best first, as ``token_logprobs`` gives them.
+        anchor int32 [N]; top_ids int32, top_logp fp32 [N, G, K], best first, as ``token_logprobs`` gives them.  A row's
+        score is its parent's plus its logp (in units of 2^-44; at most 1,024 in magnitude each); the best scores become
+        rows, ties at the lowest parent, and nothing behind an alternative whose logp is not finite.
         """
         _index(self.token, "the tree")
         G, K = top_ids.shape[1:] if top_ids.dim() == 3 else (0, 0)

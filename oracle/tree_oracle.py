@@ -34,7 +34,7 @@ def draft_tree(anchor, ids, logp, B):
 
     def offer(p, k):
         g = depth[p]
-        if g < G and k < K and logp[g][k] > -np.inf:
+        if g < G and k < K and np.isfinite(logp[g][k]):
             heapq.heappush(heap, (-(score[p] + float(logp[g][k])), p, k))
 
     offer(0, 0)

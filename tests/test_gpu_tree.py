@@ -162,6 +162,15 @@ def test_leading_dims_strides_and_optional_outputs():
         dfl.token_logprobs(flat[1:])  # not on a 16-byte boundary
 
 
+def test_rows_past_2_31_elements():
+    rng = np.random.default_rng(3)
+    V, stride = 1000, (1 << 31) + 8
+    buf = torch.zeros(2 * stride, dtype=torch.bfloat16, device="cuda")
+    z = buf.view(2, stride)[:, :V]
+    z.copy_(torch.from_numpy(rng.standard_normal((2, V)).astype(np.float32)))
+    check_logprobs(z, some_ids(rng, 2, V, 2), 5, 1.0)
+
+
 def test_logprobs_write_their_rows_only_and_repeat():
     rng = np.random.default_rng(2)
     rows, V, M, K = 37, 5003, 3, 6
@@ -216,7 +225,7 @@ def test_trees_of_all_sizes(N, G, K, B, kind):
 
 def test_alternatives_that_are_none_end_a_trees_branches():
     rng = np.random.default_rng(4)
-    N, G, K, B = 6, 6, 4, 40
+    N, G, K, B = 8, 6, 4, 40
     lp = -np.sort(rng.exponential(1.0, (N, G, K)), -1).astype(np.float32)
     ids = rng.integers(0, 1000, (N, G, K)).astype(np.int32)
     lp[0, :, 2:] = -INF
@@ -225,9 +234,18 @@ def test_alternatives_that_are_none_end_a_trees_branches():
     lp[3, 1, 1] = np.nan
     lp[4, 0, 0] = np.nan
     lp[5] = -1e38            # sums past fp32
+    lp[6, 2] = INF
+    lp[7] = 0.25             # a little above 0, as rounding leaves them
     tree = dfl.DraftTree(N, B).build(i32(np.arange(N)), i32(ids), torch.from_numpy(lp).cuda())
     check_tree(tree, np.arange(N), ids, lp)
     assert host(tree.count)[[2, 4]].tolist() == [1, 1]
+
+
+def test_alternatives_far_out_count_as_1024():
+    lp = np.array([[[-1.0, -1500.0, -3000.0]], [[-1.0, -1500.0, -3000.0]]], np.float32).repeat(2, 1)
+    lp[0, 1], ids = [-0.5, -900.0, -1100.0], np.arange(12).reshape(2, 2, 3)
+    tree = dfl.DraftTree(2, 13).build(i32([0, 0]), i32(ids), torch.from_numpy(lp).cuda())
+    check_tree(tree, [0, 0], ids, np.maximum(lp, -1024.0))
 
 
 def random_tree(rng, B, count):
@@ -379,18 +397,19 @@ def test_rows_that_see_everything_see_what_unmasked_ones_do(B, Hq, Hkv, hd):
 
 
 @pytest.mark.parametrize("B,Hq,Hkv,hd", HEADS)
-def test_unseen_own_rows_touch_nothing(B, Hq, Hkv, hd):
+@pytest.mark.parametrize("lens", [[90, 0, 700], [90, 0, 150] * 54])   # triples cut and joined; whole ones
+def test_unseen_own_rows_touch_nothing(B, Hq, Hkv, hd, lens):
     # infinities and NaN in rows that are none, and in branches that a row does not see
     rng = np.random.default_rng(hd + B)
-    lens = [90, 0, 700]
-    c = make_cache(rng, 3, lens, 32, Hkv, hd)
+    N = len(lens)
+    c = make_cache(rng, N, lens, 32, Hkv, hd)
     K, V = fill(rng, c, 0, lens)
-    mask = [to.tree_mask(random_tree(rng, B, max(1, B - 2 * n))) for n in range(3)]
-    Q, Kb, Vb = bf16(rng, (3, B, Hq, hd)), bf16(rng, (3, B, Hkv, hd)), bf16(rng, (3, B, Hkv, hd))
+    mask = [to.tree_mask(random_tree(rng, B, max(1, B - 2 * (n % 3)))) for n in range(N)]
+    Q, Kb, Vb = bf16(rng, (N, B, Hq, hd)), bf16(rng, (N, B, Hkv, hd)), bf16(rng, (N, B, Hkv, hd))
     m = mask_tensor(mask)
     clean = c.attn(0, Q, Kb, Vb, mask=m)
-    check_attn(c, K, V, lens, Q, Kb, Vb, mask, 0, 0, clean)
-    for n in range(3):
+    check_attn(c, K, V, lens, Q, Kb, Vb, mask, 0, 0, clean, [0, 1, 2])
+    for n in range(N):
         for b in range(B):
             if mask[n][b] == 0:   # no row: whatever was in memory
                 Q[n, b], Kb[n, b], Vb[n, b] = float("nan"), float("nan"), float("nan")
@@ -421,14 +440,15 @@ def test_unseen_own_rows_touch_nothing(B, Hq, Hkv, hd):
 
 @pytest.mark.parametrize("B,Hq,Hkv,hd", HEADS)
 @pytest.mark.parametrize("window,sinks", [(70, 5), (200, 0), (33, 40)])
-def test_cached_tokens_outside_a_rows_window_touch_nothing(B, Hq, Hkv, hd, window, sinks):
+@pytest.mark.parametrize("lens", [[600, 333], [600, 333] * 80])   # triples cut and joined; whole ones
+def test_cached_tokens_outside_a_rows_window_touch_nothing(B, Hq, Hkv, hd, window, sinks, lens):
     rng = np.random.default_rng(hd + B)
-    lens = [600, 333]
-    c = make_cache(rng, 2, lens, 32, Hkv, hd)
-    Kc, Vc = (bf16(rng, (2, 600, Hkv, hd)) for _ in range(2))
-    zero = i32([0, 0])
-    Q, Kb, Vb = bf16(rng, (2, B, Hq, hd)), bf16(rng, (2, B, Hkv, hd)), bf16(rng, (2, B, Hkv, hd))
-    mask = [to.tree_mask([-1] + list(range(B - 1)))] * 2    # one path: every depth
+    N = len(lens)
+    c = make_cache(rng, N, lens, 32, Hkv, hd)
+    Kc, Vc = (bf16(rng, (N, 600, Hkv, hd)) for _ in range(2))
+    zero = i32(np.zeros(N))
+    Q, Kb, Vb = bf16(rng, (N, B, Hq, hd)), bf16(rng, (N, B, Hkv, hd)), bf16(rng, (N, B, Hkv, hd))
+    mask = [to.tree_mask([-1] + list(range(B - 1)))] * N    # one path: every depth
     m = mask_tensor(mask)
     c.append(0, Kc, Vc, zero, i32(lens))
     clean = host(c.attn(0, Q, Kb, Vb, mask=m, window=window, sinks=sinks))
@@ -441,7 +461,7 @@ def test_cached_tokens_outside_a_rows_window_touch_nothing(B, Hq, Hkv, hd, windo
     at = [l - window + 1 + deep for l in lens]              # seen by the rows of that depth and less
     want = clean.copy()
     G = Hq // Hkv
-    for n in range(2):
+    for n in range(N):
         bad[n, at[n], 0, hd - 16] = float("nan")            # its group of 16 dims reads back as NaN
         for b in range(B):
             if b <= deep:

@@ -48,9 +48,10 @@ def test_a_tree_holds_the_most_probable_prefixes():
     # equal scores: the lowest parent first, then the better rank
     t, p, d = to.draft_tree(0, [[1, 2], [3, 4]], np.zeros((2, 2)), 7)
     assert p == [-1, 0, 0, 1, 1, 2, 2] and t == [0, 1, 2, 3, 4, 3, 4]
-    # nothing behind -inf or NaN
+    # nothing behind infinities or NaN
     assert to.draft_tree(0, [[1, 2]], [[-1.0, -np.inf]], 9)[0] == [0, 1]
     assert to.draft_tree(0, [[1, 2]], [[np.nan, -1.0]], 9)[0] == [0]
+    assert to.draft_tree(0, [[1, 2]], [[np.inf, -1.0]], 9)[0] == [0]
 
 
 def test_what_rows_see():
