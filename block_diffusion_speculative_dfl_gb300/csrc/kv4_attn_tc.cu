@@ -71,8 +71,9 @@ struct KtCfg {
     static constexpr int SLOT = KU / 4 / KV4_CELL_TOKENS * CELL / PARTS;
     static constexpr int PIPE = Q + 2 * ST * TILE + RST * 4 * SLOT;
     static constexpr int S_COL = 0, O_COL = 128, COLS = 256;
+    static constexpr bool TWO_S = KU == 64;             // S of the next unit beside that of this one
     static constexpr int SMEM = 1024 + KT_PIPES * PIPE;
-    static_assert(KU <= O_COL && O_COL + HD <= COLS, "tensor memory columns");
+    static_assert((TWO_S ? 2 : 1) * KU <= O_COL && O_COL + HD <= COLS, "tensor memory columns");
     static_assert(SMEM <= 225 * 1024, "shared memory");
     static_assert(PIPE % 1024 == 0, "tiles start on 1024-byte boundaries");
 };
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
         constexpr int RPW = HALF ? 16 : 32;          // rows per warp
         const int q4 = warp & 3, hh = HALF ? lane >> 4 : 0;
         const int row = RPW * q4 + (HALF ? lane & 15 : lane);   // row of the triple held by this thread
-        const uint32_t my = tmem + ((uint32_t)(q4 * 32) << 16), s_at = my + Cfg::S_COL;
+        const uint32_t my = tmem + ((uint32_t)(q4 * 32) << 16);
         uint32_t unit = 0, triple = 0;
         bool ok = true, issued = false;
         // ---- products, by the first warp: one elected lane issues them (operands
@@ -627,7 +628,9 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
         // descriptors of slot 0; slots and K blocks are added to the address field (16-byte units)
         const uint64_t qd = sw128_desc(smem_u32(sQ)), kd = sw128_desc(smem_u32(sK));
         const uint64_t vd = sw128_desc_mn(smem_u32(sV), Cfg::TKB, 1024);
-        auto issue_s = [&](bool first) {   // S of the next unit; S's columns are free
+        constexpr bool TWO_S = Cfg::TWO_S;
+        auto s_col = [&](uint32_t i) { return Cfg::S_COL + (TWO_S ? (i & 1) * KU : 0); };   // of a pipeline's unit i
+        auto issue_s = [&](bool first, uint32_t i) {   // S of unit i; its columns are free
             const bool ready = kt_wait(&bb.t_full[0][ks.i], ks.ph, err, abort) &&
                                (!first || kt_wait(&bb.q_full, triple & 1, err, abort));
             if (!__all_sync(0xFFFFFFFFu, ready)) return false;
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             if (elect_one()) {
                 #pragma unroll
                 for (int j = 0; j < HD / 16; ++j)
-                    mma_bf16(tmem + Cfg::S_COL, qd + (j >> 2) * (Cfg::QKB >> 4) + (j & 3) * 2,
+                    mma_bf16(tmem + s_col(i), qd + (j >> 2) * (Cfg::QKB >> 4) + (j & 3) * 2,
                              kdi + (j >> 2) * (Cfg::TKB >> 4) + (j & 3) * 2, kt_idesc_f16(MM, KU), j > 0);
                 mma_commit(&bb.s_full);
                 mma_commit(&bb.t_empty[0][ks.i]);
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             if (elect_one()) {
                 #pragma unroll
                 for (int j = 0; j < KU / 16; ++j)   // V is MN-major
-                    mma_bf16_ts(tmem + Cfg::O_COL, tmem + Cfg::S_COL + 8 * j, vdi + j * (16 * 128 >> 4),
+                    mma_bf16_ts(tmem + Cfg::O_COL, tmem + s_col(unit) + 8 * j, vdi + j * (16 * 128 >> 4),
                                 kt_idesc_f16(MM, HD) | (1u << 16), j > 0 || !first);
                 mma_commit(&bb.pv_done);
                 mma_commit(&bb.t_empty[1][vs.i]);
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
             fence_proxy_async_smem();
             __syncwarp();
             if (elect_one()) mbar_arrive(&bb.q_full);
-            if (issuer && !issue_s(true)) { ok = false; break; }
+            if (issuer && !issue_s(true, unit)) { ok = false; break; }
             const float mult = ka_mult(a, q_up[pipe][row]);
             uint64_t nans = 0;   // tokens from nan0 on that some row does not see, with NaN among their values
             const int nan0 = MASK && a.window > 0 ? max(max(ka_first(a, pos.len, 0), a.sinks), 0) : 0;
@@ -704,6 +707,7 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                 ok = kt_wait(&bb.s_full, unit & 1, err, abort);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
+                const uint32_t s_at = my + s_col(unit);
                 if (!pad) {
                     // The maximum first: O is rescaled only where it grows by more than 2^8
                     // (S of this unit was issued after the P V of the units before had ended).
@@ -852,9 +856,14 @@ __global__ void __launch_bounds__(KT_THREADS, 1) kv4_attn_tc_kernel(const KaArgs
                 if (elect_one()) mbar_arrive(&bb.p_full);
                 if (issuer) {
                     ok = issue_pv(u == u0);
+                    // Products run in the order of their issue, so with columns of its own S may follow P V at once; its end
+                    // is P V's end too.
                     if (ok && u + 1 < u1) {
-                        ok = kt_wait(&bb.pv_done, unit & 1, err, abort);
-                        ok = __all_sync(0xFFFFFFFFu, ok) && issue_s(false);
+                        if constexpr (!TWO_S) {
+                            ok = kt_wait(&bb.pv_done, unit & 1, err, abort);
+                            ok = __all_sync(0xFFFFFFFFu, ok);
+                        }
+                        ok = ok && issue_s(false, unit + 1);
                     }
                     if (!ok) break;
                 }
