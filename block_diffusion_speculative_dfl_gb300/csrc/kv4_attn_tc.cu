@@ -378,8 +378,8 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
         const bool edge = MASK && !own && ka_edge(a, pos.len, k0 + share, SHARE);
         const bool mend = left < SHARE || edge;
         // The K tile's turn, then the V tile's.  Once each, whatever the unit is: the instruction cache holds one expansion of
-        // each kind and little more (with a loop of its own for units that are not whole, 200 sequences of 10 to 600 tokens took
-        // 214 us, a third of it waiting for instructions).
+        // each kind and little more (with a loop of its own for units that are not whole, 200 trees over 10 to 600 tokens took
+        // 214 us, a third of it waiting for instructions; 146 now).
         auto turn = [&](auto which) {
             constexpr int half = decltype(which)::value;
             if (PARTS == 2 || half == 0)
@@ -390,7 +390,7 @@ __device__ __forceinline__ void kt_expander(const KaArgs& a, const DevErr& err, 
             const uint32_t t = tiles + (half * ST + ts.i) * tile_bytes + share * 128;
             const uint32_t src = smem_u32(ring) + r.i * NC * PART + (PARTS == 1 ? half * HALF : 0);
             if (cell) {
-                #pragma unroll
+                #pragma unroll 1   // (unrolled, ragged batches of short sequences take 5 to 12 % longer, whole ones 1 % less)
                 for (int j = 0; j < NC; ++j) {
                     const int kj = k0 + share + j * KV4_CELL_TOKENS;
                     if constexpr (half)
