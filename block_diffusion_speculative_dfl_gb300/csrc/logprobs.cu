@@ -5,9 +5,11 @@
 // One pass over the row for all three sums: a thread's reference M is the maximum
 // of its first elements, moved only when a later one passes it by more than 2^8,
 // so that the loop is loads, one product and sum, one exponential and two sums an
-// element.  y is never rounded (it is an operand of a fused product and sum), so any
-// reference serves that is near the maximum; rows whose maximum is past 2^20 in y take
-// differences of logits first, in a second pass.
+// element, all but the exponential two elements at a time, bf16's maximum too (4,097 rows
+// of 201,087 281 us one at a time, 269 so; 480 of 151,936 with 8 41.3 and 36.0).  y is
+// never rounded (it is an operand of a fused product and sum), so any reference serves
+// that is near the maximum; rows whose maximum is past 2^20 in y take differences of
+// logits first, in a second pass.
 //
 // Alternatives cost the pass one maximum an element: each group of vectors (a
 // thread's) has its largest logit and where it was met first.  Order all elements by
@@ -22,13 +24,13 @@
 // distributed shared memory in a fixed order: results repeat bit for bit.
 //
 // What bounds it: bytes, where rows are many: 4,097 rows of 201,087 in bf16 with 2
-// alternatives 282 us, 5.8 TB/s, 86 % of a copy's rate (265 without alternatives); 480
-// rows of 151,936 in fp32 with 8 52 us, 5.6 TB/s (48 without).  What is left of that is
+// alternatives 269 us, 6.1 TB/s, 90 % of a copy's rate (261 without alternatives); 480
+// rows of 151,936 in fp32 with 8 51 us, 5.7 TB/s (48 without).  What is left of that is
 // a row's end, when its CTA reads nothing: the joins, 0.1 us a round of the maximum, one
 // more read.  One row of 151,936 in bf16 takes 4.9 us without alternatives, 8.3 with 8.
-// Short rows pay their end more often: 20,000 of 4,000 in bf16 34 us without, 56 with 8.
-// CTAs of 128 threads, eight to an SM, take 372 us for the first case with 8 (290), five
-// of 256 to an SM spill.
+// Short rows pay their end more often: 20,000 of 4,000 in bf16 32 us without, 52 with 8.
+// (Before the pairs) CTAs of 128 threads, eight to an SM, took 372 us for the first case
+// with 8, 290 so; five of 256 to an SM spill.
 #include "internal.h"
 #include "tree.h"
 
@@ -44,19 +46,54 @@ constexpr int LP_UNROLL = 4;       // 16-byte loads in flight per thread
 constexpr int LP_MAX_CLUSTER = 8;
 constexpr float LP_LAZY = 8.f;     // a thread's reference moves when passed by more (log2)
 constexpr float LP_FAR = 1048576.f;  // references stay within: rounded by 2^-5 at most, which a sum takes
-constexpr float LP_TINY = -1000.f; // exponents stay above: 2^-1000 is 0 and 0 * -1000 is 0, where 0 * -inf is NaN
+// Logits count as this at least (-2^100; a NaN stays one): its weight is 0, and 0 times its exponent 0, where 0 * -inf is NaN.
+constexpr uint32_t LP_LEAST = 0xF1800000u, LP_LEAST_X2 = 0xF180F180u;
+constexpr float LP_TINY = -1000.f; // (rows whose differences are taken first) the same of exponents
 constexpr float LN2 = 0.69314718055994531f;
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {       // the number of a number and a NaN
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {   // the NaN
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// 16 bytes of logits: N of them, NONE of them all -inf.
 template <typename T>
 struct LpVec;
 template <>
 struct LpVec<float> {
     static constexpr int N = 4;
-    static constexpr uint32_t NONE = 0xFF800000u;     // -inf
+    static constexpr uint32_t NONE = 0xFF800000u;
     static __device__ __forceinline__ void get(const uint4& r, float (&z)[4]) {
         z[0] = __uint_as_float(r.x); z[1] = __uint_as_float(r.y); z[2] = __uint_as_float(r.z); z[3] = __uint_as_float(r.w);
     }
+    // their maximum (NaNs passed over), and in pairs, as LP_LEAST at least
+    static __device__ __forceinline__ float pairs(const uint4& r, float2 (&z)[2]) {
+        float x[4];
+        get(r, x);
+        #pragma unroll
+        for (int i = 0; i < 2; ++i)
+            z[i] = make_float2(max_nan(x[2 * i], __uint_as_float(LP_LEAST)), max_nan(x[2 * i + 1], __uint_as_float(LP_LEAST)));
+        return max3(fmaxf(x[0], x[1]), x[2], x[3]);
+    }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
+    static __device__ __forceinline__ uint4 some(const float* p, int from, int to) {   // elements from .. to - 1 of p[0 .. N - 1]
+        uint32_t w[4];
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = e >= from && e < to ? __float_as_uint(p[e]) : NONE;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
 template <>
 struct LpVec<__nv_bfloat16> {
@@ -67,14 +104,29 @@ struct LpVec<__nv_bfloat16> {
         #pragma unroll
         for (int i = 0; i < 4; ++i) { z[2 * i] = bf16lo(w[i]); z[2 * i + 1] = bf16hi(w[i]); }
     }
+    static __device__ __forceinline__ float pairs(const uint4& r, float2 (&z)[4]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = max_nan_bf16x2(w[i], LP_LEAST_X2);
+            z[i] = make_float2(bf16lo(x), bf16hi(x));
+        }
+        const uint32_t m = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+        return fmaxf(bf16lo(m), bf16hi(m));
+    }
     static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+    static __device__ __forceinline__ uint4 some(const __nv_bfloat16* p, int from, int to) {
+        uint32_t w[4];
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = 2 * e >= from && 2 * e < to ? q[2 * e] : NONE & 0xFFFFu;
+            const uint32_t hi = 2 * e + 1 >= from && 2 * e + 1 < to ? q[2 * e + 1] : NONE & 0xFFFFu;
+            w[e] = lo | hi << 16;
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
 };
-
-__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
 
 __device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
     uint4 v;
@@ -200,38 +252,44 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     const int nv = (head + a.V + EPV - 1) / EPV, whole0 = head > 0, whole1 = (head + a.V) / EPV;
     const int per = NW == 1 ? nv : (nv + C - 1) / C, v0 = min(nv, rank * per), v1 = min(nv, v0 + per);
     // elements of vector v that belong to the row, the others as -inf
-    auto load = [&](int v, float (&z)[EPV]) {
-        if (v >= whole0 && v < whole1) { Vec::get(vec[v], z); return; }
-        #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            const int i = v * EPV - head + e;
-            z[e] = i >= 0 && i < a.V ? Vec::one(z0 + i) : -INFINITY;
-        }
+    auto load_raw = [&](int v) {
+        if (v >= whole0 && v < whole1) return vec[v];
+        const int first = v * EPV - head;
+        return Vec::some(z0 + first, -first, a.V - first);
     };
+    auto load = [&](int v, float (&z)[EPV]) { Vec::get(load_raw(v), z); };
 
-    LpSums t{-LP_FAR, 0.f, 0.f};
+    // this thread's sums, in two halves
+    float m = -LP_FAR;
+    float2 s2 = make_float2(0.f, 0.f), w2 = s2;
     constexpr int PT = Team::PER_THREAD;
     float best_z[PT], next_z[PT];
     uint32_t best_at[PT];
     #pragma unroll
     for (int i = 0; i < PT; ++i) { best_z[i] = next_z[i] = -INFINITY; best_at[i] = 0xFFFFFFFFu; }
-    auto add = [&](const float (&z)[EPV], int v, int i) {
-        float m4[2] = {z[0], z[1]};
-        #pragma unroll
-        for (int e = 2; e < EPV; e += 2) { m4[0] = fmaxf(m4[0], z[e]); m4[1] = fmaxf(m4[1], z[e + 1]); }
-        const float mx = fmaxf(m4[0], m4[1]);
+    auto add = [&](const uint4& raw, int v, int i) {
+        float2 z[EPV / 2];
+        const float mx = Vec::pairs(raw, z);
         if (TOP) {
             if (mx > best_z[i] || (mx == best_z[i] && (uint32_t)v < best_at[i])) best_at[i] = (uint32_t)v;
             next_z[i] = fmaxf(next_z[i], fminf(best_z[i], mx));
         }
         best_z[i] = fmaxf(best_z[i], mx);
         const float ref = mx * a.c;
-        if (ref > t.m + LP_LAZY) t.move(ref);
+        if (ref > m + LP_LAZY) {
+            LpSums x{m, s2.x, w2.x}, y{m, s2.y, w2.y};
+            x.move(ref);
+            y.move(ref);
+            m = ref;
+            s2 = make_float2(x.s, y.s);
+            w2 = make_float2(x.w, y.w);
+        }
+        const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-m, -m);
         #pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            const float d = max_nan(fmaf(z[e], a.c, -t.m), LP_TINY), p = ex2_ftz(d);
-            t.s += p;
-            t.w = fmaf(p, d, t.w);
+        for (int e = 0; e < EPV / 2; ++e) {
+            const float2 d = fma_f32x2(z[e], c2, m2), p = make_float2(ex2_ftz(d.x), ex2_ftz(d.y));
+            s2 = add_f32x2(s2, p);
+            w2 = fma_f32x2(p, d, w2);
         }
     };
     const int lo = max(v0, whole0), hi = min(v1, whole1);
@@ -246,9 +304,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
         }
         #pragma unroll
         for (int u = 0; u < LP_UNROLL; ++u) {
-            float z[EPV];
-            Vec::get(raw[u], z);
-            add(z, v + u * THREADS, u % PT);
+            add(raw[u], v + u * THREADS, u % PT);
         }
     }
     // the row's ends, where they share a vector with something else
@@ -256,13 +312,13 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LpA
     for (int end = 0; end < 2; ++end) {
         const int v = end ? nv - 1 : 0;
         if (v >= v0 && v < v1 && (end ? v >= whole1 && v >= whole0 : v < whole0) && (v - v0) % THREADS == tid) {
-            float z[EPV];
-            load(v, z);
+            const uint4 raw = load_raw(v);
             #pragma unroll
             for (int i = 0; i < PT; ++i)
-                if (i == (v - v0) / THREADS % PT) add(z, v, i);
+                if (i == (v - v0) / THREADS % PT) add(raw, v, i);
         }
     }
+    LpSums t{m, s2.x + s2.y, w2.x + w2.y};
     float zmax = best_z[0];
     #pragma unroll
     for (int i = 1; i < PT; ++i) zmax = fmaxf(zmax, best_z[i]);
