@@ -10,7 +10,6 @@ captured into CUDA graphs.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -37,8 +36,12 @@ def _index(x, what):
     return index
 
 
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _handle(index, stream):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _lib._stream(stream)
+    return _raw_stream(index) if stream is None else _lib._stream(stream)
 
 
 def _row_stride(logits, rows):
@@ -56,6 +59,13 @@ def _row_stride(logits, rows):
     if (V > 1 and logits.stride(-1) != 1) or (rows > 1 and stride < V):
         raise ValueError("a row of logits must be contiguous and the rows apart")
     return stride
+
+
+def _outputs(dev, lead, M, entropy, top):
+    empty, f32 = torch.empty, torch.float32
+    return TokenLogprobs(None if M is None else empty((*lead, M), dtype=f32, device=dev),
+                         empty(lead, dtype=f32, device=dev) if entropy else None,
+                         empty((*lead, top), dtype=torch.int32, device=dev), empty((*lead, top), dtype=f32, device=dev))
 
 
 def token_logprobs(logits, ids=None, top=0, T=1.0, entropy=True, stream=None) -> TokenLogprobs:
@@ -87,20 +97,21 @@ def token_logprobs(logits, ids=None, top=0, T=1.0, entropy=True, stream=None) ->
         M = ids.shape[-1]
     if not 0 <= top <= 64:
         raise ValueError(f"top={top} outside 0..64")
-    with contextlib.nullcontext() if stream is None else on_stream(index, stream):
-        dev, f32 = logits.device, torch.float32
-        logp = torch.empty((*lead, M), dtype=f32, device=dev) if ids is not None else None
-        H = torch.empty(lead, dtype=f32, device=dev) if entropy else None
-        top_ids = torch.empty((*lead, top), dtype=torch.int32, device=dev)
-        top_logp = torch.empty((*lead, top), dtype=f32, device=dev)
+    if stream is None:   # (no context manager on the host's way)
+        out = _outputs(logits.device, lead, M if ids is not None else None, entropy, top)
+        handle = _raw_stream(index)
+    else:
+        with on_stream(index, stream):
+            out = _outputs(logits.device, lead, M if ids is not None else None, entropy, top)
+        handle = _lib._stream(stream)
     if rows and (M or top or entropy):
+        logp, H, top_ids, top_logp = out
         rc = _lib.load().dfl_token_logprobs(logits.data_ptr(), dt, rows, V, stride, T, ids.data_ptr() if M else None, M,
                                             logp.data_ptr() if M else None, H.data_ptr() if entropy else None, top,
-                                            top_ids.data_ptr() if top else None, top_logp.data_ptr() if top else None,
-                                            _handle(index, stream))
+                                            top_ids.data_ptr() if top else None, top_logp.data_ptr() if top else None, handle)
         if rc:
             _lib._check("dfl_token_logprobs", rc)
-    return TokenLogprobs(logp, H, top_ids, top_logp)
+    return out
 
 
 class DraftTree:
