@@ -2,9 +2,9 @@
 // on the 5th-generation tensor cores.  The same sum and the same line of work
 // units as kv4_attn.cu, with up to 128 rows to a triple, where products and
 // exponentials, not bytes, are most of the work.  A block of 16 at 4 query heads
-// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 51 us, 338 TFLOP/s
-// of products and 1.7 TB/s of cache; 64 rows of a head of 64 over 33,333 to
-// 100,001 tokens: 71.7 us; 128 rows: 74 and 106 us.
+// a K/V head (32 sequences of 2,048 tokens, 8 heads of 128): 49 us, 350 TFLOP/s
+// of products and 1.8 TB/s of cache; 64 rows of a head of 64 over 33,333 to
+// 100,001 tokens: 71.8 us; 128 rows: 70.5 and 104 us.
 //
 // One CTA per SM, two pipelines of eight warps, each with a range of the line of
 // its own, so that one pipeline's products run under the other's exponentials:
